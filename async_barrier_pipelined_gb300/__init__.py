@@ -1,9 +1,11 @@
-"""Python binding of the gemm_f16 C ABI (include/gemm_f16.h).
+"""Python binding of the gemm_f16 / attn_f16 C ABI (include/*.h).
 
-Argument marshalling only: every step of the product runs in the CUDA
-kernels of ``csrc/gemm_f16.cu``.  The functions keep the C names; raw
-pointers are Python ints.  ``matmul`` is a convenience that takes torch
-tensors (PyTorch is used only for device memory and streams).
+Argument marshalling only: every step of an operation runs in the CUDA
+kernels of ``csrc/``.  The functions keep the C names; raw pointers are
+Python ints.  ``matmul``, ``attention`` and the calls of a serving step over
+a paged cache (``paged_maps``, ``rotary``, ``rotary_to_cache``,
+``paged_attention``) are conveniences that take torch tensors (PyTorch is
+used only for device memory and streams).
 
 The library is built in-tree by ``async_barrier_pipelined_gb300.build.build()``
 (``__graft_entry__.build()`` calls it).  If it is missing, loading fails
@@ -11,7 +13,9 @@ loudly; there is no fallback implementation.
 """
 from __future__ import annotations
 
+import collections
 import ctypes
+import math
 import os
 import threading
 
@@ -30,6 +34,10 @@ __all__ = [
     "attn_f16_key_ranges", "gemm_f16_run_info", "gemm_f16_run_choice", "attn_f16_fwd_host", "attention_host",
     "attention", "ATTN_HEAD_DIM", "gemm_f16_kernel_time",
     "LAYOUT_NN", "LAYOUT_TN", "LAYOUT_NT", "LAYOUT_TT",
+    "ERR_BAD_INDEX", "attn_f16_paged_maps", "attn_f16_paged_maps_validate", "attn_f16_rope",
+    "attn_f16_rope_validate", "attn_f16_rope_turns", "attn_f16_paged_fwd",
+    "attn_f16_paged_validate", "ROPE_HALF", "ROPE_INTERLEAVED", "PagedMaps", "paged_maps",
+    "rope_frequencies", "rope_turns", "rotary", "rotary_to_cache", "paged_attention",
 ]
 
 OK = 0
@@ -40,6 +48,7 @@ ERR_OOM = -4
 ERR_CUDA = -5
 ERR_TIMEOUT = -6
 ERR_SCRATCH_TOO_SMALL = -7
+ERR_BAD_INDEX = -8
 
 OPT_TIMEOUT_NS = 1
 OPT_TILE_ORDER = 2
@@ -62,9 +71,20 @@ LAYOUT_TN = 1   # A stored K x M
 LAYOUT_NT = 2   # B stored N x K
 LAYOUT_TT = 3
 
+ROPE_HALF = 0
+ROPE_INTERLEAVED = 1
+
 _c_int, _c_i64, _vp = ctypes.c_int, ctypes.c_int64, ctypes.c_void_p
 
-#: name -> (restype, argtypes) for every entry point of include/gemm_f16.h
+_i64p = ctypes.POINTER(_c_i64)
+_MAPS_ARGS = [_c_int, _vp, _vp, _vp, _c_i64, _c_int, _vp, _c_int, _vp, _c_int, _c_int,
+              _vp, _vp, _vp, _vp, _vp]
+_ROPE_TAIL = [_vp, _vp, _vp, _i64p, _vp, _i64p, _vp, _i64p, _vp, _i64p, _vp, _vp, _i64p, _vp,
+              _i64p, _c_int, _c_int]
+_PAGED_ARGS = [_c_int] * 6 + [_vp, _i64p, _vp, _i64p, _vp, _i64p, _c_int, _c_int, _vp, _c_i64,
+                              _c_int, _vp, _vp, _vp, _i64p, ctypes.c_float, _c_int, _c_int]
+
+#: name -> (restype, argtypes) for every entry point of include/*.h
 _SIGNATURES = {
     "gemm_f16_plan": (_c_int, [ctypes.POINTER(_vp), _c_int]),
     "gemm_f16_run": (_c_int, [_vp, _c_int, _c_int, _c_int, _vp, _c_i64, _vp, _c_i64,
@@ -108,6 +128,14 @@ _SIGNATURES = {
                                      _c_int, _c_int, ctypes.POINTER(_c_int)]),
     "attn_f16_fwd_host": (_c_int, [_vp, _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _vp, _vp,
                                    _vp, ctypes.c_float, _vp]),
+    "attn_f16_paged_maps": (_c_int, [_vp, *_MAPS_ARGS, _vp]),
+    "attn_f16_paged_maps_validate": (_c_int, _MAPS_ARGS),
+    "attn_f16_rope": (_c_int, [_vp] + [_c_int] * 7 + [ctypes.c_float, *_ROPE_TAIL, _vp]),
+    "attn_f16_rope_validate": (_c_int, [_c_int] * 6 + [ctypes.c_float, *_ROPE_TAIL]),
+    "attn_f16_rope_turns": (_c_int, [ctypes.POINTER(ctypes.c_double), _c_int,
+                                     ctypes.POINTER(ctypes.c_uint64)]),
+    "attn_f16_paged_fwd": (_c_int, [_vp, *_PAGED_ARGS, _vp]),
+    "attn_f16_paged_validate": (_c_int, _PAGED_ARGS),
     "gemm_f16_kernel_time": (_c_int, [_vp, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_c_i64)]),
 }
 EXPORTED_SYMBOLS = tuple(_SIGNATURES)
@@ -172,7 +200,8 @@ def gemm_f16_destroy(plan: int) -> None:
 
 
 def gemm_f16_status(plan: int) -> int:
-    """Device-reported status since the last call (0 or ERR_TIMEOUT); clears it."""
+    """Device-reported status since the last call (0, ERR_TIMEOUT or
+    ERR_BAD_INDEX); clears it."""
     return load().gemm_f16_status(plan)
 
 
@@ -464,3 +493,335 @@ def attention_host(plan: Plan, hQ, hK, hV, hO, scale=None, stream=None):
     attn_f16_fwd_host(plan.handle, B, H, Sq, Skv, D, hQ.data_ptr(), hK.data_ptr(), hV.data_ptr(),
                       hO.data_ptr(), scale, _stream_handle(stream))
     return hO
+
+
+# ---------------------------------------------------------------- paged cache
+def attn_f16_paged_maps(plan: int, batch: int, cached: int, added: int, block_table: int,
+                        table_stride: int, max_pages: int, free_pages: int, num_free: int,
+                        free_head: int, page_size: int, max_tokens: int, starts: int,
+                        kv_lens: int, positions: int, slots: int, free_head_out: int,
+                        stream: int = 0) -> None:
+    """Enqueue the maps of a serving step (device pointers; see attn_f16.h)."""
+    _check(load().attn_f16_paged_maps(plan, batch, cached, added, block_table, table_stride,
+                                      max_pages, free_pages, num_free, free_head, page_size,
+                                      max_tokens, starts, kv_lens, positions, slots,
+                                      free_head_out, stream), "attn_f16_paged_maps")
+
+
+def attn_f16_paged_maps_validate(*args) -> int:
+    """The argument check of attn_f16_paged_maps (its arguments without plan and stream)."""
+    return load().attn_f16_paged_maps_validate(*args)
+
+
+def _i64s(values):
+    return None if values is None else (_c_i64 * len(values))(*[int(x) for x in values])
+
+
+def attn_f16_rope(plan: int, tokens: int, q_heads: int, kv_heads: int, head_dim: int,
+                  rot_dim: int, layout: int, inverse: int, factor: float, turns: int,
+                  positions: int, Q: int, q_strides, Qo: int, qo_strides, K: int = 0,
+                  k_strides=None, V: int = 0, v_strides=None, slots: int = 0, Kc: int = 0,
+                  kc_strides=None, Vc: int = 0, vc_strides=None, num_pages: int = 0,
+                  page_size: int = 0, stream: int = 0) -> None:
+    """Enqueue rotary positions, with the write of K and V into a paged cache
+    when kv_heads > 0 (device pointers; see attn_f16.h)."""
+    _check(load().attn_f16_rope(plan, tokens, q_heads, kv_heads, head_dim, rot_dim, layout,
+                                inverse, factor, turns, positions, Q, _i64s(q_strides), Qo,
+                                _i64s(qo_strides), K, _i64s(k_strides), V, _i64s(v_strides),
+                                slots, Kc, _i64s(kc_strides), Vc, _i64s(vc_strides), num_pages,
+                                page_size, stream), "attn_f16_rope")
+
+
+def attn_f16_rope_validate(tokens, q_heads, kv_heads, head_dim, rot_dim, layout, factor, turns,
+                           positions, Q, q_strides, Qo, qo_strides, K=0, k_strides=None, V=0,
+                           v_strides=None, slots=0, Kc=0, kc_strides=None, Vc=0,
+                           vc_strides=None, num_pages=0, page_size=0) -> int:
+    return load().attn_f16_rope_validate(
+        tokens, q_heads, kv_heads, head_dim, rot_dim, layout, factor, turns, positions, Q,
+        _i64s(q_strides), Qo, _i64s(qo_strides), K, _i64s(k_strides), V, _i64s(v_strides), slots,
+        Kc, _i64s(kc_strides), Vc, _i64s(vc_strides), num_pages, page_size)
+
+
+def attn_f16_rope_turns(radians) -> list:
+    """Frequencies in radians per position -> fixed-point turns (2^64 a turn)."""
+    n = len(radians)
+    out = (ctypes.c_uint64 * max(n, 1))()
+    _check(load().attn_f16_rope_turns((ctypes.c_double * max(n, 1))(*radians), n, out),
+           "attn_f16_rope_turns")
+    return list(out[:n])
+
+
+def attn_f16_paged_fwd(plan: int, batch: int, total_q: int, max_q: int, q_heads: int,
+                       kv_heads: int, head_dim: int, Q: int, q_strides, Kc: int, kc_strides,
+                       Vc: int, vc_strides, num_pages: int, page_size: int, block_table: int,
+                       table_stride: int, max_pages: int, starts: int, kv_lens: int, O: int,
+                       o_strides, scale: float, window: int = 0, sinks: int = 0,
+                       stream: int = 0) -> None:
+    """Enqueue attention over a paged cache (device pointers; see attn_f16.h)."""
+    _check(load().attn_f16_paged_fwd(plan, batch, total_q, max_q, q_heads, kv_heads, head_dim, Q,
+                                     _i64s(q_strides), Kc, _i64s(kc_strides), Vc,
+                                     _i64s(vc_strides), num_pages, page_size, block_table,
+                                     table_stride, max_pages, starts, kv_lens, O,
+                                     _i64s(o_strides), scale, window, sinks, stream),
+           "attn_f16_paged_fwd")
+
+
+def attn_f16_paged_validate(batch, total_q, max_q, q_heads, kv_heads, head_dim, Q, q_strides, Kc,
+                            kc_strides, Vc, vc_strides, num_pages, page_size, block_table,
+                            table_stride, max_pages, starts, kv_lens, O, o_strides, scale,
+                            window=0, sinks=0) -> int:
+    return load().attn_f16_paged_validate(
+        batch, total_q, max_q, q_heads, kv_heads, head_dim, Q, _i64s(q_strides), Kc,
+        _i64s(kc_strides), Vc, _i64s(vc_strides), num_pages, page_size, block_table,
+        table_stride, max_pages, starts, kv_lens, O, _i64s(o_strides), scale, window, sinks)
+
+
+def _need(X, name: str, dtype, dims: int, plan: Plan):
+    """A torch tensor of this type and rank on the plan's device, its last
+    dimension contiguous."""
+    if X.dtype != dtype or X.dim() != dims:
+        raise ValueError(f"{name} must be a {dims}-dimensional {dtype} tensor")
+    if not X.is_cuda or X.device.index != plan.device:
+        raise ValueError(f"{name} must be on the plan's device")
+    if X.stride(-1) != 1 and X.shape[-1] > 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+
+
+PagedMaps = collections.namedtuple("PagedMaps", "starts kv_lens positions slots free_head")
+PagedMaps.__doc__ = """The maps of one serving step (see paged_maps)."""
+
+
+def paged_maps(plan: Plan, cached, added, block_table, free_pages, free_head, page_size: int,
+               max_tokens: int, out=None, stream=None) -> PagedMaps:
+    """Block tables and slot maps of a serving step, built on the GPU from
+    the requests' lengths.
+
+    cached, added: int32 [batch], the tokens of each request that the cache
+    holds already and the step's new ones.  block_table: int32 [batch,
+    max_pages]; the pages that the new tokens need are taken from free_pages
+    (int32 [n]) at free_head (int32 [1]) and written into it.  Returns
+    starts [batch + 1], kv_lens [batch], positions and slots [max_tokens]
+    (0 and -1 past the last token) and the new free_head [1], written into
+    ``out`` (a PagedMaps of an earlier call) if given.
+    """
+    import torch
+    i32 = torch.int32
+    for name, X, dims in (("cached", cached, 1), ("added", added, 1),
+                          ("block_table", block_table, 2), ("free_pages", free_pages, 1),
+                          ("free_head", free_head, 1)):
+        _need(X, name, i32, dims, plan)
+    batch = cached.shape[0]
+    if added.shape[0] != batch or block_table.shape[0] != batch or free_head.shape[0] != 1:
+        raise ValueError("shape mismatch: cached [B], added [B], block_table [B, P], free_head [1]")
+    if out is None:
+        room = (max(max_tokens, 0) + 3) // 4 * 4
+        buf = torch.empty(2 * room + 2 * batch + 2, dtype=i32, device=cached.device)
+        positions, slots, starts, kv_lens, head = buf.split_with_sizes(
+            (room, room, batch + 1, batch, 1))
+        if room != max_tokens:
+            positions, slots = positions[:max(max_tokens, 0)], slots[:max(max_tokens, 0)]
+        out = PagedMaps(starts, kv_lens, positions, slots, head)
+    else:
+        for name, X, n in (("starts", out.starts, batch + 1), ("kv_lens", out.kv_lens, batch),
+                           ("positions", out.positions, max_tokens),
+                           ("slots", out.slots, max_tokens), ("free_head", out.free_head, 1)):
+            _need(X, "out." + name, i32, 1, plan)
+            if X.shape[0] != n:
+                raise ValueError(f"out.{name} must have {n} entries")
+    attn_f16_paged_maps(plan.handle, batch, cached.data_ptr(), added.data_ptr(),
+                        block_table.data_ptr(),
+                        block_table.stride(0) if batch > 1 else block_table.shape[1],
+                        block_table.shape[1], free_pages.data_ptr(), free_pages.shape[0],
+                        free_head.data_ptr(), page_size, max_tokens, out.starts.data_ptr(),
+                        out.kv_lens.data_ptr(), out.positions.data_ptr(), out.slots.data_ptr(),
+                        out.free_head.data_ptr(), _stream_handle(stream))
+    return out
+
+
+def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none",
+                     factor: float = 1.0, original_len: int = 0, slow_turns: float = 1.0,
+                     fast_turns: float = 32.0):
+    """Frequencies (radians per position, one per pair) of rotary positions.
+
+    scaling "none": base^(-2i/rot_dim).  "linear": divided by ``factor``
+    (positions squeezed into the trained range).  "base": the base is raised
+    to base * factor^(rot_dim/(rot_dim-2)), so that the slowest pair is
+    slowed by ``factor`` and the fastest not at all.  "parts": pairs that make
+    at least ``fast_turns`` turns over the trained ``original_len`` positions
+    keep their frequency, those with at most ``slow_turns`` are slowed by
+    ``factor``, with a ramp linear in the turns between; the values are then
+    usually multiplied by 0.1 ln(factor) + 1 (the ``factor`` argument of
+    rotary).
+    """
+    if rot_dim < 2 or rot_dim % 2 or not base > 1.0 or not factor > 0.0:
+        raise ValueError("rot_dim must be even, base above 1 and factor above 0")
+    if scaling == "base":
+        if rot_dim < 4:
+            raise ValueError("base scaling needs at least two pairs")
+        base = base * factor ** (rot_dim / (rot_dim - 2.0))
+    f = [base ** (-2.0 * i / rot_dim) for i in range(rot_dim // 2)]
+    if scaling in ("none", "base"):
+        return f
+    if scaling == "linear":
+        return [w / factor for w in f]
+    if scaling == "parts":
+        if original_len < 1 or not fast_turns > slow_turns:
+            raise ValueError("parts scaling needs original_len and fast_turns > slow_turns")
+        out = []
+        for w in f:
+            keep = (original_len * w / (2.0 * math.pi) - slow_turns) / (fast_turns - slow_turns)
+            keep = min(1.0, max(0.0, keep))
+            out.append(w * keep + w / factor * (1.0 - keep))
+        return out
+    raise ValueError("scaling is 'none', 'linear', 'base' or 'parts'")
+
+
+def rope_turns(frequencies):
+    """Frequencies (radians per position, a list or a CPU tensor) as the int64
+    tensor of fixed-point turns that rotary takes (2^64 a turn, as bits)."""
+    import torch
+    if isinstance(frequencies, torch.Tensor):
+        frequencies = frequencies.tolist()
+    bits = attn_f16_rope_turns([float(w) for w in frequencies])
+    return torch.tensor([b - (1 << 64) if b >> 63 else b for b in bits], dtype=torch.int64)
+
+
+def _rope_layout(layout: str) -> int:
+    if layout == "half":
+        return ROPE_HALF
+    if layout == "interleaved":
+        return ROPE_INTERLEAVED
+    raise ValueError("layout is 'half' or 'interleaved'")
+
+
+def _token_heads(X, name: str, plan: Plan, tokens=None):
+    import torch
+    _need(X, name, torch.float16, 3, plan)
+    if X.shape[2] != ATTN_HEAD_DIM or (tokens is not None and X.shape[0] != tokens):
+        raise ValueError(f"{name} must be [tokens, heads, {ATTN_HEAD_DIM}]")
+
+
+def _cache_pair(K_cache, V_cache, plan: Plan):
+    import torch
+    _need(K_cache, "K_cache", torch.float16, 4, plan)
+    _need(V_cache, "V_cache", torch.float16, 4, plan)
+    if K_cache.shape != V_cache.shape or K_cache.shape[3] != ATTN_HEAD_DIM:
+        raise ValueError(f"K_cache and V_cache must be [pages, page_size, kv_heads, "
+                         f"{ATTN_HEAD_DIM}]")
+
+
+def _rope_common(positions, turns, tokens, plan):
+    import torch
+    _need(positions, "positions", torch.int32, 1, plan)
+    _need(turns, "turns", torch.int64, 1, plan)
+    if positions.shape[0] != tokens:
+        raise ValueError("positions must have one entry per token")
+
+
+def rotary(plan: Plan, X, positions, turns, out=None, layout: str = "half", factor: float = 1.0,
+           inverse: bool = False, stream=None):
+    """Rotary positions of X, float16 [tokens, heads, 256] (tokens and heads
+    may be strided): the first 2 * len(turns) numbers of each head are rotated
+    by the token's position (int32 [tokens]), in pairs (i, i + half) or, with
+    layout "interleaved", (2i, 2i + 1), and multiplied by ``factor``; the rest
+    is copied.  turns: int64, from rope_turns, on the device.  ``inverse``
+    rotates back: given the gradient of the output it returns the gradient
+    of X.  ``out`` may be X.
+    """
+    import torch
+    _token_heads(X, "X", plan)
+    _rope_common(positions, turns, X.shape[0], plan)
+    if out is None:
+        out = torch.empty(X.shape, dtype=X.dtype, device=X.device)
+    else:
+        _token_heads(out, "out", plan)
+        if out.shape != X.shape:
+            raise ValueError("out must have the shape of X")
+    attn_f16_rope(plan.handle, X.shape[0], X.shape[1], 0, X.shape[2], 2 * turns.shape[0],
+                  _rope_layout(layout), int(inverse), factor, turns.data_ptr(),
+                  positions.data_ptr(), X.data_ptr(), X.stride()[:2], out.data_ptr(),
+                  out.stride()[:2], stream=_stream_handle(stream))
+    return out
+
+
+def rotary_to_cache(plan: Plan, Q, K, V, positions, slots, turns, K_cache, V_cache, out=None,
+                    layout: str = "half", factor: float = 1.0, stream=None):
+    """Rotary positions of a step's new queries and keys, with the rotated
+    keys and the values written into their slots of a paged cache.
+
+    Q: float16 [tokens, q_heads, 256]; K, V: [tokens, kv_heads, 256] (all may
+    be strided, e.g. views of one projection's output).  K_cache, V_cache:
+    [pages, page_size, kv_heads, 256], any strides with the last dimension
+    contiguous.  positions, slots: int32 [tokens], from paged_maps (slot -1:
+    nothing is written).  Returns the rotated Q (in ``out``, which may be Q).
+    """
+    import torch
+    _token_heads(Q, "Q", plan)
+    tokens = Q.shape[0]
+    _token_heads(K, "K", plan, tokens)
+    _token_heads(V, "V", plan, tokens)
+    _cache_pair(K_cache, V_cache, plan)
+    if K.shape != V.shape or K.shape[1] != K_cache.shape[2]:
+        raise ValueError("K, V and the caches must have the same heads")
+    _rope_common(positions, turns, tokens, plan)
+    _need(slots, "slots", torch.int32, 1, plan)
+    if slots.shape[0] != tokens:
+        raise ValueError("slots must have one entry per token")
+    if out is None:
+        out = torch.empty(Q.shape, dtype=Q.dtype, device=Q.device)
+    else:
+        _token_heads(out, "out", plan)
+        if out.shape != Q.shape:
+            raise ValueError("out must have the shape of Q")
+    attn_f16_rope(plan.handle, tokens, Q.shape[1], K.shape[1], Q.shape[2], 2 * turns.shape[0],
+                  _rope_layout(layout), 0, factor, turns.data_ptr(), positions.data_ptr(),
+                  Q.data_ptr(), Q.stride()[:2], out.data_ptr(), out.stride()[:2], K.data_ptr(),
+                  K.stride()[:2], V.data_ptr(), V.stride()[:2], slots.data_ptr(),
+                  K_cache.data_ptr(), K_cache.stride()[:3], V_cache.data_ptr(),
+                  V_cache.stride()[:3], K_cache.shape[0], K_cache.shape[1],
+                  _stream_handle(stream))
+    return out
+
+
+def paged_attention(plan: Plan, Q, K_cache, V_cache, block_table, starts, kv_lens, max_q: int,
+                    out=None, scale=None, window: int = 0, sinks: int = 0, stream=None):
+    """Causal attention of a step's new tokens over their requests' pages.
+
+    Q: float16 [tokens, q_heads, 256], the new tokens of all requests one
+    after another (request b's from starts[b] to starts[b + 1] - 1), the last
+    of them at position kv_lens[b] - 1.  K_cache, V_cache: [pages, page_size,
+    kv_heads, 256] (page_size a multiple of 8), holding the new tokens' keys
+    and values too; query head h reads key/value head h * kv_heads // q_heads.
+    block_table: int32 [batch, max_pages]; starts [batch + 1], kv_lens
+    [batch]: int32.  max_q: the most new tokens a request has (a larger number
+    is fine).  A token at position p sees the keys at j <= p; with ``window``
+    only j > p - window and the first ``sinks`` of its request.  ``scale``
+    defaults to 1/sqrt(256).  Rows that see no key, and rows past the last
+    request's, are 0.
+    """
+    import torch
+    _token_heads(Q, "Q", plan)
+    _cache_pair(K_cache, V_cache, plan)
+    _need(block_table, "block_table", torch.int32, 2, plan)
+    _need(starts, "starts", torch.int32, 1, plan)
+    _need(kv_lens, "kv_lens", torch.int32, 1, plan)
+    batch = kv_lens.shape[0]
+    if starts.shape[0] != batch + 1 or block_table.shape[0] != batch:
+        raise ValueError("shape mismatch: block_table [B, P], starts [B + 1], kv_lens [B]")
+    if out is None:
+        out = torch.empty(Q.shape, dtype=Q.dtype, device=Q.device)
+    else:
+        _token_heads(out, "out", plan)
+        if out.shape != Q.shape:
+            raise ValueError("out must have the shape of Q")
+    if scale is None:
+        scale = 1.0 / math.sqrt(ATTN_HEAD_DIM)
+    attn_f16_paged_fwd(plan.handle, batch, Q.shape[0], max_q, Q.shape[1], K_cache.shape[2],
+                       Q.shape[2], Q.data_ptr(), Q.stride()[:2], K_cache.data_ptr(),
+                       K_cache.stride()[:3], V_cache.data_ptr(), V_cache.stride()[:3],
+                       K_cache.shape[0], K_cache.shape[1], block_table.data_ptr(),
+                       block_table.stride(0) if batch > 1 else block_table.shape[1],
+                       block_table.shape[1], starts.data_ptr(), kv_lens.data_ptr(),
+                       out.data_ptr(), out.stride()[:2], scale, window, sinks,
+                       _stream_handle(stream))
+    return out

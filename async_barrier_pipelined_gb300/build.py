@@ -1,9 +1,9 @@
 """Build the gemm_f16 shared library in-tree with nvcc for sm_103a.
 
 Output: async_barrier_pipelined_gb300/_lib/libgemm_f16.so (git-ignored).
-Three translation units (plan and shared host code, the GEMM kernels and
-entry points, the attention kernels and entry points) are compiled in
-parallel with one -gencode each and linked into one library, so a build
+Five translation units (plan and shared host code; the kernels and entry
+points of the GEMM, the attention, the paged-cache maps with rotary
+positions, and the attention over a paged cache) are compiled in parallel with one -gencode each and linked into one library, so a build
 takes seconds on either the x86 build host or the aarch64 GPU host.
 """
 from __future__ import annotations
@@ -19,7 +19,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(PKG_DIR, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libgemm_f16.so")
 
-SOURCES = [os.path.join(CSRC, f) for f in ("plan.cu", "gemm_f16.cu", "attn_f16.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("plan.cu", "gemm_f16.cu", "attn_f16.cu",
+                                             "paged_f16.cu", "paged_attn.cu")]
 HEADERS = [os.path.join(CSRC, f) for f in ("host.h", "ptx.cuh", "schedule.h", "common.cuh",
                                             "gemm_pair.cuh", "gemm_quad.cuh", "attn_f16.cuh",
                                             "attn_pair.cuh")]

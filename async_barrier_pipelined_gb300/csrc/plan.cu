@@ -191,6 +191,7 @@ const char* gemm_f16_strerror(int code) {
     case GEMM_F16_ERR_CUDA: return "CUDA call failed";
     case GEMM_F16_ERR_TIMEOUT: return "an in-kernel barrier wait timed out";
     case GEMM_F16_ERR_SCRATCH_TOO_SMALL: return "problem too large for the fixed no-alloc scratch";
+    case GEMM_F16_ERR_BAD_INDEX: return "a length, page or slot read on the device is out of range";
     default: return "unknown error code";
   }
 }

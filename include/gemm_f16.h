@@ -58,7 +58,9 @@ typedef enum gemm_f16_error {
     GEMM_F16_ERR_OOM = -4,                /* device or pinned-host allocation failed */
     GEMM_F16_ERR_CUDA = -5,               /* a CUDA runtime/driver call failed (see gemm_f16_last_cuda_error) */
     GEMM_F16_ERR_TIMEOUT = -6,            /* a bounded in-kernel wait expired (reported by gemm_f16_status) */
-    GEMM_F16_ERR_SCRATCH_TOO_SMALL = -7   /* gemm_f16_run_noalloc: problem exceeds its fixed scratch */
+    GEMM_F16_ERR_SCRATCH_TOO_SMALL = -7,  /* gemm_f16_run_noalloc: problem exceeds its fixed scratch */
+    GEMM_F16_ERR_BAD_INDEX = -8           /* a length, page or slot read on the device is out of range (attn_f16.h's
+                                             paged calls; reported by gemm_f16_status) */
 } gemm_f16_error;
 
 /* Options for gemm_f16_set_option. */
@@ -281,7 +283,8 @@ int gemm_f16_destroy(gemm_f16_plan_t plan);
 
 /*
  * Device-reported status of the runs completed so far, then cleared:
- * GEMM_F16_OK or GEMM_F16_ERR_TIMEOUT.  Synchronises nothing: call it after
+ * GEMM_F16_OK, GEMM_F16_ERR_TIMEOUT, or GEMM_F16_ERR_BAD_INDEX (paged calls
+ * of attn_f16.h; of several reports the last one stays).  Synchronises nothing: call it after
  * synchronising the stream of the runs it should cover.
  */
 int gemm_f16_status(gemm_f16_plan_t plan);
