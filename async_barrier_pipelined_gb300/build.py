@@ -23,7 +23,8 @@ SOURCES = [os.path.join(CSRC, f) for f in ("plan.cu", "gemm_f16.cu", "attn_f16.c
                                              "paged_f16.cu", "paged_attn.cu")]
 HEADERS = [os.path.join(CSRC, f) for f in ("host.h", "ptx.cuh", "schedule.h", "common.cuh",
                                             "gemm_pair.cuh", "gemm_quad.cuh", "attn_f16.cuh",
-                                            "attn_pair.cuh")]
+                                            "attn_pair.cuh", "paged_schedule.h",
+                                            "paged_small.cuh")]
 DEPENDS = SOURCES + HEADERS + [os.path.join(INCLUDE, "gemm_f16.h"),
                                os.path.join(INCLUDE, "attn_f16.h")]
 

@@ -2,9 +2,9 @@
 // object behind gemm_f16_plan_t, CUDA error bookkeeping, tensor-map
 // encoding (with the plan's cache) and stream-ordered buffer growth.
 //
-// plan.cu defines these; gemm_f16.cu (GEMM kernels and entry points) and
-// attn_f16.cu (attention kernels and entry points) use them.  Each of the
-// two adds its own part of plan creation and destruction through the
+// plan.cu defines these; gemm_f16.cu (GEMM kernels and entry points),
+// attn_f16.cu (attention kernels and entry points) and paged_attn.cu
+// (attention over a paged cache) use them.  Each of the three adds its own part of plan creation and destruction through the
 // *_plan_init / *_plan_release hooks below.
 #pragma once
 
@@ -111,6 +111,8 @@ struct gemm_f16_plan_s {
   int attn_pairs = 0;  // co-resident clusters of two for the pair attention kernel
   void* ws = nullptr;
   size_t ws_bytes = 0;
+  void* paged_ws = nullptr;  // attention over a paged cache: tile counters and partial sums
+  size_t paged_ws_bytes = 0;
   void* apack = nullptr;  // repacked copy of A (see pack_rows_kernel)
   size_t apack_bytes = 0;
   // FP32 values of the K halves of the pair kernel's last-wave tiles.
@@ -169,6 +171,8 @@ int gemm_plan_init(gemm_f16_plan_s* p, const cudaDeviceProp& prop);
 void gemm_plan_release(gemm_f16_plan_s* p);
 int attn_plan_init(gemm_f16_plan_s* p, const cudaDeviceProp& prop);
 void attn_plan_release(gemm_f16_plan_s* p);
+int paged_plan_init(gemm_f16_plan_s* p, const cudaDeviceProp& prop);
+void paged_plan_release(gemm_f16_plan_s* p);
 
 }  // namespace host
 }  // namespace gf16

@@ -214,6 +214,7 @@ int gemm_f16_plan(gemm_f16_plan_t* out, int device) {
   p->num_sms = prop.multiProcessorCount;
   int rc = gemm_plan_init(p, prop);
   if (!rc) rc = attn_plan_init(p, prop);
+  if (!rc) rc = paged_plan_init(p, prop);
   if (rc) {
     delete p;
     return rc;
@@ -241,6 +242,7 @@ int gemm_f16_destroy(gemm_f16_plan_t p) {
     cudaDeviceSynchronize();
     gemm_plan_release(p);
     attn_plan_release(p);
+    paged_plan_release(p);
     if (p->ws) cudaFree(p->ws);
     if (p->in_stream) cudaStreamDestroy(p->in_stream);
     for (cudaEvent_t ev : p->timing_marks) cudaEventDestroy(ev);
