@@ -24,7 +24,7 @@ SOURCES = [os.path.join(CSRC, f) for f in ("plan.cu", "gemm_f16.cu", "attn_f16.c
 HEADERS = [os.path.join(CSRC, f) for f in ("host.h", "ptx.cuh", "schedule.h", "common.cuh",
                                             "gemm_pair.cuh", "gemm_quad.cuh", "attn_f16.cuh",
                                             "attn_pair.cuh", "paged_schedule.h",
-                                            "paged_small.cuh")]
+                                            "paged_small.cuh", "paged_large.cuh")]
 DEPENDS = SOURCES + HEADERS + [os.path.join(INCLUDE, "gemm_f16.h"),
                                os.path.join(INCLUDE, "attn_f16.h")]
 

@@ -16,6 +16,7 @@
 #include "paged_schedule.h"
 
 #include "paged_small.cuh"
+#include "paged_large.cuh"
 
 using namespace gf16;
 using namespace gf16::host;
@@ -23,7 +24,7 @@ using namespace gf16::host;
 namespace gf16 {
 namespace host {
 
-int paged_plan_init(gemm_f16_plan_s*, const cudaDeviceProp&) {
+int paged_plan_init(gemm_f16_plan_s* p, const cudaDeviceProp& prop) {
   GF16_CUDA(cudaFuncSetAttribute(paged::small::paged_small_kernel<16>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)paged::small::Cfg<16>::SMEM),
@@ -36,6 +37,25 @@ int paged_plan_init(gemm_f16_plan_s*, const cudaDeviceProp&) {
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)paged::small::Cfg<64>::SMEM),
             "cudaFuncSetAttribute(paged attention kernel smem)");
+  GF16_CUDA(cudaFuncSetAttribute(paged::large::paged_large_kernel,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)paged::large::SMEM_BYTES),
+            "cudaFuncSetAttribute(paged attention kernel smem)");
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(prop.multiProcessorCount / 2 * 2), 1, 1);
+  cfg.blockDim = dim3(paged::large::NUM_THREADS, 1, 1);
+  cfg.dynamicSmemBytes = paged::large::SMEM_BYTES;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 2;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int clusters = 0;
+  GF16_CUDA(cudaOccupancyMaxActiveClusters(&clusters, paged::large::paged_large_kernel, &cfg),
+            "cudaOccupancyMaxActiveClusters(paged attention kernel)");
+  p->paged_pairs = clusters > 1 ? clusters : 1;
   return GEMM_F16_OK;
 }
 
@@ -49,115 +69,19 @@ void paged_plan_release(gemm_f16_plan_s* p) {
 namespace {
 
 constexpr int HEAD_DIM = 256;
-constexpr int WARPS = 4;
 
-struct Params {
-  int batch, total_q, max_q, q_heads, kv_heads;
-  const __half *Q, *Kc, *Vc;
-  __half* O;
-  int64_t q_st[2], o_st[2], k_st[3], v_st[3];
-  int num_pages, page_size, max_pages;
-  const int32_t *table, *starts, *kv_lens;
-  int64_t table_stride;
-  float scale_log2;
-  int window, sinks;
-  int* status;
-  int skip;   // requests with at most this many new tokens are another kernel's
-};
-
-__device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
-  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
-    f[2 * i] = t.x;
-    f[2 * i + 1] = t.y;
-  }
-}
-
-// One warp per (token, query head), eight numbers of the head per lane; one
-// pass over the visible keys with the running maximum and sum.
-__global__ void __launch_bounds__(WARPS * 32) paged_attn_kernel(const Params p) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int lane = threadIdx.x & 31;
-  const int64_t w = (int64_t)blockIdx.x * WARPS + (threadIdx.x >> 5);
-  if (w >= (int64_t)p.total_q * p.q_heads) return;
-  const int t = (int)(w / p.q_heads), h = (int)(w - (int64_t)t * p.q_heads);
-  __half* out = p.O + t * p.o_st[0] + h * p.o_st[1] + lane * 8;
-  // The last request whose first token is not after t.
-  int lo = 0, hi = p.batch + 1;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (p.starts[mid] <= t) lo = mid; else hi = mid;
-  }
-  if (lo == p.batch) {
-    *reinterpret_cast<uint4*>(out) = make_uint4(0, 0, 0, 0);
-    return;
-  }
-  const int b = lo;
-  const int s0 = p.starts[b], s1 = p.starts[b + 1];
-  int64_t n = (int64_t)s1 - s0, len = p.kv_lens[b];
-  const int64_t room = (int64_t)p.max_pages * p.page_size;
-  if (s0 < 0 || n < 0 || n > p.max_q || s1 > p.total_q || len < 0 || len > room) {
-    *(volatile int*)p.status = GEMM_F16_ERR_BAD_INDEX;
-    len = len < 0 ? 0 : min(len, room);
-  }
-  if (n <= p.skip) return;
-  const int64_t pos = min(len - n + (t - s0), len - 1);
-  const int kvh = h / (p.q_heads / p.kv_heads);
-  float q[8];
-  unpack8(*reinterpret_cast<const uint4*>(p.Q + t * p.q_st[0] + h * p.q_st[1] + lane * 8), q);
-  float m = -INFINITY, l = 0.f, acc[8] = {};
-  const int64_t first = p.window > 0 ? max((int64_t)0, pos - p.window + 1) : 0;
-  for (int64_t j = 0; j <= pos; ++j) {
-    if (j < first && j >= p.sinks) j = first;
-    const int page = p.table[b * p.table_stride + j / p.page_size];
-    const int64_t row = j % p.page_size;
-    float k[8] = {}, v[8] = {};
-    if (page < 0 || page >= p.num_pages) {
-      *(volatile int*)p.status = GEMM_F16_ERR_BAD_INDEX;
-    } else {
-      unpack8(*reinterpret_cast<const uint4*>(p.Kc + page * p.k_st[0] + row * p.k_st[1] +
-                                              kvh * p.k_st[2] + lane * 8), k);
-      unpack8(*reinterpret_cast<const uint4*>(p.Vc + page * p.v_st[0] + row * p.v_st[1] +
-                                              kvh * p.v_st[2] + lane * 8), v);
-    }
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s = fmaf(q[i], k[i], s);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    s *= p.scale_log2;
-    const float mn = fmaxf(m, s);
-    const float at = mn == -INFINITY ? 0.f : mn;  // only scores of -inf so far: no weight
-    const float a = exp2f(m - at), e = exp2f(s - at);
-    m = mn;
-    l = l * a + e;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] = fmaf(acc[i], a, e * v[i]);
-  }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  uint4 o;
-  __half2 r[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) r[i] = __floats2half2_rn(acc[2 * i] * inv, acc[2 * i + 1] * inv);
-  o.x = *reinterpret_cast<uint32_t*>(&r[0]);
-  o.y = *reinterpret_cast<uint32_t*>(&r[1]);
-  o.z = *reinterpret_cast<uint32_t*>(&r[2]);
-  o.w = *reinterpret_cast<uint32_t*>(&r[3]);
-  *reinterpret_cast<uint4*>(out) = o;
-}
-
-// Workspace of the attention over a paged cache: a counter per partial slot,
-// zero between calls, then the partials' offsets and sums, then their FP32 O.
+// Workspace of the attention over a paged cache: counters, zero between
+// calls, then the partials' offsets and sums, then their FP32 O; of the two
+// kernels' needs the larger.  Its size depends on the device alone.
 constexpr int SMALL_ROWS = 64;   // most rows of a request for the small kernel
 
 int ensure_workspace(gemm_f16_plan_s* p, cudaStream_t stream, paged::Params* prm) {
-  const size_t slots = 2 * (size_t)p->num_sms;
-  const size_t counters = (slots * sizeof(int) + 255) / 256 * 256;
-  const size_t ml = slots * SMALL_ROWS * sizeof(float2);
-  const size_t bytes = counters + ml + slots * SMALL_ROWS * HEAD_DIM * sizeof(float);
+  const size_t small_slots = 2 * (size_t)p->num_sms, large_slots = 2 * (size_t)p->paged_pairs;
+  const size_t rows = std::max(small_slots * SMALL_ROWS, large_slots * paged::large::PART_ROWS);
+  const size_t counters =
+      (std::max(small_slots, large_slots * paged::large::COUNTERS) * sizeof(int) + 255) / 256 * 256;
+  const size_t ml = rows * sizeof(float2);
+  const size_t bytes = counters + ml + rows * HEAD_DIM * sizeof(float);
   if (p->paged_ws_bytes < bytes) {
     const int rc = ensure_buffer(&p->paged_ws, &p->paged_ws_bytes, bytes, stream,
                                  "paged attention workspace allocation");
@@ -236,20 +160,29 @@ int encode_q(gemm_f16_plan_s* p, CUtensorMap* map, const void* ptr, int total_q,
   return encode(p, key, map, 3, ptr, dims, strides, box);
 }
 
-template <int N>
-cudaError_t launch_small(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
-                         const paged::Params& prm, int ctas, cudaStream_t stream) {
+using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap,
+                        const paged::Params);
+
+int launch(gemm_f16_plan_s* p, Kernel kernel, const char* what, int ctas, int threads,
+           size_t smem, cudaStream_t stream, const CUtensorMap& tmQ, const CUtensorMap& tmK,
+           const CUtensorMap& tmV, const paged::Params& prm) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas, 1, 1);
-  cfg.blockDim = dim3(paged::small::NUM_THREADS, 1, 1);
-  cfg.dynamicSmemBytes = paged::small::Cfg<N>::SMEM;
+  cfg.blockDim = dim3((unsigned)threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute pdl;
   pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   pdl.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &pdl;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged::small::paged_small_kernel<N>, tmQ, tmK, tmV, prm);
+  cudaEvent_t t0;
+  int rc = timing_begin(p, stream, &t0);
+  if (rc) return rc;
+  const cudaError_t le = cudaLaunchKernelEx(&cfg, kernel, tmQ, tmK, tmV, prm);
+  rc = timing_end(p, stream, t0, le == cudaSuccess);
+  GF16_CUDA(le, what);
+  return rc;
 }
 
 bool off(const void* p, uintptr_t mask) { return ((uintptr_t)p & mask) != 0; }
@@ -306,102 +239,82 @@ int attn_f16_paged_fwd(gemm_f16_plan_t p, int batch, int total_q, int max_q, int
                        const int64_t o_strides[2], float scale, int window, int sinks,
                        gemm_f16_stream_t stream) {
   if (!p) return GEMM_F16_ERR_INVALID_ARG;
-  const int rc = attn_f16_paged_validate(batch, total_q, max_q, q_heads, kv_heads, head_dim, Q,
+  int rc = attn_f16_paged_validate(batch, total_q, max_q, q_heads, kv_heads, head_dim, Q,
                                          q_strides, Kc, kc_strides, Vc, vc_strides, num_pages,
                                          page_size, block_table, table_stride, max_pages, starts,
                                          kv_lens, O, o_strides, scale, window, sinks);
   if (rc) return rc;
   if (total_q == 0) return GEMM_F16_OK;
   DeviceGuard g(p->device);
-  Params prm = {};
+  const cudaStream_t st = (cudaStream_t)stream;
+  paged::Params prm = {};
   prm.batch = batch;
   prm.total_q = total_q;
   prm.max_q = max_q;
   prm.q_heads = q_heads;
   prm.kv_heads = kv_heads;
-  prm.Q = static_cast<const __half*>(Q);
-  prm.Kc = static_cast<const __half*>(Kc);
-  prm.Vc = static_cast<const __half*>(Vc);
-  prm.O = static_cast<__half*>(O);
-  for (int i = 0; i < 2; ++i) {
-    prm.q_st[i] = q_strides[i];
-    prm.o_st[i] = o_strides[i];
-  }
-  for (int i = 0; i < 3; ++i) {
-    prm.k_st[i] = kc_strides[i];
-    prm.v_st[i] = vc_strides[i];
-  }
+  prm.group = q_heads / kv_heads;
   prm.num_pages = num_pages;
   prm.page_size = page_size;
   prm.max_pages = max_pages;
   prm.table = block_table;
-  prm.table_stride = table_stride;
   prm.starts = starts;
   prm.kv_lens = kv_lens;
-  prm.scale_log2 = scale * 1.4426950408889634f;
-  prm.window = window;
-  prm.sinks = sinks;
+  prm.table_stride = table_stride;
+  prm.O = static_cast<__half*>(O);
+  prm.o_tok = o_strides[0];
+  prm.o_head = o_strides[1];
+  prm.scale_log2 = scale * 1.4426950408889634f;  // log2(e)
+  prm.masks.window = window;
+  prm.masks.sinks = sinks;
   prm.status = p->status_dev;
-  const int group = q_heads / kv_heads;
-  int sk = 0;   // requests of up to this many tokens go to the small kernel
-  {
-    const int64_t rows = (int64_t)max_q * group;
-    const int N = rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
-    paged::Params sp = {};
-    sp.batch = batch;
-    sp.total_q = total_q;
-    sp.max_q = max_q;
-    sp.q_heads = q_heads;
-    sp.kv_heads = kv_heads;
-    sp.group = group;
-    sp.num_pages = num_pages;
-    sp.page_size = page_size;
-    sp.max_pages = max_pages;
-    sp.rows = std::min(page_size & -page_size, paged::BLOCK_KEYS);
-    sp.table = block_table;
-    sp.starts = starts;
-    sp.kv_lens = kv_lens;
-    sp.table_stride = table_stride;
-    sp.O = static_cast<__half*>(O);
-    sp.o_tok = o_strides[0];
-    sp.o_head = o_strides[1];
-    sp.scale_log2 = prm.scale_log2;
-    sp.masks.window = window;
-    sp.masks.sinks = sinks;
-    sp.tile_tokens = N / group;
-    sp.status = p->status_dev;
-    sp.timeout_ns = p->timeout_ns;
-    sp.fault_unit = p->fault_unit;
-    int rc2 = ensure_workspace(p, (cudaStream_t)stream, &sp);
-    CUtensorMap tmQ, tmK, tmV;
-    if (rc2 || (rc2 = encode_q(p, &tmQ, Q, total_q, q_heads, q_strides, group, sp.tile_tokens)) ||
-        (rc2 = encode_cache(p, &tmK, Kc, num_pages, page_size, kv_heads, kc_strides, sp.rows)) ||
-        (rc2 = encode_cache(p, &tmV, Vc, num_pages, page_size, kv_heads, vc_strides, sp.rows)))
-      return rc2;
+  prm.timeout_ns = p->timeout_ns;
+  prm.fault_unit = p->fault_unit;
+  if ((rc = ensure_workspace(p, st, &prm))) return rc;
+  CUtensorMap tmQ, tmK, tmV;
+  const int page_rows = page_size & -page_size;   // the largest power of two in it
+  const int64_t rows = (int64_t)max_q * prm.group;
+  // Requests of up to SMALL_ROWS rows (new tokens x group) are bound by
+  // reading the cache and go to the small kernel, with room for the rows
+  // that the step's largest has (16, 32 or 64).  The others go to the large
+  // one; a step of one request that may be large launches that alone, which
+  // takes a request of any size.
+  const bool any_large = rows > SMALL_ROWS, any_small = !any_large || batch > 1;
+  if (any_small) {
+    const int n = rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
+    prm.rows = std::min(page_rows, paged::BLOCK_KEYS);
+    prm.tile_tokens = n / prm.group;
+    prm.zero_rows = 1;
+    if ((rc = encode_q(p, &tmQ, Q, total_q, q_heads, q_strides, prm.group, prm.tile_tokens)) ||
+        (rc = encode_cache(p, &tmK, Kc, num_pages, page_size, kv_heads, kc_strides, prm.rows)) ||
+        (rc = encode_cache(p, &tmV, Vc, num_pages, page_size, kv_heads, vc_strides, prm.rows)))
+      return rc;
     const int ctas = p->sm_limit > 0 ? std::min(p->sm_limit, p->num_sms) : p->num_sms;
-    cudaEvent_t t0;
-    if ((rc2 = timing_begin(p, (cudaStream_t)stream, &t0))) return rc2;
-    const auto fn = N == 16 ? launch_small<16> : (N == 32 ? launch_small<32> : launch_small<64>);
-    const cudaError_t le = fn(tmQ, tmK, tmV, sp, ctas, (cudaStream_t)stream);
-    rc2 = timing_end(p, (cudaStream_t)stream, t0, le == cudaSuccess);
-    GF16_CUDA(le, "launch paged_small_kernel");
-    if (rc2) return rc2;
-    sk = sp.tile_tokens;
-    if (rows <= N) return GEMM_F16_OK;
+    using namespace paged::small;
+    const Kernel kernel = n == 16 ? paged_small_kernel<16>
+                                  : (n == 32 ? paged_small_kernel<32> : paged_small_kernel<64>);
+    const size_t smem = n == 16 ? Cfg<16>::SMEM : (n == 32 ? Cfg<32>::SMEM : Cfg<64>::SMEM);
+    if ((rc = launch(p, kernel, "launch paged_small_kernel", ctas, NUM_THREADS, smem, st, tmQ, tmK,
+                     tmV, prm)))
+      return rc;
+    prm.skip_tokens = prm.tile_tokens;
   }
-  prm.skip = sk;
-  cudaLaunchConfig_t cfg = {};
-  const int64_t blocks = ceil_div((int64_t)total_q * q_heads, WARPS);
-  if (blocks > INT32_MAX) return GEMM_F16_ERR_INVALID_ARG;
-  cfg.gridDim = dim3((unsigned)blocks, 1, 1);
-  cfg.blockDim = dim3(WARPS * 32, 1, 1);
-  cfg.stream = (cudaStream_t)stream;
-  cudaLaunchAttribute pdl;
-  pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  pdl.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &pdl;
-  cfg.numAttrs = 1;
-  GF16_CUDA(cudaLaunchKernelEx(&cfg, paged_attn_kernel, prm), "launch paged_attn_kernel");
+  if (any_large) {
+    using namespace paged::large;
+    const int cta_tokens = CQ / prm.group;
+    prm.rows = std::min(page_rows, MAX_ROWS);
+    prm.tile_tokens = 2 * cta_tokens;
+    prm.zero_rows = !any_small;
+    if ((rc = encode_q(p, &tmQ, Q, total_q, q_heads, q_strides, prm.group, cta_tokens)) ||
+        (rc = encode_cache(p, &tmK, Kc, num_pages, page_size, kv_heads, kc_strides, prm.rows)) ||
+        (rc = encode_cache(p, &tmV, Vc, num_pages, page_size, kv_heads, vc_strides, prm.rows)))
+      return rc;
+    int pairs = p->paged_pairs;
+    if (p->sm_limit > 0) pairs = std::max(1, std::min(pairs, p->sm_limit / 2));
+    if ((rc = launch(p, paged_large_kernel, "launch paged_large_kernel", 2 * pairs, NUM_THREADS,
+                     SMEM_BYTES, st, tmQ, tmK, tmV, prm)))
+      return rc;
+  }
   return GEMM_F16_OK;
 }
 

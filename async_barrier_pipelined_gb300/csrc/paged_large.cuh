@@ -1,0 +1,908 @@
+// Attention over a paged cache for requests with many new tokens (prompts and
+// chunks of them): tiles of up to 256 rows, a row being one new token's query
+// under one of the query heads that share a key/value head.
+//
+// Bound by the tensor cores.  The same CTA pair as the dense attention kernel
+// (attn_pair.cuh): S = Q K^T and O += P V as 256-row MMAs over two SMs, P and O
+// in tensor memory, the softmax of a block beside the products of its
+// neighbours, O written while the next tile runs.  What is different:
+//   rows     CTA r holds tokens T*r .. T*(r+1) - 1 of the tile, T = 128 / group,
+//            times the `group` query heads: a tile reads each key once for
+//            all of them, and Q lands in row order by one 3-D copy per chunk.
+//   keys     come page by page: lane l of the copy warp takes one group of
+//            rows (at most 64) of one 64-number chunk; the pages of the next
+//            block are looked up a block ahead.  Groups that no query of the
+//            tile sees, and rows past its last key, read as zeros without
+//            touching memory (paged_schedule.h).
+//   masks    only in blocks that the causal edge, the window's edge or the
+//            sinks cut; there each softmax thread builds the 128 bits of the
+//            keys that its row sees.
+//   dealing  the pairs get equal shares of the step's key blocks, whatever
+//            the lengths (causal tiles differ in cost); a tile that is cut
+//            leaves FP32 partials, and of each 32 rows the last warp to
+//            finish merges them in order, counted as in the small kernel.
+// Barriers and signals are those of attn_pair.cuh.
+#pragma once
+
+namespace gf16 {
+namespace paged {
+namespace large {
+
+constexpr int CQ = 128;                 // rows per CTA
+constexpr int BKV = BLOCK_KEYS;
+constexpr int MAX_ROWS = 64;            // most keys per copy group (a CTA's half of a key block)
+constexpr int RING = 4;
+constexpr int SM_WARPS = 4;             // softmax warps 2..5
+constexpr int EP_WARPS = 4;             // epilogue warps 6..9
+constexpr int NUM_THREADS = 32 * (2 + SM_WARPS + EP_WARPS);
+constexpr int NUM_WARPS = NUM_THREADS / 32;
+constexpr int WIN = NUM_THREADS;        // requests kept in shared memory
+
+constexpr uint32_t CHUNK_Q = CQ * 128;
+constexpr uint32_t Q_BYTES = 4 * CHUNK_Q;
+constexpr uint32_t K_CHUNK = (BKV / 2) * 128;
+constexpr uint32_t V_CHUNK = BKV * 128;
+constexpr uint32_t SLOT_BYTES = 32768;
+constexpr uint32_t BOX = 32 * 128;      // 32 rows by 128 bytes of O
+constexpr uint32_t OFF_Q = 0;
+constexpr uint32_t OFF_RING = OFF_Q + Q_BYTES;
+constexpr uint32_t OFF_STAGE = OFF_RING + RING * SLOT_BYTES;   // one box per epilogue warp
+constexpr uint32_t OFF_L = OFF_STAGE + EP_WARPS * BOX;         // row sums and offsets
+constexpr uint32_t OFF_REQ = OFF_L + 2 * CQ * 4;               // WIN x (start, n, len, blocks)
+constexpr uint32_t OFF_SCHED = OFF_REQ + WIN * 16;
+constexpr uint32_t OFF_BAR = OFF_SCHED + 64;
+constexpr uint32_t NUM_BARS = 2 + 2 * RING + 2 + 2 + 2 + 3 + 1;
+constexpr uint32_t OFF_TMEM_SLOT = OFF_BAR + NUM_BARS * 8;
+constexpr uint32_t OFF_ABORT = OFF_TMEM_SLOT + 4;
+constexpr uint32_t OFF_PEER_FILLS = OFF_ABORT + 4;
+constexpr uint32_t OFF_PEER_QLOADS = OFF_PEER_FILLS + 4;
+constexpr uint32_t OFF_SIG = (OFF_PEER_QLOADS + 4 + 15) / 16 * 16;
+constexpr uint32_t SIG_BYTES = 16;
+constexpr uint32_t SIG_P = 0;
+constexpr uint32_t SIG_S = SIG_P + SM_WARPS * SIG_BYTES;
+constexpr uint32_t SIG_O = SIG_S + SM_WARPS * SIG_BYTES;
+constexpr uint32_t SIG_SRC = SIG_O + EP_WARPS * SIG_BYTES;
+constexpr uint32_t SMEM_BYTES = OFF_SIG + SIG_SRC + (SM_WARPS + EP_WARPS) * SIG_BYTES + 1024;
+static_assert(SMEM_BYTES <= 232448, "over the 227 KB shared-memory limit per CTA");
+static_assert(OFF_RING % 1024 == 0 && OFF_STAGE % 1024 == 0, "swizzled buffers");
+
+constexpr uint32_t TMEM_COLS = 512;
+constexpr uint32_t S_COL = 0;     // S: columns 0 .. 127 (FP32)
+constexpr uint32_t P_COL = 128;   // two P buffers of 64 columns (FP16 pairs)
+constexpr uint32_t O_COL = 256;   // O: columns 256 .. 511
+constexpr uint32_t IDESC_QK = (1u << 4) | ((uint32_t)(BKV >> 3) << 17) | ((uint32_t)(2 * CQ >> 4) << 24);
+constexpr uint32_t IDESC_PV =
+    (1u << 4) | (1u << 16) | ((uint32_t)(HD >> 3) << 17) | ((uint32_t)(2 * CQ >> 4) << 24);
+
+// Row r of the pair's partial of a slot; counters per slot, CTA and 32 rows.
+constexpr int PART_ROWS = 2 * CQ;
+constexpr int COUNTERS = 2 * EP_WARPS;
+
+struct Bars {
+  uint32_t q_full, q_empty, full, empty, s_full, s_free, p_full, o_done, o_free, l_ready, l_free,
+      mma_done;
+};
+
+// This cluster's share of the line, and the tile that it begins in.
+struct Sched {
+  long long w0, w1, per;
+  int b, head, tile, j;
+  int base;
+};
+static_assert(sizeof(Sched) <= 64, "room for the schedule");
+
+__device__ __forceinline__ bool own_request(const Params& p, const Request& r) {
+  return r.n > p.skip_tokens;
+}
+__device__ __forceinline__ Span span_of(const Params& p, const Request& r, int tile) {
+  const int i0 = tile * p.tile_tokens;
+  return tile_span(r, i0, imin(i0 + p.tile_tokens, r.n) - 1, p.masks);
+}
+__device__ __forceinline__ int tiles_of(const Params& p, const Request& r) {
+  return (r.n + p.tile_tokens - 1) / p.tile_tokens;
+}
+
+struct Walk {
+  const Params& p;
+  const int4* req;
+  long long w, w1;
+  int b, head, tile, j, base, tiles;
+  Request r;
+  Span s;
+  int j0, j1;
+  int cur_head, i0, cnt;    // of the current tile: head, first token, tokens
+  __device__ __forceinline__ Walk(const Params& p_, const Sched& sc, const int4* req_)
+      : p(p_), req(req_), w(sc.w0), w1(sc.w1), b(sc.b), head(sc.head), tile(sc.tile), j(sc.j),
+        base(sc.base), tiles(0) {
+    if (w < w1) fetch();
+  }
+  __device__ __forceinline__ void fetch() {
+    const int k = b - base;
+    if (k < WIN) {
+      const int4 v = req[k];
+      r.start = v.x;
+      r.n = v.y;
+      r.len = v.z;
+    } else {
+      r = load_request(p, b);
+    }
+    tiles = tiles_of(p, r);
+  }
+  __device__ __forceinline__ bool next() {
+    if (w >= w1) return false;
+    if (tile == tiles) {
+      tile = 0;
+      ++head;
+    }
+    if (head == p.kv_heads) {
+      head = 0;
+      do {
+        ++b;
+        fetch();
+      } while (!own_request(p, r));
+    }
+    s = span_of(p, r, tile);
+    cur_head = head;
+    i0 = tile * p.tile_tokens;
+    cnt = imin(p.tile_tokens, r.n - i0);
+    j0 = j;
+    j1 = (int)lmin(s.nb, (long long)j0 + (w1 - w));
+    w += j1 - j0;
+    j = 0;
+    ++tile;
+    return true;
+  }
+  __device__ __forceinline__ bool more() const { return w < w1; }
+  __device__ __forceinline__ long long line() const { return w - j1; }
+};
+
+// Key blocks of one head of a request, by a whole warp.
+__device__ __forceinline__ long long head_blocks(const Params& p, const Request& r, int lane) {
+  long long sum = 0;
+  if (own_request(p, r)) {
+    const int tiles = tiles_of(p, r);
+    for (int t = lane; t < tiles; t += 32) sum += span_of(p, r, t).nb;
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  return sum;
+}
+
+__device__ __forceinline__ void schedule(const Params& p, uint8_t* smem, int worker, int workers,
+                                         long long* warp_sum) {
+  int4* req = reinterpret_cast<int4*>(smem + OFF_REQ);
+  Sched* sc = reinterpret_cast<Sched*>(smem + OFF_SCHED);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    sc->w0 = sc->w1 = 0;
+    sc->per = 1;
+  }
+  long long total = 0, w0 = 0, per = 1, before = 0;
+  // First pass: all blocks of the step (request counts up to WIN stay in
+  // shared memory).  The second finds the worker's first tile.
+  const bool one = p.batch <= WIN;
+  for (int pass = 0; pass < 2; ++pass) {
+    before = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += WIN) {
+      if (pass == 0 || !one) {
+        __syncthreads();
+        const int b = b0 + tid;
+        Request r{0, 0, 0, false};
+        if (b < p.batch) r = load_request(p, b);
+        if (pass == 0 && r.bad) *(volatile int*)p.status = (int)GEMM_F16_ERR_BAD_INDEX;
+        req[tid] = make_int4(r.start, r.n, r.len, 0);
+        __syncthreads();
+        const int left = imin(WIN, p.batch - b0);
+        for (int k = warp; k < left; k += NUM_WARPS) {
+          const int4 v = req[k];
+          const long long hb = head_blocks(p, Request{v.x, v.y, v.z, false}, lane);
+          // (at most 2^31 / 128 blocks per tile, 2^31 tokens: a request that
+          // does not fit 32 bits would not end in a century)
+          if (lane == 0) req[k].w = (int)lmin(hb, 2147483647);
+        }
+        __syncthreads();
+      }
+      const long long mine = (long long)req[tid].w * p.kv_heads;
+      long long inc = mine;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d) inc += o;
+      }
+      if (lane == 31) warp_sum[warp] = inc;
+      __syncthreads();
+      long long all = 0, basis = before;
+      for (int k = 0; k < NUM_WARPS; ++k) {
+        if (k < warp) basis += warp_sum[k];
+        all += warp_sum[k];
+      }
+      inc += basis;
+      if (pass == 1 && mine > 0 && w0 >= inc - mine && w0 < inc) {
+        const long long at = w0 - (inc - mine), hb = req[tid].w;
+        sc->w0 = w0;
+        sc->w1 = lmin(w0 + per, total);
+        sc->per = per;
+        sc->b = b0 + tid;
+        sc->head = (int)(at / hb);
+        sc->tile = 0;
+        sc->j = (int)(at % hb);   // for now: blocks into the head
+        sc->base = b0;
+      }
+      before += all;
+      __syncthreads();
+      if (pass == 1 && w0 < before) break;   // found: req holds its part of the batch
+    }
+    if (pass == 0) {
+      total = before;
+      per = per_worker(total, workers);
+      w0 = per * worker;
+      if (w0 >= total) return;
+    }
+  }
+  // The tile within the head, 32 at a time.
+  if (warp == 0) {
+    const int4 v = req[sc->b - sc->base];
+    const Request r{v.x, v.y, v.z, false};
+    const int tiles = tiles_of(p, r);
+    int at = sc->j;
+    for (int t0 = 0; t0 < tiles; t0 += 32) {
+      const int t = t0 + lane;
+      const int nb = t < tiles ? span_of(p, r, t).nb : 0;
+      int inc = nb;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d) inc += o;
+      }
+      const int all = __shfl_sync(0xffffffffu, inc, 31);
+      if (at < all) {
+        if (at >= inc - nb && at < inc) {
+          sc->tile = t;
+          sc->j = at - (inc - nb);
+        }
+        break;
+      }
+      at -= all;
+    }
+  }
+}
+
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const Params& p,
+                                          volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, wait_phase(bar, parity, p, abort_flag));
+}
+
+// The epilogue warps wait most of a tile: they sleep between polls.
+__device__ __noinline__ bool wait_sleepy(uint32_t bar, uint32_t parity, const Params& p,
+                                         volatile int* abort_flag) {
+  const uint64_t t0 = ptx::globaltimer();
+  while (true) {
+    if (ptx::mbar_try_wait_poll(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (ptx::globaltimer() - t0 > p.timeout_ns) {
+      *abort_flag = 1;
+      *(volatile int*)p.status = (int)GEMM_F16_ERR_TIMEOUT;
+      __threadfence_system();
+      return false;
+    }
+    __nanosleep(256);
+  }
+}
+__device__ __forceinline__ bool wait_suspend(uint32_t bar, uint32_t parity, const Params& p,
+                                             volatile int* abort_flag) {
+  if (ptx::mbar_try_wait(bar, parity)) return true;
+  return wait_slow(bar, parity, p, abort_flag);
+}
+
+// One arrival per warp on a leader barrier (see attn_pair.cuh).
+__device__ __forceinline__ void signal_leader(uint32_t rank, uint32_t lane, uint32_t local_bar,
+                                              uint32_t leader_bar, uint32_t dst, uint32_t src) {
+  ptx::tc_fence_before();
+  __syncwarp();
+  if (lane == 0) {
+    if (rank == 0)
+      ptx::mbar_arrive_expect_tx(local_bar, SIG_BYTES);
+    else
+      ptx::bulk_copy_to_cluster(dst, src, SIG_BYTES, leader_bar);
+  }
+}
+
+// 3-D tensor load crediting a barrier that may live in the peer CTA: in
+// ptx.cuh (tma_load_3d_pair), as the 4-D one.
+
+struct Issued {
+  uint32_t fills, qloads;
+};
+
+// ------------------------------------------------------------------ copies
+__device__ __forceinline__ Issued producer_role(const CUtensorMap* tmQ, const CUtensorMap* tmK,
+                                                const CUtensorMap* tmV, const Params& p, Walk& walk,
+                                                uint32_t base, const Bars& b, uint32_t rank,
+                                                uint32_t lane, int cluster,
+                                                volatile int* abort_flag) {
+  const uint32_t leader_q = ptx::map_to_cta(b.q_full, 0);
+  const uint32_t leader_full = ptx::map_to_cta(b.full, 0);
+  const int cta_tokens = p.tile_tokens / 2;
+  const uint32_t q_bytes = 4u * 128u * (uint32_t)(cta_tokens * p.group);
+  const int kg = MAX_ROWS / p.rows;            // groups of this CTA's half of a key block (1 .. 8)
+  // Keys: lane = chunk * 8 + group; values: lane = chunk * 16 + group.
+  const int k_chunk = (int)lane >> 3, k_in = (int)lane & 7;
+  const int k_group = (int)rank * kg + imin(k_in, kg - 1);
+  const int v_chunk = (int)lane >> 4, v_in = (int)lane & 15;
+  const int v_group = imin(v_in, 2 * kg - 1);
+  RingPos pos{0, 0};
+  Issued n{0, 0};
+  bool ok = true;
+  while (ok && walk.next()) {
+    const int head = walk.cur_head;
+    if (n.qloads > 0)
+      ok = __all_sync(0xffffffffu, wait_suspend(b.q_empty, (n.qloads - 1) & 1u, p, abort_flag));
+    if (!ok) break;
+    if (lane == 0) {
+      if (rank == 0) ptx::mbar_arrive_expect_tx_relaxed(b.q_full, 2 * q_bytes);
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        ptx::tma_load_3d_pair(base + OFF_Q + c * CHUNK_Q, tmQ, leader_q, 64 * c, head * p.group,
+                              walk.r.start + walk.i0 + (int)rank * cta_tokens);
+    }
+    ++n.qloads;
+    auto page_of = [&](int j, int g) {
+      return j < walk.j1 ? group_page(p, walk.s, walk.b, span_block(walk.s, j), g) : 0;
+    };
+    auto fill = [&](bool is_k, int j, int page) -> bool {
+      const int g = is_k ? k_group : v_group;
+      const int2 src = group_source(p, walk.s, span_block(walk.s, j), g, page);
+      if (!__all_sync(0xffffffffu, wait_suspend(b.empty + 8 * pos.stage, producer_wait_parity(pos),
+                                                p, abort_flag)))
+        return false;
+      if (rank == 0 && lane == 0)
+        ptx::mbar_arrive_expect_tx_relaxed(b.full + 8 * pos.stage, 2 * SLOT_BYTES);
+      __syncwarp();
+      if (!(n.fills == 0 && cluster == p.fault_unit && rank == 0)) {
+        const uint32_t dst = base + OFF_RING + pos.stage * SLOT_BYTES;
+        const uint32_t fb = leader_full + 8 * pos.stage;
+        if (is_k) {
+          if (k_in < kg)
+            ptx::tma_load_4d_pair(dst + k_chunk * K_CHUNK + (uint32_t)(k_in * p.rows) * 128u, tmK,
+                                  fb, 64 * k_chunk, src.y, head, src.x);
+        } else {
+          if (v_in < 2 * kg)
+            ptx::tma_load_4d_pair(dst + v_chunk * V_CHUNK + (uint32_t)(v_in * p.rows) * 128u, tmV,
+                                  fb, (int)rank * 128 + 64 * v_chunk, src.y, head, src.x);
+        }
+      }
+      ++n.fills;
+      ring_advance(pos, RING);
+      return true;
+    };
+    int kp = page_of(walk.j0, k_group), vp = page_of(walk.j0, v_group);
+    int kp1 = page_of(walk.j0 + 1, k_group);
+    ok = fill(true, walk.j0, kp);
+    for (int j = walk.j0; ok && j < walk.j1; ++j) {
+      const int kp2 = page_of(j + 2, k_group), vp1 = page_of(j + 1, v_group);
+      if (j + 1 < walk.j1) ok = fill(true, j + 1, kp1);
+      ok = ok && fill(false, j, vp);
+      kp1 = kp2;
+      vp = vp1;
+    }
+  }
+  return n;
+}
+
+// ------------------------------------------------------------------ MMAs (leader)
+__device__ __forceinline__ void mma_role(const Params& p, Walk& walk, uint32_t base,
+                                         uint32_t tmem_base, const Bars& b,
+                                         volatile int* abort_flag) {
+  RingPos pos{0, 0};
+  const uint32_t q_addr = base + OFF_Q;
+  const uint32_t o_tmem = tmem_base + O_COL;
+  auto issue_qk = [&](uint32_t gs, bool last_of_tile) -> bool {
+    if (gs > 0) {
+      if (!wait_suspend(b.s_free, (gs - 1) & 1u, p, abort_flag)) return false;
+    }
+    if (!wait_suspend(b.full + 8 * pos.stage, consumer_wait_parity(pos), p, abort_flag))
+      return false;
+    ptx::tc_fence_after();
+    const uint32_t k_addr = base + OFF_RING + pos.stage * SLOT_BYTES;
+#pragma unroll
+    for (int kk = 0; kk < HD / 16; ++kk) {
+      const uint32_t off_q = (uint32_t)(kk >> 2) * CHUNK_Q + (uint32_t)(kk & 3) * 32u;
+      const uint32_t off_k = (uint32_t)(kk >> 2) * K_CHUNK + (uint32_t)(kk & 3) * 32u;
+      ptx::mma_f16_pair(tmem_base + S_COL, smem_desc_sw128(q_addr + off_q, 16, 1024),
+                        smem_desc_sw128(k_addr + off_k, 16, 1024), IDESC_QK, kk > 0 ? 1u : 0u);
+    }
+    ptx::mma_commit_pair(b.empty + 8 * pos.stage, 0x3);
+    ptx::mma_commit_pair(b.s_full, 0x3);
+    if (last_of_tile) ptx::mma_commit_pair(b.q_empty, 0x3);
+    ring_advance(pos, RING);
+    return true;
+  };
+  uint32_t g0 = 0, ki = 0;
+  bool ok = true;
+  while (ok && walk.next()) {
+    const int nb = walk.j1 - walk.j0;
+    if (!wait_suspend(b.q_full, ki & 1u, p, abort_flag)) break;
+    ptx::tc_fence_after();
+    ok = issue_qk(g0, nb == 1);
+    for (int j = 0; j < nb && ok; ++j) {
+      const uint32_t gj = g0 + (uint32_t)j;
+      if (j + 1 < nb && !issue_qk(gj + 1, j + 2 == nb)) {
+        ok = false;
+        break;
+      }
+      const uint32_t pb = gj & 1u;
+      if (!wait_suspend(b.p_full + 8 * pb, (gj >> 1) & 1u, p, abort_flag) ||
+          !wait_suspend(b.full + 8 * pos.stage, consumer_wait_parity(pos), p, abort_flag)) {
+        ok = false;
+        break;
+      }
+      if (j == 0 && ki > 0 && !wait_suspend(b.o_free, (ki - 1) & 1u, p, abort_flag)) {
+        ok = false;
+        break;
+      }
+      ptx::tc_fence_after();
+      const uint32_t v_addr = base + OFF_RING + pos.stage * SLOT_BYTES;
+      const uint32_t p_tmem = tmem_base + P_COL + pb * (BKV / 2);
+#pragma unroll
+      for (int kk = 0; kk < BKV / 16; ++kk)
+        ptx::mma_f16_pair_tmem_a(o_tmem, p_tmem + (uint32_t)kk * 8u,
+                                 smem_desc_sw128(v_addr + (uint32_t)kk * 2048u, V_CHUNK, 1024),
+                                 IDESC_PV, (j > 0 || kk > 0) ? 1u : 0u);
+      ptx::mma_commit_pair(b.empty + 8 * pos.stage, 0x3);
+      ptx::mma_commit_pair(b.o_done + 8 * pb, 0x3);
+      ring_advance(pos, RING);
+    }
+    g0 += (uint32_t)nb;
+    ++ki;
+  }
+}
+
+// ------------------------------------------------------------------ softmax
+// New exponent offset of one row for a key block (base-2 units): it moves
+// only when the block's maximum passes it by more than RESCALE_LOG2.
+__device__ __forceinline__ float block_offset(const uint32_t (&s)[BKV], float sl2, float m,
+                                              float* alpha) {
+  float r8[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) r8[k] = __uint_as_float(s[k]);
+  if (sl2 >= 0.f) {
+#pragma unroll
+    for (int c = 8; c < BKV; ++c) r8[c & 7] = fmaxf(r8[c & 7], __uint_as_float(s[c]));
+#pragma unroll
+    for (int k = 1; k < 8; ++k) r8[0] = fmaxf(r8[0], r8[k]);
+  } else {
+#pragma unroll
+    for (int c = 8; c < BKV; ++c) r8[c & 7] = fminf(r8[c & 7], __uint_as_float(s[c]));
+#pragma unroll
+    for (int k = 1; k < 8; ++k) r8[0] = fminf(r8[0], r8[k]);
+  }
+  const float mx = (sl2 == 0.f) ? 0.f : r8[0] * sl2;
+  const float m_new = (mx > m + RESCALE_LOG2) ? mx : m;
+  *alpha = (m_new == m) ? 1.f : ptx::ex2_approx(m - m_new);
+  return m_new;
+}
+
+// Weights 2^(sl2 s - m) as binary16 pairs (the product with V takes binary16;
+// half a step of 2^-11 each), and their FP32 sum before that rounding.
+template <bool MASK>
+__device__ __forceinline__ float block_weights(const uint32_t (&s)[BKV], float sl2, float neg_m,
+                                               const uint32_t (&see)[4], uint32_t (&pk)[BKV / 2]) {
+  float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int c = 0; c < BKV / 2; ++c) {
+    float p0 = ptx::ex2_approx(fmaf(__uint_as_float(s[2 * c]), sl2, neg_m));
+    float p1 = ptx::ex2_approx(fmaf(__uint_as_float(s[2 * c + 1]), sl2, neg_m));
+    if (MASK) {
+      p0 = (see[c >> 4] >> ((2 * c) & 31)) & 1u ? p0 : 0.f;
+      p1 = (see[c >> 4] >> ((2 * c + 1) & 31)) & 1u ? p1 : 0.f;
+    }
+    pk[c] = pack_half2(p0, p1);
+    l4[c & 3] += p0 + p1;
+  }
+  return (l4[0] + l4[1]) + (l4[2] + l4[3]);
+}
+
+__device__ __forceinline__ void softmax_role(const Params& p, Walk& walk, uint32_t base,
+                                             uint32_t tmem_base, const Bars& b, float* l_rows,
+                                             uint32_t rank, uint32_t warp, uint32_t lane,
+                                             volatile int* abort_flag) {
+  const uint32_t quarter = warp & 3u;
+  const uint32_t t_lane = (quarter * 32u) << 16;
+  const uint32_t row = quarter * 32u + lane;
+  const uint32_t leader_p_full = ptx::map_to_cta(b.p_full, 0);
+  const uint32_t leader_s_free = ptx::map_to_cta(b.s_free, 0);
+  const uint32_t sig_p = ptx::map_to_cta(base + OFF_SIG + SIG_P + (warp - 2) * SIG_BYTES, 0);
+  const uint32_t sig_s = ptx::map_to_cta(base + OFF_SIG + SIG_S + (warp - 2) * SIG_BYTES, 0);
+  const uint32_t sig_src = base + OFF_SIG + SIG_SRC + (warp - 2) * SIG_BYTES;
+  const float sl2 = p.scale_log2;
+  const int my_tok = (int)rank * (p.tile_tokens / 2) + (int)row / p.group;   // in the tile
+  uint32_t g = 0, ki = 0;
+  bool ok = true;
+  while (ok && walk.next()) {
+    const int p0 = walk.r.len - walk.r.n + walk.i0;      // positions of the tile's tokens
+    const int p1 = p0 + walk.cnt - 1, pos = p0 + my_tok;
+    float m = NO_OFFSET, l = 0.f;
+    for (int j = walk.j0; j < walk.j1; ++j, ++g) {
+      const int blk = span_block(walk.s, j);
+      const bool full_block = block_is_full(p0, p1, blk, p.masks);
+      uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
+      if (!full_block) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) see[w] = seen_word(walk.s, blk, w, p.rows, pos, p.masks);
+      }
+      if (!warp_wait(b.s_full, g & 1u, p, abort_flag)) {
+        ok = false;
+        break;
+      }
+      ptx::tc_fence_after();
+      uint32_t s[BKV];
+#pragma unroll
+      for (int c = 0; c < BKV / 32; ++c)
+        ptx::tmem_ld_32x32b_x32(tmem_base + t_lane + S_COL + 32u * c,
+                                *reinterpret_cast<uint32_t(*)[32]>(&s[32 * c]));
+      ptx::tmem_ld_wait();
+      ptx::reg_fence(s);
+      if (j + 1 < walk.j1 || walk.more())
+        signal_leader(rank, lane, b.s_free, leader_s_free, sig_s, sig_src);
+      float alpha, m_new, lsum;
+      uint32_t pk[BKV / 2];
+      if (!full_block) {
+        const uint32_t fill = __float_as_uint(sl2 >= 0.f ? -INFINITY : INFINITY);
+#pragma unroll
+        for (int c = 0; c < BKV; ++c) s[c] = (see[c >> 5] >> (c & 31)) & 1u ? s[c] : fill;
+        m_new = block_offset(s, sl2, m, &alpha);
+        lsum = block_weights<true>(s, sl2, -m_new, see, pk);
+      } else {
+        m_new = block_offset(s, sl2, m, &alpha);
+        lsum = block_weights<false>(s, sl2, -m_new, see, pk);
+      }
+      const uint32_t pb = g & 1u;
+      if (g >= 2) {
+        if (!warp_wait(b.o_done + 8 * pb, ((g - 2) >> 1) & 1u, p, abort_flag)) {
+          ok = false;
+          break;
+        }
+        ptx::tc_fence_after();
+      }
+      const uint32_t p_tmem = tmem_base + t_lane + P_COL + pb * (BKV / 2);
+      ptx::tmem_st_32x32b_x32(p_tmem, *reinterpret_cast<const uint32_t(*)[32]>(&pk[0]));
+      ptx::tmem_st_32x32b_x32(p_tmem + 32u, *reinterpret_cast<const uint32_t(*)[32]>(&pk[32]));
+      if (j > walk.j0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+        const uint32_t ob = (g - 1) & 1u;
+        if (!warp_wait(b.o_done + 8 * ob, ((g - 1) >> 1) & 1u, p, abort_flag)) {
+          ok = false;
+          break;
+        }
+        ptx::tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < HD / 32; ++c) {
+          uint32_t o[32];
+          const uint32_t ta = tmem_base + t_lane + O_COL + (uint32_t)c * 32u;
+          ptx::tmem_ld_32x32b_x32(ta, o);
+          ptx::tmem_ld_wait();
+          ptx::reg_fence(o);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+          ptx::tmem_st_32x32b_x32(ta, o);
+        }
+      }
+      ptx::tmem_st_wait();
+      signal_leader(rank, lane, b.p_full + 8 * pb, leader_p_full + 8 * pb, sig_p, sig_src);
+      l = l * alpha + lsum;
+      m = m_new;
+    }
+    if (!ok) break;
+    if (ki > 0 && !warp_wait(b.l_free, (ki - 1) & 1u, p, abort_flag)) break;
+    l_rows[row] = l;
+    l_rows[CQ + row] = m;
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(b.l_ready);
+    ++ki;
+  }
+}
+
+// ------------------------------------------------------------------ epilogue
+// Per tile, each warp its 32 rows: O out of tensor memory, through a box in
+// shared memory (128 bytes of each row) to whole 128-byte pieces of rows in
+// global memory: normalised binary16 rows of O, or, of a tile that is cut, the
+// unnormalised FP32 partial.
+__device__ __forceinline__ void epilogue_role(const Params& p, const Sched& sc, Walk& walk,
+                                              uint8_t* smem, uint32_t base, uint32_t tmem_base,
+                                              const Bars& b, const float* l_rows, uint32_t rank,
+                                              uint32_t warp, uint32_t lane, int cluster,
+                                              volatile int* abort_flag) {
+  const uint32_t quarter = warp & 3u;
+  const uint32_t t_lane = (quarter * 32u) << 16;
+  const uint32_t e = warp - (2 + SM_WARPS);
+  const uint32_t leader_o_free = ptx::map_to_cta(b.o_free, 0);
+  const uint32_t sig_o = ptx::map_to_cta(base + OFF_SIG + SIG_O + e * SIG_BYTES, 0);
+  const uint32_t sig_src = base + OFF_SIG + SIG_SRC + (SM_WARPS + e) * SIG_BYTES;
+  const uint32_t box = base + OFF_STAGE + e * BOX;
+  const uint4* box_rows = reinterpret_cast<const uint4*>(smem + OFF_STAGE + e * BOX);
+  const uint32_t lsw = lane & 7u;
+  const int cta_tokens = p.tile_tokens / 2;
+  uint32_t ki = 0, g_end = 0;
+  bool ok = true;
+  while (walk.next()) {
+    const int head = walk.cur_head;
+    const bool more = walk.more();
+    const bool whole = walk.j0 == 0 && walk.j1 == walk.s.nb;
+    const long long L = walk.line();
+    const int slot = part_slot(L, sc.per, cluster);
+    g_end += (uint32_t)(walk.j1 - walk.j0);
+    const uint32_t g_last = g_end - 1;
+    // Tokens of this CTA that exist; where its rows go.
+    const int tokens = imin(imax(walk.cnt - (int)rank * cta_tokens, 0), cta_tokens);
+    const int rows = imin(imax(tokens * p.group - (int)quarter * 32, 0), 32);
+    __half* const dst0 = p.O + (int64_t)(walk.r.start + walk.i0 + (int)rank * cta_tokens) * p.o_tok +
+                         (int64_t)(head * p.group) * p.o_head;
+    const int64_t part_row = (int64_t)slot * PART_ROWS + (int)rank * CQ + (int)quarter * 32;
+    ok = ok && __all_sync(0xffffffffu, wait_sleepy(b.l_ready, ki & 1u, p, abort_flag));
+    if (ok) {
+      const float l = l_rows[quarter * 32u + lane];
+      const float m = l_rows[CQ + quarter * 32u + lane];
+      __syncwarp();
+      if (more && lane == 0) ptx::mbar_arrive(b.l_free);
+      ok = warp_wait(b.o_done + 8 * (g_last & 1u), (g_last >> 1) & 1u, p, abort_flag);
+      ptx::tc_fence_after();
+      if (ok) {
+        const float inv_l = l > 0.f ? 1.f / l : 0.f;
+        if (!whole) __stcg(p.part_ml + part_row + lane, make_float2(m, l));
+#pragma unroll 1
+        for (int c = 0; c < HD / 32; ++c) {
+          uint32_t o[32];
+          ptx::tmem_ld_32x32b_x32(tmem_base + t_lane + O_COL + (uint32_t)c * 32u, o);
+          ptx::tmem_ld_wait();
+          ptx::reg_fence(o);
+          if (c == HD / 32 - 1 && more)
+            signal_leader(rank, lane, b.o_free, leader_o_free, sig_o, sig_src);
+          if (!whole) {
+#pragma unroll
+            for (uint32_t i = 0; i < 8; ++i)
+              ptx::st_shared_v4(box + lane * 128u + ((i ^ lsw) << 4), o[4 * i], o[4 * i + 1],
+                                o[4 * i + 2], o[4 * i + 3]);
+          } else {
+#pragma unroll
+            for (uint32_t i = 0; i < 4; ++i) {
+              const float* f = reinterpret_cast<const float*>(&o[8 * i]);
+              const uint32_t col = (uint32_t)(c & 1) * 4u + i;
+              ptx::st_shared_v4(box + lane * 128u + ((col ^ lsw) << 4),
+                                pack_half2(f[0] * inv_l, f[1] * inv_l),
+                                pack_half2(f[2] * inv_l, f[3] * inv_l),
+                                pack_half2(f[4] * inv_l, f[5] * inv_l),
+                                pack_half2(f[6] * inv_l, f[7] * inv_l));
+            }
+            if (!(c & 1)) continue;   // a box holds 64 binary16 numbers of a row
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = i * 4 + (int)(lane >> 3);
+            const uint4 v = box_rows[r * 8 + (int)((lane & 7u) ^ (uint32_t)(r & 7))];
+            if (r < rows) {
+              if (!whole) {
+                __stcg(reinterpret_cast<uint4*>(p.part + (part_row + r) * HD + c * 32) +
+                           (lane & 7u), v);
+              } else {
+                const int rr = (int)quarter * 32 + r, tok = rr / p.group;
+                *(reinterpret_cast<uint4*>(dst0 + tok * p.o_tok +
+                                           (int64_t)(rr - tok * p.group) * p.o_head +
+                                           (c >> 1) * 64) + (lane & 7u)) = v;
+              }
+            }
+          }
+          __syncwarp();
+        }
+      }
+    }
+    ++ki;
+    if (!whole) {
+      const int c0 = (int)(L / sc.per), c1 = (int)((L + walk.s.nb - 1) / sc.per);
+      const int first = part_slot(L, sc.per, c0);
+      int* counter = p.counters + first * COUNTERS + (int)rank * EP_WARPS + (int)quarter;
+      __threadfence();
+      __syncwarp();
+      int before = 0;
+      if (lane == 0) before = atomicAdd(counter, 1);
+      before = __shfl_sync(0xffffffffu, before, 0);
+      if (before != c1 - c0) continue;
+      if (lane == 0) *counter = 0;
+      __threadfence();
+      // Merge: lane k takes numbers 8k .. 8k+7 of each row.
+      const int64_t sub = (int64_t)rank * CQ + (int)quarter * 32;
+#pragma unroll 1
+      for (int r0 = 0; r0 < rows; r0 += 4) {
+        float mx[4], sum[4], acc[4][8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          mx[i] = NO_OFFSET;
+          sum[i] = 0.f;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) acc[i][k] = 0.f;
+        }
+        for (int c = c0; c <= c1; ++c) {
+          const int64_t pr = (int64_t)(c == c0 ? first : 2 * c) * PART_ROWS + sub + r0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mx[i] = fmaxf(mx[i], __ldcg(p.part_ml + pr + i).x);
+        }
+        for (int c = c0; c <= c1; ++c) {
+          const int64_t pr = (int64_t)(c == c0 ? first : 2 * c) * PART_ROWS + sub + r0;
+          float4 a[4], bb[4];
+          float2 ml[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4* src = reinterpret_cast<const float4*>(p.part + (pr + i) * HD) + lane * 2;
+            a[i] = __ldcg(src);
+            bb[i] = __ldcg(src + 1);
+            ml[i] = __ldcg(p.part_ml + pr + i);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float w = ptx::ex2_approx(ml[i].x - mx[i]);
+            sum[i] = fmaf(w, ml[i].y, sum[i]);
+            acc[i][0] = fmaf(w, a[i].x, acc[i][0]);
+            acc[i][1] = fmaf(w, a[i].y, acc[i][1]);
+            acc[i][2] = fmaf(w, a[i].z, acc[i][2]);
+            acc[i][3] = fmaf(w, a[i].w, acc[i][3]);
+            acc[i][4] = fmaf(w, bb[i].x, acc[i][4]);
+            acc[i][5] = fmaf(w, bb[i].y, acc[i][5]);
+            acc[i][6] = fmaf(w, bb[i].z, acc[i][6]);
+            acc[i][7] = fmaf(w, bb[i].w, acc[i][7]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (r0 + i >= rows) continue;
+          const float inv = sum[i] > 0.f ? 1.f / sum[i] : 0.f;
+          const int rr = (int)quarter * 32 + r0 + i, tok = rr / p.group;
+          uint4 out;
+          out.x = pack_half2(acc[i][0] * inv, acc[i][1] * inv);
+          out.y = pack_half2(acc[i][2] * inv, acc[i][3] * inv);
+          out.z = pack_half2(acc[i][4] * inv, acc[i][5] * inv);
+          out.w = pack_half2(acc[i][6] * inv, acc[i][7] * inv);
+          *(reinterpret_cast<uint4*>(dst0 + tok * p.o_tok +
+                                     (int64_t)(rr - tok * p.group) * p.o_head) + lane) = out;
+        }
+      }
+    }
+  }
+}
+
+// See attn_pair.cuh: completes every phase a producer opened and waits
+// (bounded) for the copies that were issued.
+__device__ __noinline__ void leader_drain(const Bars& b, Issued mine, Issued peer, uint32_t q_bytes,
+                                          uint64_t limit_ns) {
+  const uint32_t hi = mine.fills > peer.fills ? mine.fills : peer.fills;
+  const uint32_t lo = hi > (uint32_t)RING ? hi - (uint32_t)RING : 0u;
+  for (uint32_t f = lo; f < hi; ++f) {
+    const uint32_t bar = b.full + 8 * (f % RING);
+    if (f >= mine.fills) ptx::mbar_arrive_expect_tx_relaxed(bar, SLOT_BYTES);
+    if (f >= peer.fills) ptx::mbar_complete_tx(bar, SLOT_BYTES);
+    wait_drain(bar, (f / RING) & 1u, limit_ns);
+  }
+  const uint32_t qhi = mine.qloads > peer.qloads ? mine.qloads : peer.qloads;
+  if (qhi > 0) {
+    const uint32_t q = qhi - 1;
+    if (q >= mine.qloads) ptx::mbar_arrive_expect_tx_relaxed(b.q_full, q_bytes);
+    if (q >= peer.qloads) ptx::mbar_complete_tx(b.q_full, q_bytes);
+    wait_drain(b.q_full, q & 1u, limit_ns);
+  }
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
+    paged_large_kernel(const __grid_constant__ CUtensorMap tmQ,
+                       const __grid_constant__ CUtensorMap tmK,
+                       const __grid_constant__ CUtensorMap tmV, const Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ long long warp_sum[NUM_WARPS];
+  const uint32_t raw = ptx::smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (base - raw);
+  const uint32_t warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+  const uint32_t lane = threadIdx.x & 31u;
+  const uint32_t rank = ptx::cluster_ctarank();
+  const int cluster = (int)(blockIdx.x >> 1);
+  const int nclusters = (int)(gridDim.x >> 1);
+  float* l_rows = reinterpret_cast<float*>(smem + OFF_L);
+
+  Bars b;
+  b.q_full = base + OFF_BAR;
+  b.q_empty = b.q_full + 8;
+  b.full = b.q_empty + 8;
+  b.empty = b.full + 8 * RING;
+  b.s_full = b.empty + 8 * RING;
+  b.s_free = b.s_full + 8;
+  b.p_full = b.s_free + 8;
+  b.o_done = b.p_full + 16;
+  b.o_free = b.o_done + 16;
+  b.l_ready = b.o_free + 8;
+  b.l_free = b.l_ready + 8;
+  b.mma_done = b.l_free + 8;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_ABORT);
+
+  if (warp == 0 && lane == 0) {
+    ptx::prefetch_tmap(&tmQ);
+    ptx::prefetch_tmap(&tmK);
+    ptx::prefetch_tmap(&tmV);
+    ptx::mbar_init(b.q_full, 1);
+    ptx::mbar_init(b.q_empty, 1);
+    for (int s = 0; s < RING; ++s) {
+      ptx::mbar_init(b.full + 8 * s, 1);
+      ptx::mbar_init(b.empty + 8 * s, 1);
+    }
+    ptx::mbar_init(b.s_full, 1);
+    ptx::mbar_init(b.s_free, SM_WARPS);  // leader warps (+ the peer's bytes)
+    for (int k = 0; k < 2; ++k) {
+      ptx::mbar_init(b.p_full + 8 * k, SM_WARPS);
+      ptx::mbar_init(b.o_done + 8 * k, 1);
+    }
+    ptx::mbar_init(b.o_free, EP_WARPS);
+    ptx::mbar_init(b.l_ready, SM_WARPS);
+    ptx::mbar_init(b.l_free, EP_WARPS);
+    ptx::mbar_init(b.mma_done, 1);
+    *abort_flag = 0;
+    *reinterpret_cast<volatile uint32_t*>(smem + OFF_PEER_FILLS) = 0;
+    *reinterpret_cast<volatile uint32_t*>(smem + OFF_PEER_QLOADS) = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc_pair(base + OFF_TMEM_SLOT, TMEM_COLS);
+    ptx::tmem_relinquish_pair();
+  }
+  // Rows of Q past group * tokens are never copied: numbers whose results are dropped.
+  for (uint32_t i = threadIdx.x; i < Q_BYTES / 16; i += NUM_THREADS)
+    ptx::st_shared_v4(base + OFF_Q + 16 * i, 0, 0, 0, 0);
+  ptx::fence_proxy_async_smem();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  schedule(p, smem, cluster, nclusters, warp_sum);
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::cluster_sync();  // the peer's barriers exist before anyone signals them
+  ptx::tc_fence_after();
+  const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEM_SLOT);
+  const Sched sc = *reinterpret_cast<const Sched*>(smem + OFF_SCHED);
+  Walk walk(p, sc, reinterpret_cast<const int4*>(smem + OFF_REQ));
+
+  Issued issued{0, 0};
+  if (warp == 0) {
+    issued = producer_role(&tmQ, &tmK, &tmV, p, walk, base, b, rank, lane, cluster, abort_flag);
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      mma_role(p, walk, base, tmem_base, b, abort_flag);
+      ptx::mma_commit_pair(b.mma_done, 0x1);
+      wait_drain(b.mma_done, 0, p.timeout_ns);
+    }
+    __syncwarp();
+  } else if (warp < 2 + SM_WARPS) {
+    softmax_role(p, walk, base, tmem_base, b, l_rows, rank, warp, lane, abort_flag);
+  } else {
+    if (p.zero_rows)
+      zero_tail(p, (int)blockIdx.x * EP_WARPS + (int)warp - 2 - SM_WARPS, (int)gridDim.x * EP_WARPS);
+    epilogue_role(p, sc, walk, smem, base, tmem_base, b, l_rows, rank, warp, lane, cluster,
+                  abort_flag);
+  }
+
+  if (warp == 0 && lane == 0 && rank == 1) {
+    ptx::st_cluster_u32(ptx::map_to_cta(base + OFF_PEER_FILLS, 0), issued.fills);
+    ptx::st_cluster_u32(ptx::map_to_cta(base + OFF_PEER_QLOADS, 0), issued.qloads);
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::cluster_sync();  // both CTAs have stopped issuing
+  if (warp == 0 && lane == 0 && rank == 0) {
+    const Issued peer{*reinterpret_cast<volatile uint32_t*>(smem + OFF_PEER_FILLS),
+                      *reinterpret_cast<volatile uint32_t*>(smem + OFF_PEER_QLOADS)};
+    leader_drain(b, issued, peer, 4u * 128u * (uint32_t)(p.tile_tokens / 2 * p.group),
+                 p.timeout_ns);
+  }
+  ptx::cluster_sync();  // no copy into either CTA is still in flight
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc_pair(tmem_base, TMEM_COLS);
+  }
+}
+
+}  // namespace large
+}  // namespace paged
+}  // namespace gf16

@@ -52,8 +52,9 @@ struct Params {
   int64_t o_tok, o_head;
   float scale_log2;
   Masks masks;
-  int tile_tokens;                // tokens of a request that a tile (small: a request) can hold
-  int min_rows;                   // large kernel: requests with at most this many rows are not its own
+  int tile_tokens;                // tokens that a tile (small kernel: a request) can hold
+  int skip_tokens;                // large kernel: requests with at most this many are not its own
+  int zero_rows;                  // whether this launch writes the rows past the last request's
   float* part;                    // partial O, FP32 [slot][row][256]
   float2* part_ml;                // their offsets and sums [slot][row]
   int* counters;
@@ -553,7 +554,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                            (uint32_t)(key_row & 7) * 2u;
     const uint32_t p_col = (uint32_t)(key_row & 63) >> 3;   // 16-byte column, swizzled by row
     const float sl2 = p.scale_log2;
-    zero_tail(p, cta * SM_WARPS + (int)quarter, ctas * SM_WARPS);
+    if (p.zero_rows) zero_tail(p, cta * SM_WARPS + (int)quarter, ctas * SM_WARPS);
     uint32_t g = 0;
     bool ok = true;
     while (walk.next()) {

@@ -569,3 +569,46 @@ def test_step_in_a_graph(g, plan):
         assert ((o.double() - want).norm() <= 2e-3 * want.norm())
         lens = [a + b for a, b in zip(lens, new)]
         head.copy_(m.free_head)
+
+
+@pytest.mark.parametrize("lens", [[(500, 1), (900, 1)], [(500, 3), (900, 700)], [(500, 400)]],
+                         ids=["few", "both", "many"])
+def test_attention_bounded_wait(g, lens):
+    """The first copy of worker 0 is left out (the test-only fault option):
+    the call must end with ERR_TIMEOUT, and the next ones, which find the
+    tile counters where the failed call left them, must be right."""
+    pr = ref.PagedProblem(lens, 8, 2, 16, seed=13)
+    with g.Plan(0) as own:
+        run_attention(g, own, pr)
+        done(own)
+        own.set_option(g.OPT_TIMEOUT_NS, 20_000_000)
+        for unit in (0, 1):
+            own.set_option(g.OPT_FAULT_UNIT, unit)
+            run_attention(g, own, pr)
+            done(own, g.ERR_TIMEOUT)
+        own.set_option(g.OPT_FAULT_UNIT, -1)
+        for _ in range(2):
+            o = run_attention(g, own, pr)
+            done(own)
+            check(o, pr)
+
+
+@pytest.mark.parametrize("limit", [1, 2, 7, 40])
+def test_attention_sm_limit(g, limit):
+    """Fewer workers: other cuts of the same tiles."""
+    with g.Plan(0) as own:
+        own.set_option(g.OPT_SM_LIMIT, limit)
+        for lens in ([(300, 1), (0, 1), (700, 1)], [(100, 200), (5, 1), (600, 60)]):
+            pr = ref.PagedProblem(lens, 8, 2, 16, seed=14)
+            o = run_attention(g, own, pr)
+            done(own)
+            check(o, pr)
+
+
+def test_attention_many_requests(g, plan):
+    """More requests than the kernels keep in shared memory, empty ones among them."""
+    for most in (1, 90):
+        pr = ref.PagedProblem(ragged(15, 700, 90, most, 0.6), 2, 1, 8, seed=15)
+        o = run_attention(g, plan, pr)
+        done(plan)
+        check(o, pr)
