@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import collections
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -158,6 +159,8 @@ class GemmError(RuntimeError):
 def load() -> ctypes.CDLL:
     """Load the in-tree library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -513,7 +516,10 @@ def attn_f16_paged_maps_validate(*args) -> int:
     return load().attn_f16_paged_maps_validate(*args)
 
 
+@functools.lru_cache(maxsize=1024)
 def _i64s(values):
+    """A tuple of strides as the C array that the library reads (and never
+    writes): the same tuples come back every step."""
     return None if values is None else (_c_i64 * len(values))(*[int(x) for x in values])
 
 
@@ -578,13 +584,24 @@ def attn_f16_paged_validate(batch, total_q, max_q, q_heads, kv_heads, head_dim, 
 
 def _need(X, name: str, dtype, dims: int, plan: Plan):
     """A torch tensor of this type and rank on the plan's device, its last
-    dimension contiguous."""
-    if X.dtype != dtype or X.dim() != dims:
+    dimension contiguous.  Returns its strides."""
+    if X.dtype is not dtype or X.dim() != dims:
         raise ValueError(f"{name} must be a {dims}-dimensional {dtype} tensor")
-    if not X.is_cuda or X.device.index != plan.device:
+    if X.get_device() != plan.device:
         raise ValueError(f"{name} must be on the plan's device")
-    if X.stride(-1) != 1 and X.shape[-1] > 1:
+    st = X.stride()
+    if st[-1] != 1 and X.shape[-1] > 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
+    return st
+
+
+def _plan_stream(plan: Plan, stream) -> int:
+    """The handle of `stream`, by default torch's current one on the plan's device."""
+    if stream is not None:
+        return _stream_handle(stream)
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # without a Stream object
+    return raw(plan.device) if raw else int(torch.cuda.current_stream(plan.device).cuda_stream)
 
 
 PagedMaps = collections.namedtuple("PagedMaps", "starts kv_lens positions slots free_head")
@@ -606,16 +623,18 @@ def paged_maps(plan: Plan, cached, added, block_table, free_pages, free_head, pa
     """
     import torch
     i32 = torch.int32
-    for name, X, dims in (("cached", cached, 1), ("added", added, 1),
-                          ("block_table", block_table, 2), ("free_pages", free_pages, 1),
-                          ("free_head", free_head, 1)):
-        _need(X, name, i32, dims, plan)
+    _need(cached, "cached", i32, 1, plan)
+    _need(added, "added", i32, 1, plan)
+    table_st = _need(block_table, "block_table", i32, 2, plan)
+    _need(free_pages, "free_pages", i32, 1, plan)
+    _need(free_head, "free_head", i32, 1, plan)
     batch = cached.shape[0]
-    if added.shape[0] != batch or block_table.shape[0] != batch or free_head.shape[0] != 1:
+    rows, max_pages = block_table.shape
+    if added.shape[0] != batch or rows != batch or free_head.shape[0] != 1:
         raise ValueError("shape mismatch: cached [B], added [B], block_table [B, P], free_head [1]")
     if out is None:
-        room = (max(max_tokens, 0) + 3) // 4 * 4
-        buf = torch.empty(2 * room + 2 * batch + 2, dtype=i32, device=cached.device)
+        room = (max(max_tokens, 0) + 3) // 4 * 4    # 16-byte pieces
+        buf = cached.new_empty(2 * room + 2 * batch + 2)
         positions, slots, starts, kv_lens, head = buf.split_with_sizes(
             (room, room, batch + 1, batch, 1))
         if room != max_tokens:
@@ -629,12 +648,11 @@ def paged_maps(plan: Plan, cached, added, block_table, free_pages, free_head, pa
             if X.shape[0] != n:
                 raise ValueError(f"out.{name} must have {n} entries")
     attn_f16_paged_maps(plan.handle, batch, cached.data_ptr(), added.data_ptr(),
-                        block_table.data_ptr(),
-                        block_table.stride(0) if batch > 1 else block_table.shape[1],
-                        block_table.shape[1], free_pages.data_ptr(), free_pages.shape[0],
+                        block_table.data_ptr(), table_st[0] if batch > 1 else max_pages,
+                        max_pages, free_pages.data_ptr(), free_pages.shape[0],
                         free_head.data_ptr(), page_size, max_tokens, out.starts.data_ptr(),
                         out.kv_lens.data_ptr(), out.positions.data_ptr(), out.slots.data_ptr(),
-                        out.free_head.data_ptr(), _stream_handle(stream))
+                        out.free_head.data_ptr(), _plan_stream(plan, stream))
     return out
 
 
@@ -694,24 +712,37 @@ def _rope_layout(layout: str) -> int:
     raise ValueError("layout is 'half' or 'interleaved'")
 
 
-def _token_heads(X, name: str, plan: Plan, tokens=None):
-    import torch
-    _need(X, name, torch.float16, 3, plan)
-    if X.shape[2] != ATTN_HEAD_DIM or (tokens is not None and X.shape[0] != tokens):
+def _token_heads(X, name: str, plan: Plan, f16, tokens=None):
+    """[tokens, heads, 256] binary16; returns the (token, head) strides."""
+    st = _need(X, name, f16, 3, plan)
+    shape = X.shape
+    if shape[2] != ATTN_HEAD_DIM or (tokens is not None and shape[0] != tokens):
         raise ValueError(f"{name} must be [tokens, heads, {ATTN_HEAD_DIM}]")
+    return st[:2]
 
 
-def _cache_pair(K_cache, V_cache, plan: Plan):
-    import torch
-    _need(K_cache, "K_cache", torch.float16, 4, plan)
-    _need(V_cache, "V_cache", torch.float16, 4, plan)
+def _cache_pair(K_cache, V_cache, plan: Plan, f16):
+    """[pages, page_size, kv_heads, 256] binary16 each; their (page, row, head) strides."""
+    k_st = _need(K_cache, "K_cache", f16, 4, plan)
+    v_st = _need(V_cache, "V_cache", f16, 4, plan)
     if K_cache.shape != V_cache.shape or K_cache.shape[3] != ATTN_HEAD_DIM:
         raise ValueError(f"K_cache and V_cache must be [pages, page_size, kv_heads, "
                          f"{ATTN_HEAD_DIM}]")
+    return k_st[:3], v_st[:3]
 
 
-def _rope_common(positions, turns, tokens, plan):
-    import torch
+def _output(X, out, name: str, plan: Plan, f16):
+    """`out`, or a new tensor of X's shape; and its (token, head) strides."""
+    if out is None:
+        shape = X.shape
+        return X.new_empty(shape), (shape[1] * ATTN_HEAD_DIM or ATTN_HEAD_DIM, ATTN_HEAD_DIM)
+    st = _token_heads(out, "out", plan, f16)
+    if out.shape != X.shape:
+        raise ValueError(f"out must have the shape of {name}")
+    return out, st
+
+
+def _rope_common(positions, turns, tokens, plan, torch):
     _need(positions, "positions", torch.int32, 1, plan)
     _need(turns, "turns", torch.int64, 1, plan)
     if positions.shape[0] != tokens:
@@ -729,18 +760,14 @@ def rotary(plan: Plan, X, positions, turns, out=None, layout: str = "half", fact
     of X.  ``out`` may be X.
     """
     import torch
-    _token_heads(X, "X", plan)
-    _rope_common(positions, turns, X.shape[0], plan)
-    if out is None:
-        out = torch.empty(X.shape, dtype=X.dtype, device=X.device)
-    else:
-        _token_heads(out, "out", plan)
-        if out.shape != X.shape:
-            raise ValueError("out must have the shape of X")
-    attn_f16_rope(plan.handle, X.shape[0], X.shape[1], 0, X.shape[2], 2 * turns.shape[0],
-                  _rope_layout(layout), int(inverse), factor, turns.data_ptr(),
-                  positions.data_ptr(), X.data_ptr(), X.stride()[:2], out.data_ptr(),
-                  out.stride()[:2], stream=_stream_handle(stream))
+    f16 = torch.float16
+    x_st = _token_heads(X, "X", plan, f16)
+    tokens, heads, dim = X.shape
+    _rope_common(positions, turns, tokens, plan, torch)
+    out, o_st = _output(X, out, "X", plan, f16)
+    attn_f16_rope(plan.handle, tokens, heads, 0, dim, 2 * turns.shape[0], _rope_layout(layout),
+                  int(inverse), factor, turns.data_ptr(), positions.data_ptr(), X.data_ptr(), x_st,
+                  out.data_ptr(), o_st, stream=_plan_stream(plan, stream))
     return out
 
 
@@ -756,30 +783,25 @@ def rotary_to_cache(plan: Plan, Q, K, V, positions, slots, turns, K_cache, V_cac
     nothing is written).  Returns the rotated Q (in ``out``, which may be Q).
     """
     import torch
-    _token_heads(Q, "Q", plan)
-    tokens = Q.shape[0]
-    _token_heads(K, "K", plan, tokens)
-    _token_heads(V, "V", plan, tokens)
-    _cache_pair(K_cache, V_cache, plan)
-    if K.shape != V.shape or K.shape[1] != K_cache.shape[2]:
+    f16 = torch.float16
+    q_st = _token_heads(Q, "Q", plan, f16)
+    tokens, heads, dim = Q.shape
+    k_st = _token_heads(K, "K", plan, f16, tokens)
+    v_st = _token_heads(V, "V", plan, f16, tokens)
+    kc_st, vc_st = _cache_pair(K_cache, V_cache, plan, f16)
+    pages, page_size, kv_heads, _ = K_cache.shape
+    if K.shape != V.shape or K.shape[1] != kv_heads:
         raise ValueError("K, V and the caches must have the same heads")
-    _rope_common(positions, turns, tokens, plan)
+    _rope_common(positions, turns, tokens, plan, torch)
     _need(slots, "slots", torch.int32, 1, plan)
     if slots.shape[0] != tokens:
         raise ValueError("slots must have one entry per token")
-    if out is None:
-        out = torch.empty(Q.shape, dtype=Q.dtype, device=Q.device)
-    else:
-        _token_heads(out, "out", plan)
-        if out.shape != Q.shape:
-            raise ValueError("out must have the shape of Q")
-    attn_f16_rope(plan.handle, tokens, Q.shape[1], K.shape[1], Q.shape[2], 2 * turns.shape[0],
+    out, o_st = _output(Q, out, "Q", plan, f16)
+    attn_f16_rope(plan.handle, tokens, heads, kv_heads, dim, 2 * turns.shape[0],
                   _rope_layout(layout), 0, factor, turns.data_ptr(), positions.data_ptr(),
-                  Q.data_ptr(), Q.stride()[:2], out.data_ptr(), out.stride()[:2], K.data_ptr(),
-                  K.stride()[:2], V.data_ptr(), V.stride()[:2], slots.data_ptr(),
-                  K_cache.data_ptr(), K_cache.stride()[:3], V_cache.data_ptr(),
-                  V_cache.stride()[:3], K_cache.shape[0], K_cache.shape[1],
-                  _stream_handle(stream))
+                  Q.data_ptr(), q_st, out.data_ptr(), o_st, K.data_ptr(), k_st, V.data_ptr(), v_st,
+                  slots.data_ptr(), K_cache.data_ptr(), kc_st, V_cache.data_ptr(), vc_st, pages,
+                  page_size, _plan_stream(plan, stream))
     return out
 
 
@@ -800,28 +822,23 @@ def paged_attention(plan: Plan, Q, K_cache, V_cache, block_table, starts, kv_len
     request's, are 0.
     """
     import torch
-    _token_heads(Q, "Q", plan)
-    _cache_pair(K_cache, V_cache, plan)
-    _need(block_table, "block_table", torch.int32, 2, plan)
-    _need(starts, "starts", torch.int32, 1, plan)
-    _need(kv_lens, "kv_lens", torch.int32, 1, plan)
+    f16, i32 = torch.float16, torch.int32
+    q_st = _token_heads(Q, "Q", plan, f16)
+    kc_st, vc_st = _cache_pair(K_cache, V_cache, plan, f16)
+    table_st = _need(block_table, "block_table", i32, 2, plan)
+    _need(starts, "starts", i32, 1, plan)
+    _need(kv_lens, "kv_lens", i32, 1, plan)
     batch = kv_lens.shape[0]
-    if starts.shape[0] != batch + 1 or block_table.shape[0] != batch:
+    rows, max_pages = block_table.shape
+    if starts.shape[0] != batch + 1 or rows != batch:
         raise ValueError("shape mismatch: block_table [B, P], starts [B + 1], kv_lens [B]")
-    if out is None:
-        out = torch.empty(Q.shape, dtype=Q.dtype, device=Q.device)
-    else:
-        _token_heads(out, "out", plan)
-        if out.shape != Q.shape:
-            raise ValueError("out must have the shape of Q")
-    if scale is None:
-        scale = 1.0 / math.sqrt(ATTN_HEAD_DIM)
-    attn_f16_paged_fwd(plan.handle, batch, Q.shape[0], max_q, Q.shape[1], K_cache.shape[2],
-                       Q.shape[2], Q.data_ptr(), Q.stride()[:2], K_cache.data_ptr(),
-                       K_cache.stride()[:3], V_cache.data_ptr(), V_cache.stride()[:3],
-                       K_cache.shape[0], K_cache.shape[1], block_table.data_ptr(),
-                       block_table.stride(0) if batch > 1 else block_table.shape[1],
-                       block_table.shape[1], starts.data_ptr(), kv_lens.data_ptr(),
-                       out.data_ptr(), out.stride()[:2], scale, window, sinks,
-                       _stream_handle(stream))
+    out, o_st = _output(Q, out, "Q", plan, f16)
+    tokens, heads, dim = Q.shape
+    pages, page_size, kv_heads, _ = K_cache.shape
+    attn_f16_paged_fwd(plan.handle, batch, tokens, max_q, heads, kv_heads, dim, Q.data_ptr(), q_st,
+                       K_cache.data_ptr(), kc_st, V_cache.data_ptr(), vc_st, pages, page_size,
+                       block_table.data_ptr(), table_st[0] if batch > 1 else max_pages, max_pages,
+                       starts.data_ptr(), kv_lens.data_ptr(), out.data_ptr(), o_st,
+                       ATTN_HEAD_DIM ** -0.5 if scale is None else scale, window, sinks,
+                       _plan_stream(plan, stream))
     return out

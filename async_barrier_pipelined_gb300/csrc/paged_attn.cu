@@ -79,7 +79,8 @@ int ensure_workspace(gemm_f16_plan_s* p, cudaStream_t stream, paged::Params* prm
   const size_t small_slots = 2 * (size_t)p->num_sms, large_slots = 2 * (size_t)p->paged_pairs;
   const size_t rows = std::max(small_slots * SMALL_ROWS, large_slots * paged::large::PART_ROWS);
   const size_t counters =
-      (std::max(small_slots, large_slots * paged::large::COUNTERS) * sizeof(int) + 255) / 256 * 256;
+      (std::max(small_slots * paged::small::MAX_GROUPS, large_slots * paged::large::COUNTERS) *
+           sizeof(int) + 255) / 256 * 256;
   const size_t ml = rows * sizeof(float2);
   const size_t bytes = counters + ml + rows * HEAD_DIM * sizeof(float);
   if (p->paged_ws_bytes < bytes) {
@@ -276,12 +277,14 @@ int attn_f16_paged_fwd(gemm_f16_plan_t p, int batch, int total_q, int max_q, int
   const int64_t rows = (int64_t)max_q * prm.group;
   // Requests of up to SMALL_ROWS rows (new tokens x group) are bound by
   // reading the cache and go to the small kernel, with room for the rows
-  // that the step's largest has (16, 32 or 64).  The others go to the large
-  // one; a step of one request that may be large launches that alone, which
-  // takes a request of any size.
+  // that the step's largest has (16, 32 or 64).  Where some may be larger,
+  // the small kernel takes those that fit the narrowest form a single token
+  // fits, and the large one the others; a step of one request that may be
+  // large launches that alone, which takes a request of any size.
   const bool any_large = rows > SMALL_ROWS, any_small = !any_large || batch > 1;
   if (any_small) {
-    const int n = rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
+    const int64_t fit = any_large ? prm.group : rows;
+    const int n = fit <= 16 ? 16 : (fit <= 32 ? 32 : 64);
     prm.rows = std::min(page_rows, paged::BLOCK_KEYS);
     prm.tile_tokens = n / prm.group;
     prm.zero_rows = 1;
@@ -293,8 +296,9 @@ int attn_f16_paged_fwd(gemm_f16_plan_t p, int batch, int total_q, int max_q, int
     using namespace paged::small;
     const Kernel kernel = n == 16 ? paged_small_kernel<16>
                                   : (n == 32 ? paged_small_kernel<32> : paged_small_kernel<64>);
+    const int threads = n == 16 ? Cfg<16>::THREADS : (n == 32 ? Cfg<32>::THREADS : Cfg<64>::THREADS);
     const size_t smem = n == 16 ? Cfg<16>::SMEM : (n == 32 ? Cfg<32>::SMEM : Cfg<64>::SMEM);
-    if ((rc = launch(p, kernel, "launch paged_small_kernel", ctas, NUM_THREADS, smem, st, tmQ, tmK,
+    if ((rc = launch(p, kernel, "launch paged_small_kernel", ctas, threads, smem, st, tmQ, tmK,
                      tmV, prm)))
       return rc;
     prm.skip_tokens = prm.tile_tokens;

@@ -14,9 +14,11 @@
 // share of the memory rate; the MMAs of a block take ~0.55 us.
 //
 // One CTA per SM; the step's key blocks are dealt out evenly (paged_schedule.h),
-// whatever the lengths.  192 threads: warp 0 copies (lanes take the pages of
-// a block side by side), one lane of warp 1 issues the MMAs, warps 2..5 are
-// the softmax, one key per thread.  Per block the threads only agree on
+// whatever the lengths.  Warp 0 copies (lanes take the pages of a block side
+// by side), one lane of warp 1 issues the MMAs, and each 16 rows of the tile
+// have four softmax warps, one key per thread, that share nothing with the
+// others (a thread that held all 64 rows of the widest tile spilled its
+// registers and took 13 us for a block).  Per block the threads only agree on
 // whether some score passed the exponent offset in use by more than
 // RESCALE_LOG2 (one barrier with an OR); only then do they take the block's
 // maximum, move the offset and rescale O.  Row sums stay one per thread and
@@ -138,14 +140,17 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, uint
 
 namespace small {
 
-constexpr int NUM_THREADS = 192;
-constexpr int SM_WARPS = 4;
-constexpr int WIN = NUM_THREADS;        // requests kept in shared memory
+constexpr int WIN = 192;                // requests kept in shared memory
+constexpr int MAX_GROUPS = 4;           // softmax groups, and counters per partial slot
+constexpr int COLS = 16;                // rows of the tile (columns of S^T) per softmax group
 constexpr uint32_t CHUNK = 128 * 128;   // 128 keys x 64 numbers: 16 KB
 constexpr uint32_t SLOT = 2 * CHUNK;
 
 template <int N>
 struct Cfg {
+  static constexpr int GROUPS = N / COLS;                 // softmax groups of four warps
+  static constexpr int THREADS = 64 + 128 * GROUPS;
+  static constexpr int WARPS = THREADS / 32;
   static constexpr int RING = N == 16 ? 6 : (N == 32 ? 5 : 4);
   static constexpr uint32_t Q_CHUNK = N * 128;
   static constexpr uint32_t Q_BYTES = 4 * Q_CHUNK;
@@ -155,7 +160,7 @@ struct Cfg {
   static constexpr uint32_t OFF_Q = OFF_RING + RING * SLOT;
   static constexpr uint32_t OFF_P = OFF_Q + Q_BYTES;
   static constexpr uint32_t OFF_RED = OFF_P + 2 * P_BYTES;          // [4][N] floats
-  static constexpr uint32_t OFF_REQ = OFF_RED + SM_WARPS * N * 4;   // WIN x (start, n, len)
+  static constexpr uint32_t OFF_REQ = OFF_RED + 4 * N * 4;          // WIN x (start, n, len)
   static constexpr uint32_t OFF_SCHED = OFF_REQ + WIN * 12;         // see Sched
   static constexpr uint32_t OFF_BAR = (OFF_SCHED + 64 + 7) / 8 * 8;
   static constexpr uint32_t NUM_BARS = 2 + 2 * RING + 6 + 1;
@@ -164,7 +169,7 @@ struct Cfg {
   static_assert(SMEM <= 232448, "over the 227 KB shared-memory limit per CTA");
   // Tensor memory: two S buffers, then O (two halves of 128 numbers).
   static constexpr uint32_t S_COL = 0, O_COL = 2 * N;
-  static constexpr uint32_t COLS = N == 64 ? 256 : (N == 32 ? 128 : 64);
+  static constexpr uint32_t TMEM_COLS = N == 64 ? 256 : (N == 32 ? 128 : 64);
   // kind::f16, FP32 accumulate, M = 128: S^T with both operands K-major;
   // O^T with A (V^T) MN-major (bit 15) and B (P) K-major.
   static constexpr uint32_t IDESC_S = (1u << 4) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
@@ -177,59 +182,44 @@ struct Sched {
   int base;                 // first request in shared memory
 };
 
-template <int N>
-__device__ __forceinline__ void tmem_ld_n(uint32_t taddr, uint32_t (&r)[N]) {
-  if constexpr (N == 16) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr)
-        : "memory");
-  } else {
-#pragma unroll
-    for (int c = 0; c < N / 32; ++c)
-      ptx::tmem_ld_32x32b_x32(taddr + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&r[32 * c]));
-  }
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[COLS]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
   ptx::tmem_ld_wait();
   ptx::reg_fence(r);
 }
 
-template <int N>
-__device__ __forceinline__ void tmem_st_n(uint32_t taddr, const uint32_t (&r)[N]) {
-  if constexpr (N == 16) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-        "r"(r[15])
-        : "memory");
-  } else {
-#pragma unroll
-    for (int c = 0; c < N / 32; ++c)
-      ptx::tmem_st_32x32b_x32(taddr + 32 * c,
-                              *reinterpret_cast<const uint32_t(*)[32]>(&r[32 * c]));
-  }
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[COLS]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
 }
 
-// Barrier of the 128 softmax threads; returns the OR of `pred`.
-__device__ __forceinline__ bool softmax_or(bool pred) {
+// Barrier of the 128 threads of a softmax group (named barrier 1 + group);
+// the first returns the OR of `pred`.
+__device__ __forceinline__ bool group_or(int grp, bool pred) {
   int r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.s32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
+      "barrier.cta.red.or.pred q, %2, 128, p;\n\t"
       "selp.s32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"((int)pred)
+      : "r"((int)pred), "r"(1 + grp)
       : "memory");
   return r != 0;
 }
-__device__ __forceinline__ void softmax_sync() {
-  asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
+__device__ __forceinline__ void group_sync(int grp) {
+  asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + grp) : "memory");
 }
 
 // Warp maximum of floats (no NaN needed): as ordered integers.
@@ -298,7 +288,7 @@ __device__ __forceinline__ void schedule(const Params& p, uint8_t* smem, int cta
   using C = Cfg<N>;
   int* req = reinterpret_cast<int*>(smem + C::OFF_REQ);
   Sched* sc = reinterpret_cast<Sched*>(smem + C::OFF_SCHED);
-  __shared__ long long warp_sum[NUM_THREADS / 32];
+  __shared__ long long warp_sum[C::WARPS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // First pass: all blocks of the step.  The second finds the request that
   // holds the CTA's first block; a step of up to WIN requests needs one.
@@ -306,7 +296,7 @@ __device__ __forceinline__ void schedule(const Params& p, uint8_t* smem, int cta
   long long total = 0;
   if (!one) {
     long long sum = 0;
-    for (int b = tid; b < p.batch; b += NUM_THREADS) {
+    for (int b = tid; b < p.batch; b += C::THREADS) {
       const Request r = load_request(p, b);
       if (r.bad) *(volatile int*)p.status = (int)GEMM_F16_ERR_BAD_INDEX;
       sum += (long long)request_blocks(p, r) * p.kv_heads;
@@ -315,7 +305,7 @@ __device__ __forceinline__ void schedule(const Params& p, uint8_t* smem, int cta
     for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
     if (lane == 0) warp_sum[warp] = sum;
     __syncthreads();
-    for (int k = 0; k < NUM_THREADS / 32; ++k) total += warp_sum[k];
+    for (int k = 0; k < C::WARPS; ++k) total += warp_sum[k];
     __syncthreads();
   }
   if (tid == 0) {
@@ -326,11 +316,13 @@ __device__ __forceinline__ void schedule(const Params& p, uint8_t* smem, int cta
   for (int b0 = 0; b0 < p.batch; b0 += WIN) {
     const int b = b0 + tid;
     Request r{0, 0, 0, false};
-    if (b < p.batch) r = load_request(p, b);
-    if (one && r.bad) *(volatile int*)p.status = (int)GEMM_F16_ERR_BAD_INDEX;
-    req[3 * tid] = r.start;
-    req[3 * tid + 1] = r.n;
-    req[3 * tid + 2] = r.len;
+    if (tid < WIN) {
+      if (b < p.batch) r = load_request(p, b);
+      if (one && r.bad) *(volatile int*)p.status = (int)GEMM_F16_ERR_BAD_INDEX;
+      req[3 * tid] = r.start;
+      req[3 * tid + 1] = r.n;
+      req[3 * tid + 2] = r.len;
+    }
     const int nb = request_blocks(p, r);
     const long long mine = (long long)nb * p.kv_heads;
     long long inc = mine;
@@ -342,7 +334,7 @@ __device__ __forceinline__ void schedule(const Params& p, uint8_t* smem, int cta
     if (lane == 31) warp_sum[warp] = inc;
     __syncthreads();
     long long all = 0, base = before;
-    for (int k = 0; k < NUM_THREADS / 32; ++k) {
+    for (int k = 0; k < C::WARPS; ++k) {
       if (k < warp) base += warp_sum[k];
       all += warp_sum[k];
     }
@@ -367,7 +359,7 @@ __device__ __forceinline__ void schedule(const Params& p, uint8_t* smem, int cta
 }
 
 template <int N>
-__global__ void __launch_bounds__(NUM_THREADS, 1)
+__global__ void __launch_bounds__(Cfg<N>::THREADS, 1)
     paged_small_kernel(const __grid_constant__ CUtensorMap tmQ,
                        const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const Params p) {
@@ -384,7 +376,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                  empty = full + 8 * C::RING, s_full = empty + 8 * C::RING, p_full = s_full + 16,
                  o_done = p_full + 16, mma_done = o_done + 16;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_TMEM + 4);
-  int* const last_flag = reinterpret_cast<int*>(smem + C::OFF_TMEM + 8);
 
   if (threadIdx.x == 0) {
     ptx::prefetch_tmap(&tmQ);
@@ -398,7 +389,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
     for (int k = 0; k < 2; ++k) {
       ptx::mbar_init(s_full + 8 * k, 1);
-      ptx::mbar_init(p_full + 8 * k, SM_WARPS);
+      ptx::mbar_init(p_full + 8 * k, 4 * C::GROUPS);
       ptx::mbar_init(o_done + 8 * k, 1);
     }
     ptx::mbar_init(mma_done, 1);
@@ -406,11 +397,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     ptx::fence_mbar_init();
   }
   if (warp == 1) {
-    ptx::tmem_alloc(base + C::OFF_TMEM, C::COLS);
+    ptx::tmem_alloc(base + C::OFF_TMEM, C::TMEM_COLS);
     ptx::tmem_relinquish();
   }
   // Rows of Q that no copy fills must be numbers (their results are dropped).
-  for (uint32_t i = threadIdx.x; i < C::Q_BYTES / 16; i += NUM_THREADS)
+  for (uint32_t i = threadIdx.x; i < C::Q_BYTES / 16; i += C::THREADS)
     ptx::st_shared_v4(base + C::OFF_Q + 16 * i, 0, 0, 0, 0);
   ptx::fence_proxy_async_smem();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -546,24 +537,28 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     __syncwarp();
   } else {
     // ---------------------------------------------------------------- softmax
+    // Group grp works on rows col0 .. col0 + 15 of the tile; its threads'
+    // keys are rows of S^T.
     const uint32_t quarter = warp & 3u;
-    const uint32_t t_lane = (quarter * 32u) << 16;
+    const int grp = (int)(warp - 2) >> 2, col0 = grp * COLS;
+    const uint32_t t_lane = ((quarter * 32u) << 16) + (uint32_t)col0;
     const int key_row = (int)(quarter * 32u + lane);
-    float* red = reinterpret_cast<float*>(smem + C::OFF_RED);
+    float* red = reinterpret_cast<float*>(smem + C::OFF_RED) + 4 * col0;    // [4][COLS]
     const uint32_t p_off = base + C::OFF_P + (uint32_t)(key_row >> 6) * C::P_CHUNK +
-                           (uint32_t)(key_row & 7) * 2u;
+                           (uint32_t)col0 * 128u + (uint32_t)(key_row & 7) * 2u;
     const uint32_t p_col = (uint32_t)(key_row & 63) >> 3;   // 16-byte column, swizzled by row
     const float sl2 = p.scale_log2;
-    if (p.zero_rows) zero_tail(p, cta * SM_WARPS + (int)quarter, ctas * SM_WARPS);
+    if (p.zero_rows)
+      zero_tail(p, cta * 4 * C::GROUPS + (int)warp - 2, ctas * 4 * C::GROUPS);
     uint32_t g = 0;
     bool ok = true;
     while (walk.next()) {
       const int head = walk.head - 1;
-      const int rows = walk.r.n * p.group;
+      const int rows = imin(imax(walk.r.n * p.group - col0, 0), COLS);   // of this group
       const int pos0 = walk.r.len - walk.r.n;               // position of the first new token
-      float m[N], l[N];
+      float m[COLS], l[COLS];
 #pragma unroll
-      for (int n = 0; n < N; ++n) {
+      for (int n = 0; n < COLS; ++n) {
         m[n] = NO_OFFSET;
         l[n] = 0.f;
       }
@@ -571,115 +566,122 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const uint32_t sb = g & 1u;
         const int blk = span_block(walk.s, j);
         const bool full_block = block_is_full(pos0, pos0 + walk.r.n - 1, blk, p.masks);
-        // Row n is new token n / group: the first that sees this thread's key
-        // is row lo; of those in the window, hi is one past the last.
         int lo = 0, hi = N;
         if (!full_block)
           rows_that_see(walk.s, blk, key_row, p.rows, pos0, p.group, p.masks, N, &lo, &hi);
+        lo -= col0;
+        hi -= col0;
         const bool got = wait_phase(s_full + 8 * sb, (g >> 1) & 1u, p, abort_flag);
         // The four warps go on or stop together: the barriers below need all.
-        if (softmax_or(!(ok && got))) {
+        if (group_or(grp, !(ok && got))) {
           ok = false;
           break;
         }
         ptx::tc_fence_after();
-        uint32_t s[N];
-        tmem_ld_n<N>(tmem + t_lane + C::S_COL + sb * N, s);
-        bool over = false;
+        if (rows > 0) {
+          uint32_t s[COLS];
+          tmem_ld(tmem + t_lane + C::S_COL + sb * N, s);
+          bool over = false;
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-          float x = __uint_as_float(s[n]) * sl2;
-          if (!full_block) x = (n >= lo && n < hi) ? x : -INFINITY;
-          s[n] = __float_as_uint(x);
-          over |= x > m[n] + RESCALE_LOG2;
-        }
-        // P buffer sb was last read by the O products of block g - 2.
-        if (g >= 2 && !__all_sync(0xffffffffu, wait_phase(o_done + 8 * sb, ((g - 2) >> 1) & 1u, p,
-                                                         abort_flag)))
-          ok = false;
-        if (softmax_or(over)) {
-#pragma unroll
-          for (int n = 0; n < N; ++n) {
-            const float wm = warp_max(__uint_as_float(s[n]));
-            if (lane == 0) red[quarter * N + n] = wm;
+          for (int n = 0; n < COLS; ++n) {
+            float x = __uint_as_float(s[n]) * sl2;
+            if (!full_block) x = (n >= lo && n < hi) ? x : -INFINITY;
+            s[n] = __float_as_uint(x);
+            over |= x > m[n] + RESCALE_LOG2;
           }
-          softmax_sync();
-          if (j > walk.j0 && !__all_sync(0xffffffffu, wait_phase(o_done + 8 * ((g - 1) & 1u),
-                                                                ((g - 1) >> 1) & 1u, p, abort_flag)))
+          // P buffer sb was last read by the O products of block g - 2.
+          if (g >= 2 && !__all_sync(0xffffffffu, wait_phase(o_done + 8 * sb, ((g - 2) >> 1) & 1u, p,
+                                                           abort_flag)))
             ok = false;
-          ptx::tc_fence_after();
-          uint32_t o[N];
-          float alpha[N];
+          if (group_or(grp, over)) {
 #pragma unroll
-          for (int n = 0; n < N; ++n) {
-            const float mx = fmaxf(fmaxf(red[n], red[N + n]), fmaxf(red[2 * N + n], red[3 * N + n]));
-            const float mn = mx > m[n] + RESCALE_LOG2 ? mx : m[n];
-            alpha[n] = ptx::ex2_approx(m[n] - mn);
-            l[n] *= alpha[n];
-            m[n] = mn;
-          }
-          if (j > walk.j0) {
-#pragma unroll 1
-            for (int half = 0; half < 2; ++half) {
-              const uint32_t ta = tmem + t_lane + C::O_COL + (uint32_t)half * N;
-              tmem_ld_n<N>(ta, o);
-#pragma unroll
-              for (int n = 0; n < N; ++n)
-                o[n] = __float_as_uint(__uint_as_float(o[n]) * alpha[n]);
-              tmem_st_n<N>(ta, o);
+            for (int n = 0; n < COLS; ++n) {
+              const float wm = warp_max(__uint_as_float(s[n]));
+              if (lane == 0) red[quarter * COLS + n] = wm;
             }
-            ptx::tmem_st_wait();
-          }
-          softmax_sync();   // `red` is read
-        }
-        const uint32_t p_buf = p_off + sb * C::P_BYTES;
+            group_sync(grp);
+            if (j > walk.j0 &&
+                !__all_sync(0xffffffffu, wait_phase(o_done + 8 * ((g - 1) & 1u),
+                                                    ((g - 1) >> 1) & 1u, p, abort_flag)))
+              ok = false;
+            ptx::tc_fence_after();
+            float alpha[COLS];
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-          const float w = ptx::ex2_approx(__uint_as_float(s[n]) - m[n]);
-          l[n] += w;
-          const unsigned short h = __half_as_ushort(__float2half_rn(w));
-          asm volatile("st.shared.u16 [%0], %1;" ::"r"(p_buf + n * 128u + ((p_col ^ (n & 7)) << 4)),
-                       "h"(h)
-                       : "memory");
+            for (int n = 0; n < COLS; ++n) {
+              const float mx = fmaxf(fmaxf(red[n], red[COLS + n]),
+                                     fmaxf(red[2 * COLS + n], red[3 * COLS + n]));
+              const float mn = mx > m[n] + RESCALE_LOG2 ? mx : m[n];
+              alpha[n] = ptx::ex2_approx(m[n] - mn);
+              l[n] *= alpha[n];
+              m[n] = mn;
+            }
+            if (j > walk.j0) {
+#pragma unroll 1
+              for (int half = 0; half < 2; ++half) {
+                uint32_t o[COLS];
+                const uint32_t ta = tmem + t_lane + C::O_COL + (uint32_t)half * N;
+                tmem_ld(ta, o);
+#pragma unroll
+                for (int n = 0; n < COLS; ++n)
+                  o[n] = __float_as_uint(__uint_as_float(o[n]) * alpha[n]);
+                tmem_st(ta, o);
+              }
+              ptx::tmem_st_wait();
+            }
+            group_sync(grp);   // `red` is read
+          }
+          const uint32_t p_buf = p_off + sb * C::P_BYTES;
+#pragma unroll
+          for (int n = 0; n < COLS; ++n) {
+            const float w = ptx::ex2_approx(__uint_as_float(s[n]) - m[n]);
+            l[n] += w;
+            // The product with V takes binary16 weights (half a step of 2^-11 each).
+            const unsigned short h = __half_as_ushort(__float2half_rn(w));
+            asm volatile(
+                "st.shared.u16 [%0], %1;" ::"r"(p_buf + n * 128u + ((p_col ^ (n & 7)) << 4)), "h"(h)
+                : "memory");
+          }
+          ptx::fence_proxy_async_smem();
         }
-        ptx::fence_proxy_async_smem();
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(p_full + 8 * sb);
       }
       // The tile ends: sums over the 128 keys' threads, then O.
-      if (softmax_or(!ok)) ok = false;
+      if (group_or(grp, !ok)) ok = false;
+      if (rows > 0) {
 #pragma unroll
-      for (int n = 0; n < N; ++n) {
-        float v = l[n];
+        for (int n = 0; n < COLS; ++n) {
+          float v = l[n];
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-        if (lane == 0) red[quarter * N + n] = v;
+          for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+          if (lane == 0) red[quarter * COLS + n] = v;
+        }
+        group_sync(grp);
+#pragma unroll
+        for (int n = 0; n < COLS; ++n)
+          l[n] = (red[n] + red[COLS + n]) + (red[2 * COLS + n] + red[3 * COLS + n]);
       }
-      softmax_sync();
-#pragma unroll
-      for (int n = 0; n < N; ++n)
-        l[n] = (red[n] + red[N + n]) + (red[2 * N + n] + red[3 * N + n]);
       if (ok && !__all_sync(0xffffffffu, wait_phase(o_done + 8 * ((g - 1) & 1u),
                                                     ((g - 1) >> 1) & 1u, p, abort_flag)))
         ok = false;
-      softmax_sync();       // `red` is read
+      group_sync(grp);       // `red` is read
       const bool whole = walk.j0 == 0 && walk.j1 == walk.s.nb;
       const long long L = walk.line();
       const int slot = part_slot(L, sc.per, cta);
-      if (ok) {
+      if (ok && rows > 0) {
         ptx::tc_fence_after();
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
-          uint32_t o[N];
-          tmem_ld_n<N>(tmem + t_lane + C::O_COL + (uint32_t)half * N, o);
+          uint32_t o[COLS];
+          tmem_ld(tmem + t_lane + C::O_COL + (uint32_t)half * N, o);
           const int d = half * 128 + key_row;
           if (whole) {
-            __half* dst = p.O + (int64_t)walk.r.start * p.o_tok +
-                          (int64_t)(head * p.group) * p.o_head + d;
-            int in_group = 0;
+            int tok = col0 / p.group, in_group = col0 - tok * p.group;
+            __half* dst = p.O + (int64_t)(walk.r.start + tok) * p.o_tok +
+                          (int64_t)(head * p.group + in_group) * p.o_head + d;
 #pragma unroll
-            for (int n = 0; n < N; ++n) {
+            for (int n = 0; n < COLS; ++n) {
               if (n < rows) {
                 const float inv = l[n] > 0.f ? 1.f / l[n] : 0.f;
                 *dst = __float2half_rn(__uint_as_float(o[n]) * inv);
@@ -691,40 +693,43 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               }
             }
           } else {
-            float* dst = p.part + ((int64_t)slot * N) * HD + d;
+            float* dst = p.part + ((int64_t)slot * N + col0) * HD + d;
 #pragma unroll
-            for (int n = 0; n < N; ++n)
+            for (int n = 0; n < COLS; ++n)
               if (n < rows) __stcg(dst + n * HD, __uint_as_float(o[n]));
           }
         }
         if (!whole && key_row == 0) {
 #pragma unroll
-          for (int n = 0; n < N; ++n)
-            if (n < rows) __stcg(p.part_ml + (int64_t)slot * N + n, make_float2(m[n], l[n]));
+          for (int n = 0; n < COLS; ++n)
+            if (n < rows)
+              __stcg(p.part_ml + (int64_t)slot * N + col0 + n, make_float2(m[n], l[n]));
         }
       }
       // The next tile's first O product overwrites O; it follows this
       // thread's next arrival on p_full.
       ptx::tc_fence_before();
       if (!whole) {
+        // Whichever CTA's group comes last merges the group's rows.
         const int c0 = (int)(L / sc.per), c1 = (int)((L + walk.s.nb - 1) / sc.per);
         const int first = part_slot(L, sc.per, c0);
         __threadfence();
-        softmax_sync();
+        group_sync(grp);
+        bool last = false;
         if (key_row == 0) {
-          const int before = atomicAdd(p.counters + first, 1);
-          *last_flag = before == c1 - c0;
-          if (before == c1 - c0) p.counters[first] = 0;
+          int* counter = p.counters + first * MAX_GROUPS + grp;
+          last = atomicAdd(counter, 1) == c1 - c0;
+          if (last) *counter = 0;
         }
-        softmax_sync();
-        if (*reinterpret_cast<volatile int*>(last_flag)) {
+        if (group_or(grp, last)) {
           __threadfence();
           // One warp per row, eight numbers per lane.
-          for (int n = (int)quarter; n < rows; n += SM_WARPS) {
+          for (int n = (int)quarter; n < rows; n += 4) {
+            const int64_t at = col0 + n;
             float mx = NO_OFFSET;
             for (int c = c0 + (int)lane; c <= c1; c += 32) {
               const int sl = c == c0 ? first : 2 * c;
-              mx = fmaxf(mx, __ldcg(p.part_ml + (int64_t)sl * N + n).x);
+              mx = fmaxf(mx, __ldcg(p.part_ml + (int64_t)sl * N + at).x);
             }
             mx = warp_max(mx);
             float sum = 0.f, acc[8] = {};
@@ -732,7 +737,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               float wgt = 0.f;
               if (cb + (int)lane <= c1) {
                 const int c = cb + (int)lane, sl = c == c0 ? first : 2 * c;
-                const float2 ml = __ldcg(p.part_ml + (int64_t)sl * N + n);
+                const float2 ml = __ldcg(p.part_ml + (int64_t)sl * N + at);
                 wgt = ptx::ex2_approx(ml.x - mx);
                 sum += wgt * ml.y;
               }
@@ -742,7 +747,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 const int c = cb + i, sl = c == c0 ? first : 2 * c;
                 const float wi = __shfl_sync(0xffffffffu, wgt, i);
                 const float4* src =
-                    reinterpret_cast<const float4*>(p.part + ((int64_t)sl * N + n) * HD) + lane * 2;
+                    reinterpret_cast<const float4*>(p.part + ((int64_t)sl * N + at) * HD) + lane * 2;
                 const float4 a = __ldcg(src), b = __ldcg(src + 1);
                 acc[0] = fmaf(wi, a.x, acc[0]);
                 acc[1] = fmaf(wi, a.y, acc[1]);
@@ -757,14 +762,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
             const float inv = sum > 0.f ? 1.f / sum : 0.f;
-            const int tok = n / p.group;
+            const int tok = (int)at / p.group;
             uint4 out;
             out.x = pack_half2(acc[0] * inv, acc[1] * inv);
             out.y = pack_half2(acc[2] * inv, acc[3] * inv);
             out.z = pack_half2(acc[4] * inv, acc[5] * inv);
             out.w = pack_half2(acc[6] * inv, acc[7] * inv);
             *reinterpret_cast<uint4*>(p.O + (int64_t)(walk.r.start + tok) * p.o_tok +
-                                      (int64_t)(head * p.group + n - tok * p.group) * p.o_head +
+                                      (int64_t)(head * p.group + (int)at - tok * p.group) * p.o_head +
                                       lane * 8) = out;
           }
         }
@@ -782,7 +787,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   }
   if (warp == 1) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem, C::COLS);
+    ptx::tmem_dealloc(tmem, C::TMEM_COLS);
   }
 }
 
