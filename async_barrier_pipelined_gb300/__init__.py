@@ -635,10 +635,9 @@ def paged_maps(plan: Plan, cached, added, block_table, free_pages, free_head, pa
     if out is None:
         room = (max(max_tokens, 0) + 3) // 4 * 4    # 16-byte pieces
         buf = cached.new_empty(2 * room + 2 * batch + 2)
-        positions, slots, starts, kv_lens, head = buf.split_with_sizes(
-            (room, room, batch + 1, batch, 1))
-        if room != max_tokens:
-            positions, slots = positions[:max(max_tokens, 0)], slots[:max(max_tokens, 0)]
+        used = max(max_tokens, 0)
+        positions, _, slots, _, starts, kv_lens, head = buf.split_with_sizes(
+            (used, room - used, used, room - used, batch + 1, batch, 1))
         out = PagedMaps(starts, kv_lens, positions, slots, head)
     else:
         for name, X, n in (("starts", out.starts, batch + 1), ("kv_lens", out.kv_lens, batch),

@@ -20,7 +20,7 @@
 //   dealing  the pairs get equal shares of the step's key blocks, whatever
 //            the lengths (causal tiles differ in cost); a tile that is cut
 //            leaves FP32 partials, and of each 32 rows the last warp to
-//            finish merges them in order, counted as in the small kernel.
+//            finish adds them up, counted as in the small kernel.
 // Barriers and signals are those of attn_pair.cuh.
 #pragma once
 
@@ -32,11 +32,17 @@ constexpr int CQ = 128;                 // rows per CTA
 constexpr int BKV = BLOCK_KEYS;
 constexpr int MAX_ROWS = 64;            // most keys per copy group (a CTA's half of a key block)
 constexpr int RING = 4;
-constexpr int SM_WARPS = 4;             // softmax warps 2..5
-constexpr int EP_WARPS = 4;             // epilogue warps 6..9
-constexpr int NUM_THREADS = 32 * (2 + SM_WARPS + EP_WARPS);
+constexpr int SM_WARPS = 4;             // softmax warps 0..3
+constexpr int EP_WARPS = 4;             // epilogue warps 4..7
+constexpr int COPY_WARP = 8, MMA_WARP = 9;
+constexpr int NUM_THREADS = 384;        // three warpgroups (two warps of the last are idle)
+// Registers per thread: 168 at launch, then more for the softmax, whose
+// threads hold a row of 128 scores, and the epilogue (64 numbers of O and of a
+// part), less for copies and MMAs.
+constexpr int SM_REGS = 208, EP_REGS = 192, IO_REGS = 104;
+static_assert(SM_REGS + EP_REGS + IO_REGS <= 3 * 168, "the launch's registers");
 constexpr int NUM_WARPS = NUM_THREADS / 32;
-constexpr int WIN = NUM_THREADS;        // requests kept in shared memory
+constexpr int WIN = 320;                // requests kept in shared memory
 
 constexpr uint32_t CHUNK_Q = CQ * 128;
 constexpr uint32_t Q_BYTES = 4 * CHUNK_Q;
@@ -187,10 +193,12 @@ __device__ __forceinline__ void schedule(const Params& p, uint8_t* smem, int wor
       if (pass == 0 || !one) {
         __syncthreads();
         const int b = b0 + tid;
-        Request r{0, 0, 0, false};
-        if (b < p.batch) r = load_request(p, b);
-        if (pass == 0 && r.bad) *(volatile int*)p.status = (int)GEMM_F16_ERR_BAD_INDEX;
-        req[tid] = make_int4(r.start, r.n, r.len, 0);
+        if (tid < WIN) {
+          Request r{0, 0, 0, false};
+          if (b < p.batch) r = load_request(p, b);
+          if (pass == 0 && r.bad) *(volatile int*)p.status = (int)GEMM_F16_ERR_BAD_INDEX;
+          req[tid] = make_int4(r.start, r.n, r.len, 0);
+        }
         __syncthreads();
         const int left = imin(WIN, p.batch - b0);
         for (int k = warp; k < left; k += NUM_WARPS) {
@@ -202,7 +210,7 @@ __device__ __forceinline__ void schedule(const Params& p, uint8_t* smem, int wor
         }
         __syncthreads();
       }
-      const long long mine = (long long)req[tid].w * p.kv_heads;
+      const long long mine = tid < WIN ? (long long)req[tid].w * p.kv_heads : 0;
       long long inc = mine;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -465,7 +473,7 @@ __device__ __forceinline__ float block_offset(const uint32_t (&s)[BKV], float sl
   float r8[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) r8[k] = __uint_as_float(s[k]);
-  if (sl2 >= 0.f) {
+  if (sl2 > 0.f) {
 #pragma unroll
     for (int c = 8; c < BKV; ++c) r8[c & 7] = fmaxf(r8[c & 7], __uint_as_float(s[c]));
 #pragma unroll
@@ -476,7 +484,7 @@ __device__ __forceinline__ float block_offset(const uint32_t (&s)[BKV], float sl
 #pragma unroll
     for (int k = 1; k < 8; ++k) r8[0] = fminf(r8[0], r8[k]);
   }
-  const float mx = (sl2 == 0.f) ? 0.f : r8[0] * sl2;
+  const float mx = r8[0] * sl2;
   const float m_new = (mx > m + RESCALE_LOG2) ? mx : m;
   *alpha = (m_new == m) ? 1.f : ptx::ex2_approx(m - m_new);
   return m_new;
@@ -484,18 +492,13 @@ __device__ __forceinline__ float block_offset(const uint32_t (&s)[BKV], float sl
 
 // Weights 2^(sl2 s - m) as binary16 pairs (the product with V takes binary16;
 // half a step of 2^-11 each), and their FP32 sum before that rounding.
-template <bool MASK>
 __device__ __forceinline__ float block_weights(const uint32_t (&s)[BKV], float sl2, float neg_m,
-                                               const uint32_t (&see)[4], uint32_t (&pk)[BKV / 2]) {
+                                               uint32_t (&pk)[BKV / 2]) {
   float l4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int c = 0; c < BKV / 2; ++c) {
-    float p0 = ptx::ex2_approx(fmaf(__uint_as_float(s[2 * c]), sl2, neg_m));
-    float p1 = ptx::ex2_approx(fmaf(__uint_as_float(s[2 * c + 1]), sl2, neg_m));
-    if (MASK) {
-      p0 = (see[c >> 4] >> ((2 * c) & 31)) & 1u ? p0 : 0.f;
-      p1 = (see[c >> 4] >> ((2 * c + 1) & 31)) & 1u ? p1 : 0.f;
-    }
+    const float p0 = ptx::ex2_approx(fmaf(__uint_as_float(s[2 * c]), sl2, neg_m));
+    const float p1 = ptx::ex2_approx(fmaf(__uint_as_float(s[2 * c + 1]), sl2, neg_m));
     pk[c] = pack_half2(p0, p1);
     l4[c & 3] += p0 + p1;
   }
@@ -511,9 +514,9 @@ __device__ __forceinline__ void softmax_role(const Params& p, Walk& walk, uint32
   const uint32_t row = quarter * 32u + lane;
   const uint32_t leader_p_full = ptx::map_to_cta(b.p_full, 0);
   const uint32_t leader_s_free = ptx::map_to_cta(b.s_free, 0);
-  const uint32_t sig_p = ptx::map_to_cta(base + OFF_SIG + SIG_P + (warp - 2) * SIG_BYTES, 0);
-  const uint32_t sig_s = ptx::map_to_cta(base + OFF_SIG + SIG_S + (warp - 2) * SIG_BYTES, 0);
-  const uint32_t sig_src = base + OFF_SIG + SIG_SRC + (warp - 2) * SIG_BYTES;
+  const uint32_t sig_p = ptx::map_to_cta(base + OFF_SIG + SIG_P + warp * SIG_BYTES, 0);
+  const uint32_t sig_s = ptx::map_to_cta(base + OFF_SIG + SIG_S + warp * SIG_BYTES, 0);
+  const uint32_t sig_src = base + OFF_SIG + SIG_SRC + warp * SIG_BYTES;
   const float sl2 = p.scale_log2;
   const int my_tok = (int)rank * (p.tile_tokens / 2) + (int)row / p.group;   // in the tile
   uint32_t g = 0, ki = 0;
@@ -525,11 +528,8 @@ __device__ __forceinline__ void softmax_role(const Params& p, Walk& walk, uint32
     for (int j = walk.j0; j < walk.j1; ++j, ++g) {
       const int blk = span_block(walk.s, j);
       const bool full_block = block_is_full(p0, p1, blk, p.masks);
-      uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
-      if (!full_block) {
-#pragma unroll
-        for (int w = 0; w < 4; ++w) see[w] = seen_word(walk.s, blk, w, p.rows, pos, p.masks);
-      }
+      uint32_t see[4];
+      if (!full_block) seen_words(walk.s, blk, p.rows, pos, p.masks, see);
       if (!warp_wait(b.s_full, g & 1u, p, abort_flag)) {
         ok = false;
         break;
@@ -544,18 +544,16 @@ __device__ __forceinline__ void softmax_role(const Params& p, Walk& walk, uint32
       ptx::reg_fence(s);
       if (j + 1 < walk.j1 || walk.more())
         signal_leader(rank, lane, b.s_free, leader_s_free, sig_s, sig_src);
-      float alpha, m_new, lsum;
+      float alpha;
       uint32_t pk[BKV / 2];
       if (!full_block) {
-        const uint32_t fill = __float_as_uint(sl2 >= 0.f ? -INFINITY : INFINITY);
+        // A hidden key's score becomes the infinity whose weight is 0.
+        const uint32_t fill = __float_as_uint(sl2 > 0.f ? -INFINITY : INFINITY);
 #pragma unroll
         for (int c = 0; c < BKV; ++c) s[c] = (see[c >> 5] >> (c & 31)) & 1u ? s[c] : fill;
-        m_new = block_offset(s, sl2, m, &alpha);
-        lsum = block_weights<true>(s, sl2, -m_new, see, pk);
-      } else {
-        m_new = block_offset(s, sl2, m, &alpha);
-        lsum = block_weights<false>(s, sl2, -m_new, see, pk);
       }
+      const float m_new = block_offset(s, sl2, m, &alpha);
+      const float lsum = block_weights(s, sl2, -m_new, pk);
       const uint32_t pb = g & 1u;
       if (g >= 2) {
         if (!warp_wait(b.o_done + 8 * pb, ((g - 2) >> 1) & 1u, p, abort_flag)) {
@@ -602,33 +600,82 @@ __device__ __forceinline__ void softmax_role(const Params& p, Walk& walk, uint32
 }
 
 // ------------------------------------------------------------------ epilogue
-// Per tile, each warp its 32 rows: O out of tensor memory, through a box in
-// shared memory (128 bytes of each row) to whole 128-byte pieces of rows in
-// global memory: normalised binary16 rows of O, or, of a tile that is cut, the
-// unnormalised FP32 partial.
+// 64 numbers of each of a warp's 32 rows (one row per thread, FP32, times
+// `factor`) to O: through a box in shared memory, so that each row's 128 bytes
+// go out together.
+__device__ __forceinline__ void store_rows(const Params& p, const float (&f)[64], float factor,
+                                           uint32_t box, const uint4* box_rows, uint32_t lane,
+                                           uint32_t quarter, int rows, __half* dst0, int cc) {
+  const uint32_t lsw = lane & 7u;
+#pragma unroll
+  for (uint32_t i = 0; i < 8; ++i)
+    ptx::st_shared_v4(box + lane * 128u + ((i ^ lsw) << 4),
+                      pack_half2(f[8 * i] * factor, f[8 * i + 1] * factor),
+                      pack_half2(f[8 * i + 2] * factor, f[8 * i + 3] * factor),
+                      pack_half2(f[8 * i + 4] * factor, f[8 * i + 5] * factor),
+                      pack_half2(f[8 * i + 6] * factor, f[8 * i + 7] * factor));
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = i * 4 + (int)(lane >> 3);
+    const uint4 v = box_rows[r * 8 + (int)((lane & 7u) ^ (uint32_t)(r & 7))];
+    if (r < rows) {
+      const int rr = (int)quarter * 32 + r, tok = rr / p.group;
+      *(reinterpret_cast<uint4*>(dst0 + tok * p.o_tok + (int64_t)(rr - tok * p.group) * p.o_head +
+                                 cc * 64) + (lane & 7u)) = v;
+    }
+  }
+  __syncwarp();
+}
+
+// Per tile, each warp its 32 rows, a row per thread.  A tile that is the
+// cluster's alone: O out of tensor memory, normalised, to O.  Of a tile that
+// is cut, the last warp to finish these 32 rows adds its own part, still in
+// tensor memory, to those that the others left in the workspace; they are
+// written as [number / 4][row][4], so that a thread finds its own row's
+// numbers beside the other threads'.  (The part of a tile's end is done at the
+// beginning of a cluster's share and that of its beginning at the end of the
+// one before, so the merge mostly reads one part that has been there for long.)
+// The parts are added in their order, whoever adds them.
 __device__ __forceinline__ void epilogue_role(const Params& p, const Sched& sc, Walk& walk,
                                               uint8_t* smem, uint32_t base, uint32_t tmem_base,
                                               const Bars& b, const float* l_rows, uint32_t rank,
                                               uint32_t warp, uint32_t lane, int cluster,
                                               volatile int* abort_flag) {
   const uint32_t quarter = warp & 3u;
-  const uint32_t t_lane = (quarter * 32u) << 16;
-  const uint32_t e = warp - (2 + SM_WARPS);
+  const uint32_t o_addr = tmem_base + ((quarter * 32u) << 16) + O_COL;
+  const uint32_t e = warp - SM_WARPS;
   const uint32_t leader_o_free = ptx::map_to_cta(b.o_free, 0);
   const uint32_t sig_o = ptx::map_to_cta(base + OFF_SIG + SIG_O + e * SIG_BYTES, 0);
   const uint32_t sig_src = base + OFF_SIG + SIG_SRC + (SM_WARPS + e) * SIG_BYTES;
   const uint32_t box = base + OFF_STAGE + e * BOX;
   const uint4* box_rows = reinterpret_cast<const uint4*>(smem + OFF_STAGE + e * BOX);
-  const uint32_t lsw = lane & 7u;
   const int cta_tokens = p.tile_tokens / 2;
+  const int sub = (int)rank * EP_WARPS + (int)quarter;      // these 32 rows among the pair's
   uint32_t ki = 0, g_end = 0;
   bool ok = true;
+  // 64 numbers of this thread's row of O; after the last ones O may be overwritten.
+  auto load_o = [&](int cc, bool more, float (&f)[64]) {
+    uint32_t o[64];
+    ptx::tmem_ld_32x32b_x32(o_addr + (uint32_t)cc * 64u,
+                            *reinterpret_cast<uint32_t(*)[32]>(&o[0]));
+    ptx::tmem_ld_32x32b_x32(o_addr + (uint32_t)cc * 64u + 32u,
+                            *reinterpret_cast<uint32_t(*)[32]>(&o[32]));
+    ptx::tmem_ld_wait();
+    ptx::reg_fence(o);
+    if (cc == HD / 64 - 1 && more)
+      signal_leader(rank, lane, b.o_free, leader_o_free, sig_o, sig_src);
+#pragma unroll
+    for (int i = 0; i < 64; ++i) f[i] = __uint_as_float(o[i]);
+  };
+  auto part_of = [&](int slot, int cc) {   // its 16 pieces are 32 float4 apart
+    return reinterpret_cast<float4*>(p.part + ((int64_t)slot * PART_ROWS + sub * 32) * HD) +
+           cc * 16 * 32 + lane;
+  };
   while (walk.next()) {
     const int head = walk.cur_head;
     const bool more = walk.more();
     const bool whole = walk.j0 == 0 && walk.j1 == walk.s.nb;
-    const long long L = walk.line();
-    const int slot = part_slot(L, sc.per, cluster);
     g_end += (uint32_t)(walk.j1 - walk.j0);
     const uint32_t g_last = g_end - 1;
     // Tokens of this CTA that exist; where its rows go.
@@ -636,134 +683,98 @@ __device__ __forceinline__ void epilogue_role(const Params& p, const Sched& sc, 
     const int rows = imin(imax(tokens * p.group - (int)quarter * 32, 0), 32);
     __half* const dst0 = p.O + (int64_t)(walk.r.start + walk.i0 + (int)rank * cta_tokens) * p.o_tok +
                          (int64_t)(head * p.group) * p.o_head;
-    const int64_t part_row = (int64_t)slot * PART_ROWS + (int)rank * CQ + (int)quarter * 32;
+    float l = 0.f, m = NO_OFFSET;
     ok = ok && __all_sync(0xffffffffu, wait_sleepy(b.l_ready, ki & 1u, p, abort_flag));
     if (ok) {
-      const float l = l_rows[quarter * 32u + lane];
-      const float m = l_rows[CQ + quarter * 32u + lane];
+      l = l_rows[quarter * 32u + lane];
+      m = l_rows[CQ + quarter * 32u + lane];
       __syncwarp();
       if (more && lane == 0) ptx::mbar_arrive(b.l_free);
       ok = warp_wait(b.o_done + 8 * (g_last & 1u), (g_last >> 1) & 1u, p, abort_flag);
       ptx::tc_fence_after();
-      if (ok) {
-        const float inv_l = l > 0.f ? 1.f / l : 0.f;
-        if (!whole) __stcg(p.part_ml + part_row + lane, make_float2(m, l));
-#pragma unroll 1
-        for (int c = 0; c < HD / 32; ++c) {
-          uint32_t o[32];
-          ptx::tmem_ld_32x32b_x32(tmem_base + t_lane + O_COL + (uint32_t)c * 32u, o);
-          ptx::tmem_ld_wait();
-          ptx::reg_fence(o);
-          if (c == HD / 32 - 1 && more)
-            signal_leader(rank, lane, b.o_free, leader_o_free, sig_o, sig_src);
-          if (!whole) {
-#pragma unroll
-            for (uint32_t i = 0; i < 8; ++i)
-              ptx::st_shared_v4(box + lane * 128u + ((i ^ lsw) << 4), o[4 * i], o[4 * i + 1],
-                                o[4 * i + 2], o[4 * i + 3]);
-          } else {
-#pragma unroll
-            for (uint32_t i = 0; i < 4; ++i) {
-              const float* f = reinterpret_cast<const float*>(&o[8 * i]);
-              const uint32_t col = (uint32_t)(c & 1) * 4u + i;
-              ptx::st_shared_v4(box + lane * 128u + ((col ^ lsw) << 4),
-                                pack_half2(f[0] * inv_l, f[1] * inv_l),
-                                pack_half2(f[2] * inv_l, f[3] * inv_l),
-                                pack_half2(f[4] * inv_l, f[5] * inv_l),
-                                pack_half2(f[6] * inv_l, f[7] * inv_l));
-            }
-            if (!(c & 1)) continue;   // a box holds 64 binary16 numbers of a row
-          }
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int r = i * 4 + (int)(lane >> 3);
-            const uint4 v = box_rows[r * 8 + (int)((lane & 7u) ^ (uint32_t)(r & 7))];
-            if (r < rows) {
-              if (!whole) {
-                __stcg(reinterpret_cast<uint4*>(p.part + (part_row + r) * HD + c * 32) +
-                           (lane & 7u), v);
-              } else {
-                const int rr = (int)quarter * 32 + r, tok = rr / p.group;
-                *(reinterpret_cast<uint4*>(dst0 + tok * p.o_tok +
-                                           (int64_t)(rr - tok * p.group) * p.o_head +
-                                           (c >> 1) * 64) + (lane & 7u)) = v;
-              }
-            }
-          }
-          __syncwarp();
-        }
-      }
     }
     ++ki;
-    if (!whole) {
-      const int c0 = (int)(L / sc.per), c1 = (int)((L + walk.s.nb - 1) / sc.per);
-      const int first = part_slot(L, sc.per, c0);
-      int* counter = p.counters + first * COUNTERS + (int)rank * EP_WARPS + (int)quarter;
+    if (whole) {
+      if (!ok) continue;
+      const float inv_l = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll 1
+      for (int cc = 0; cc < HD / 64; ++cc) {
+        float f[64];
+        load_o(cc, more, f);
+        store_rows(p, f, inv_l, box, box_rows, lane, quarter, rows, dst0, cc);
+      }
+      continue;
+    }
+    const long long L = walk.line();
+    const int c0 = (int)(L / sc.per), c1 = (int)((L + walk.s.nb - 1) / sc.per);
+    const int first = part_slot(L, sc.per, c0), own = part_slot(L, sc.per, cluster);
+    int* counter = p.counters + first * COUNTERS + sub;
+    int before = 0;
+    if (lane == 0) before = atomicAdd(counter, 0);
+    before = __shfl_sync(0xffffffffu, before, 0);
+    bool in_tmem = before == c1 - c0;      // all the others are there
+    if (!in_tmem) {
+      if (ok) {
+        __stcg(p.part_ml + (int64_t)own * PART_ROWS + sub * 32 + lane, make_float2(m, l));
+#pragma unroll 1
+        for (int cc = 0; cc < HD / 64; ++cc) {
+          float f[64];
+          load_o(cc, more, f);
+          float4* dst = part_of(own, cc);
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            __stcg(dst + i * 32, make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]));
+        }
+      }
       __threadfence();
       __syncwarp();
-      int before = 0;
       if (lane == 0) before = atomicAdd(counter, 1);
       before = __shfl_sync(0xffffffffu, before, 0);
       if (before != c1 - c0) continue;
-      if (lane == 0) *counter = 0;
-      __threadfence();
-      // Merge: lane k takes numbers 8k .. 8k+7 of each row.
-      const int64_t sub = (int64_t)rank * CQ + (int)quarter * 32;
+    }
+    if (lane == 0) *counter = 0;
+    if (!ok) continue;
+    __threadfence();
+    auto ml_of = [&](int c) {
+      if (in_tmem && c == cluster) return make_float2(m, l);
+      const int slot = c == c0 ? first : 2 * c;
+      return __ldcg(p.part_ml + (int64_t)slot * PART_ROWS + sub * 32 + lane);
+    };
+    float mx = NO_OFFSET, sum = 0.f;
+    for (int c = c0; c <= c1; ++c) mx = fmaxf(mx, ml_of(c).x);
+    for (int c = c0; c <= c1; ++c) {
+      const float2 ml = ml_of(c);
+      sum = fmaf(ptx::ex2_approx(ml.x - mx), ml.y, sum);
+    }
+    const float inv_l = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll 1
-      for (int r0 = 0; r0 < rows; r0 += 4) {
-        float mx[4], sum[4], acc[4][8];
+    for (int cc = 0; cc < HD / 64; ++cc) {
+      float acc[64];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          mx[i] = NO_OFFSET;
-          sum[i] = 0.f;
+      for (int i = 0; i < 64; ++i) acc[i] = 0.f;
+#pragma unroll 1
+      for (int c = c0; c <= c1; ++c) {
+        const float w = ptx::ex2_approx(ml_of(c).x - mx);
+        if (in_tmem && c == cluster) {
+          float f[64];
+          load_o(cc, more, f);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) acc[i][k] = 0.f;
-        }
-        for (int c = c0; c <= c1; ++c) {
-          const int64_t pr = (int64_t)(c == c0 ? first : 2 * c) * PART_ROWS + sub + r0;
+          for (int i = 0; i < 64; ++i) acc[i] = fmaf(w, f[i], acc[i]);
+        } else {
+          const float4* src = part_of(c == c0 ? first : 2 * c, cc);
+          float4 v[16];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) mx[i] = fmaxf(mx[i], __ldcg(p.part_ml + pr + i).x);
-        }
-        for (int c = c0; c <= c1; ++c) {
-          const int64_t pr = (int64_t)(c == c0 ? first : 2 * c) * PART_ROWS + sub + r0;
-          float4 a[4], bb[4];
-          float2 ml[4];
+          for (int i = 0; i < 16; ++i) v[i] = __ldcg(src + i * 32);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float4* src = reinterpret_cast<const float4*>(p.part + (pr + i) * HD) + lane * 2;
-            a[i] = __ldcg(src);
-            bb[i] = __ldcg(src + 1);
-            ml[i] = __ldcg(p.part_ml + pr + i);
+          for (int i = 0; i < 16; ++i) {
+            acc[4 * i] = fmaf(w, v[i].x, acc[4 * i]);
+            acc[4 * i + 1] = fmaf(w, v[i].y, acc[4 * i + 1]);
+            acc[4 * i + 2] = fmaf(w, v[i].z, acc[4 * i + 2]);
+            acc[4 * i + 3] = fmaf(w, v[i].w, acc[4 * i + 3]);
           }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float w = ptx::ex2_approx(ml[i].x - mx[i]);
-            sum[i] = fmaf(w, ml[i].y, sum[i]);
-            acc[i][0] = fmaf(w, a[i].x, acc[i][0]);
-            acc[i][1] = fmaf(w, a[i].y, acc[i][1]);
-            acc[i][2] = fmaf(w, a[i].z, acc[i][2]);
-            acc[i][3] = fmaf(w, a[i].w, acc[i][3]);
-            acc[i][4] = fmaf(w, bb[i].x, acc[i][4]);
-            acc[i][5] = fmaf(w, bb[i].y, acc[i][5]);
-            acc[i][6] = fmaf(w, bb[i].z, acc[i][6]);
-            acc[i][7] = fmaf(w, bb[i].w, acc[i][7]);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (r0 + i >= rows) continue;
-          const float inv = sum[i] > 0.f ? 1.f / sum[i] : 0.f;
-          const int rr = (int)quarter * 32 + r0 + i, tok = rr / p.group;
-          uint4 out;
-          out.x = pack_half2(acc[i][0] * inv, acc[i][1] * inv);
-          out.y = pack_half2(acc[i][2] * inv, acc[i][3] * inv);
-          out.z = pack_half2(acc[i][4] * inv, acc[i][5] * inv);
-          out.w = pack_half2(acc[i][6] * inv, acc[i][7] * inv);
-          *(reinterpret_cast<uint4*>(dst0 + tok * p.o_tok +
-                                     (int64_t)(rr - tok * p.group) * p.o_head) + lane) = out;
         }
       }
+      store_rows(p, acc, inv_l, box, box_rows, lane, quarter, rows, dst0, cc);
     }
   }
 }
@@ -820,7 +831,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
   b.mma_done = b.l_free + 8;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_ABORT);
 
-  if (warp == 0 && lane == 0) {
+  if (warp == COPY_WARP && lane == 0) {
     ptx::prefetch_tmap(&tmQ);
     ptx::prefetch_tmap(&tmK);
     ptx::prefetch_tmap(&tmV);
@@ -845,7 +856,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     *reinterpret_cast<volatile uint32_t*>(smem + OFF_PEER_QLOADS) = 0;
     ptx::fence_mbar_init();
   }
-  if (warp == 1) {
+  if (warp == MMA_WARP) {
     ptx::tmem_alloc_pair(base + OFF_TMEM_SLOT, TMEM_COLS);
     ptx::tmem_relinquish_pair();
   }
@@ -861,43 +872,52 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
   ptx::cluster_sync();  // the peer's barriers exist before anyone signals them
   ptx::tc_fence_after();
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEM_SLOT);
-  const Sched sc = *reinterpret_cast<const Sched*>(smem + OFF_SCHED);
-  Walk walk(p, sc, reinterpret_cast<const int4*>(smem + OFF_REQ));
+  const Sched& sc = *reinterpret_cast<const Sched*>(smem + OFF_SCHED);
+  const int4* req = reinterpret_cast<const int4*>(smem + OFF_REQ);
 
   Issued issued{0, 0};
-  if (warp == 0) {
-    issued = producer_role(&tmQ, &tmK, &tmV, p, walk, base, b, rank, lane, cluster, abort_flag);
-  } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
-      mma_role(p, walk, base, tmem_base, b, abort_flag);
-      ptx::mma_commit_pair(b.mma_done, 0x1);
-      wait_drain(b.mma_done, 0, p.timeout_ns);
-    }
-    __syncwarp();
-  } else if (warp < 2 + SM_WARPS) {
+  if (warp < SM_WARPS) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SM_REGS));
+    Walk walk(p, sc, req);
     softmax_role(p, walk, base, tmem_base, b, l_rows, rank, warp, lane, abort_flag);
-  } else {
+  } else if (warp < SM_WARPS + EP_WARPS) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(EP_REGS));
     if (p.zero_rows)
-      zero_tail(p, (int)blockIdx.x * EP_WARPS + (int)warp - 2 - SM_WARPS, (int)gridDim.x * EP_WARPS);
+      zero_tail(p, (int)blockIdx.x * EP_WARPS + (int)warp - SM_WARPS, (int)gridDim.x * EP_WARPS);
+    Walk walk(p, sc, req);
     epilogue_role(p, sc, walk, smem, base, tmem_base, b, l_rows, rank, warp, lane, cluster,
                   abort_flag);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(IO_REGS));
+    if (warp == COPY_WARP) {
+      Walk walk(p, sc, req);
+    issued = producer_role(&tmQ, &tmK, &tmV, p, walk, base, b, rank, lane, cluster, abort_flag);
+    } else if (warp == MMA_WARP) {
+      if (lane == 0 && rank == 0) {
+        Walk walk(p, sc, req);
+    mma_role(p, walk, base, tmem_base, b, abort_flag);
+        ptx::mma_commit_pair(b.mma_done, 0x1);
+        wait_drain(b.mma_done, 0, p.timeout_ns);
+      }
+      __syncwarp();
+    }
   }
 
-  if (warp == 0 && lane == 0 && rank == 1) {
+  if (warp == COPY_WARP && lane == 0 && rank == 1) {
     ptx::st_cluster_u32(ptx::map_to_cta(base + OFF_PEER_FILLS, 0), issued.fills);
     ptx::st_cluster_u32(ptx::map_to_cta(base + OFF_PEER_QLOADS, 0), issued.qloads);
   }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::cluster_sync();  // both CTAs have stopped issuing
-  if (warp == 0 && lane == 0 && rank == 0) {
+  if (warp == COPY_WARP && lane == 0 && rank == 0) {
     const Issued peer{*reinterpret_cast<volatile uint32_t*>(smem + OFF_PEER_FILLS),
                       *reinterpret_cast<volatile uint32_t*>(smem + OFF_PEER_QLOADS)};
     leader_drain(b, issued, peer, 4u * 128u * (uint32_t)(p.tile_tokens / 2 * p.group),
                  p.timeout_ns);
   }
   ptx::cluster_sync();  // no copy into either CTA is still in flight
-  if (warp == 1) {
+  if (warp == MMA_WARP) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc_pair(tmem_base, TMEM_COLS);
   }

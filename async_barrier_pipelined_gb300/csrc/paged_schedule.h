@@ -117,38 +117,54 @@ GF16_HD void rows_that_see(const Span& s, int blk, int r, int rows, int pos0, in
     *hi = (int)lmin(lmax((int64_t)k - pos0 + m.window, 0) * group, tile_rows);
 }
 
-// Bits a .. b - 1 (cut to 0 .. 31) of a word.
-GF16_HD uint32_t bits(int64_t a, int64_t b) {
-  const int lo = (int)lmin(lmax(a, 0), 32), hi = (int)lmin(lmax(b, 0), 32);
-  if (lo >= hi) return 0;
-  return (hi == 32 ? 0xffffffffu : (1u << hi) - 1u) & ~((1u << lo) - 1u);
+// Bits a .. b - 1 of a word, a and b cut to 0 .. 32.
+GF16_HD uint32_t bits(int a, int b) {
+  const int lo = imin(imax(a, 0), 32), hi = imin(imax(b, 0), 32);
+  const uint32_t below_hi = (uint32_t)(((uint64_t)1 << hi) - 1);
+  const uint32_t below_lo = (uint32_t)(((uint64_t)1 << lo) - 1);
+  return below_hi & ~below_lo;
 }
 
-// The rows 32 * word .. + 31 of block `blk` whose keys the query at position
-// p (of the tile of span s) sees, as bits.
-GF16_HD uint32_t seen_word(const Span& s, int blk, int word, int rows, int p, const Masks& m) {
-  // Keys of the query's window and its sinks, as row numbers of an unshifted block.
-  const int64_t k0 = (int64_t)blk * BLOCK_KEYS;
-  const int64_t lo = m.window > 0 ? (int64_t)p - m.window + 1 - k0 : 0, hi = (int64_t)p + 1 - k0;
-  const int64_t sk = m.window > 0 ? lmin(m.sinks, (int64_t)p + 1) - k0 : 0;
-  // Rows before the last needed group are unshifted; that group (its first
-  // row gs) has its keys `shift` rows later.
-  const int64_t left = s.end - k0;
-  int64_t gs = BLOCK_KEYS, shift = 0;
-  if (left > 0 && left < BLOCK_KEYS && left % rows) {
-    gs = left - left % rows;
-    shift = rows - left % rows;
-  } else if (left <= 0) {
-    gs = 0;
-    shift = BLOCK_KEYS;
+// Which rows of block `blk` hold keys that the query at position p (of the
+// tile of span s) sees, as 128 bits.
+GF16_HD void seen_words(const Span& s, int blk, int rows, int p, const Masks& m,
+                        uint32_t (&see)[4]) {
+  // Keys of the query's window and its sinks as rows lo .. hi - 1 and 0 .. sk - 1
+  // of a block without a shifted group, cut to the block.
+  const int k0 = blk * BLOCK_KEYS;
+  const int hi = imin(imax(p - k0 + 1, 0), BLOCK_KEYS);
+  int lo = 0, sk = 0;
+  if (m.window > 0) {
+    lo = (int)lmin(lmax((int64_t)p - k0 + 1 - m.window, 0), BLOCK_KEYS);
+    sk = imin(imax(m.sinks - k0, 0), hi);
   }
-  const int64_t w0 = 32 * word;
-  const uint32_t plain =
-      (bits(lo - w0, hi - w0) | bits(-w0, sk - w0)) & bits(-w0, gs - w0);
-  const uint32_t late = (bits(lmax(lo, gs) + shift - w0, hi + shift - w0) |
-                         bits(gs + shift - w0, sk + shift - w0)) &
-                        bits(gs + shift - w0, gs + rows - w0);
-  return plain | (gs < BLOCK_KEYS ? late : 0u);
+#pragma unroll
+  for (int w = 0; w < 4; ++w)
+    see[w] = bits(lo - 32 * w, hi - 32 * w) | bits(-32 * w, sk - 32 * w);
+  const int left = s.end - k0;
+  if (left >= BLOCK_KEYS) return;
+  if (left <= 0) {   // a tile that sees no key
+#pragma unroll
+    for (int w = 0; w < 4; ++w) see[w] = 0;
+    return;
+  }
+  const int over = left & (rows - 1);
+  const int gs = left - over;   // rows from here on: the last needed group, `shift` rows late
+  if (over == 0) return;        // (hi ends the block's keys)
+  const int shift = rows - over;
+  uint64_t late0 = ((uint64_t)(see[1] & bits(gs - 32, BLOCK_KEYS)) << 32) | (see[0] & bits(gs, BLOCK_KEYS));
+  uint64_t late1 = ((uint64_t)(see[3] & bits(gs - 96, BLOCK_KEYS)) << 32) | (see[2] & bits(gs - 64, BLOCK_KEYS));
+  if (shift >= 64) {
+    late1 = late0 << (shift - 64);
+    late0 = 0;
+  } else {                      // shift >= 1
+    late1 = (late1 << shift) | (late0 >> (64 - shift));
+    late0 <<= shift;
+  }
+  see[0] = (see[0] & bits(0, gs)) | (uint32_t)late0;
+  see[1] = (see[1] & bits(0, gs - 32)) | (uint32_t)(late0 >> 32);
+  see[2] = (see[2] & bits(0, gs - 64)) | (uint32_t)late1;
+  see[3] = (see[3] & bits(0, gs - 96)) | (uint32_t)(late1 >> 32);
 }
 
 // Whether every query of the tile (positions p0 .. p1) sees every key of the

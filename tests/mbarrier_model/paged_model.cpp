@@ -68,8 +68,10 @@ static void check_tile(const Request& r, int i0, int i1, const Masks& m, int pag
     CHECK(!block_is_full(p0, p1, blk, m) || all);
     for (int t = i0; t <= i1; ++t) {
       const int p = r.len - r.n + t;
+      uint32_t see[4];
+      seen_words(s, blk, rows, p, m, see);
       for (int w = 0; w < 4; ++w) {
-        const uint32_t word = seen_word(s, blk, w, rows, p, m);
+        const uint32_t word = see[w];
         for (int i = 0; i < 32; ++i) {
           const int k = row_key(s, blk, 32 * w + i, rows);
           CHECK(((word >> i) & 1u) == (k >= 0 && sees(p, k, m) ? 1u : 0u));
