@@ -31,11 +31,12 @@ namespace large {
 constexpr int CQ = 128;                 // rows per CTA
 constexpr int BKV = BLOCK_KEYS;
 constexpr int MAX_ROWS = 64;            // most keys per copy group (a CTA's half of a key block)
-constexpr int RING = 4;
+constexpr int RING = 2;                 // key tiles, and value tiles, in flight
+constexpr int SLOTS = 2 * RING;         // keys in slots 0 .. RING - 1, values in the others
 constexpr int SM_WARPS = 4;             // softmax warps 0..3
 constexpr int EP_WARPS = 4;             // epilogue warps 4..7
-constexpr int COPY_WARP = 8, MMA_WARP = 9;
-constexpr int NUM_THREADS = 384;        // three warpgroups (two warps of the last are idle)
+constexpr int COPY_K_WARP = 8, COPY_V_WARP = 9, MMA_WARP = 10;
+constexpr int NUM_THREADS = 384;        // three warpgroups (the last warp is idle)
 // Registers per thread: 168 at launch, then more for the softmax, whose
 // threads hold a row of 128 scores, and the epilogue (64 numbers of O and of a
 // part), less for copies and MMAs.
@@ -52,17 +53,17 @@ constexpr uint32_t SLOT_BYTES = 32768;
 constexpr uint32_t BOX = 32 * 128;      // 32 rows by 128 bytes of O
 constexpr uint32_t OFF_Q = 0;
 constexpr uint32_t OFF_RING = OFF_Q + Q_BYTES;
-constexpr uint32_t OFF_STAGE = OFF_RING + RING * SLOT_BYTES;   // one box per epilogue warp
+constexpr uint32_t OFF_STAGE = OFF_RING + SLOTS * SLOT_BYTES;  // one box per epilogue warp
 constexpr uint32_t OFF_L = OFF_STAGE + EP_WARPS * BOX;         // row sums and offsets
 constexpr uint32_t OFF_REQ = OFF_L + 2 * CQ * 4;               // WIN x (start, n, len, blocks)
 constexpr uint32_t OFF_SCHED = OFF_REQ + WIN * 16;
 constexpr uint32_t OFF_BAR = OFF_SCHED + 64;
-constexpr uint32_t NUM_BARS = 2 + 2 * RING + 2 + 2 + 2 + 3 + 1;
+constexpr uint32_t NUM_BARS = 2 + 2 * SLOTS + 2 + 2 + 2 + 3 + 1;
 constexpr uint32_t OFF_TMEM_SLOT = OFF_BAR + NUM_BARS * 8;
 constexpr uint32_t OFF_ABORT = OFF_TMEM_SLOT + 4;
-constexpr uint32_t OFF_PEER_FILLS = OFF_ABORT + 4;
-constexpr uint32_t OFF_PEER_QLOADS = OFF_PEER_FILLS + 4;
-constexpr uint32_t OFF_SIG = (OFF_PEER_QLOADS + 4 + 15) / 16 * 16;
+constexpr uint32_t OFF_PEER = OFF_ABORT + 4;                   // see Issued
+constexpr uint32_t OFF_MINE = OFF_PEER + 12;
+constexpr uint32_t OFF_SIG = (OFF_MINE + 12 + 15) / 16 * 16;
 constexpr uint32_t SIG_BYTES = 16;
 constexpr uint32_t SIG_P = 0;
 constexpr uint32_t SIG_S = SIG_P + SM_WARPS * SIG_BYTES;
@@ -302,6 +303,15 @@ __device__ __forceinline__ bool wait_suspend(uint32_t bar, uint32_t parity, cons
   return wait_slow(bar, parity, p, abort_flag);
 }
 
+// The same wait by one lane for its warp: 32 lanes polling a barrier slow the
+// copies that complete it.
+__device__ __forceinline__ bool lane_wait(uint32_t bar, uint32_t parity, uint32_t lane,
+                                          const Params& p, volatile int* abort_flag) {
+  bool ok = true;
+  if (lane == 0) ok = wait_suspend(bar, parity, p, abort_flag);
+  return __shfl_sync(0xffffffffu, ok, 0);
+}
+
 // One arrival per warp on a leader barrier (see attn_pair.cuh).
 __device__ __forceinline__ void signal_leader(uint32_t rank, uint32_t lane, uint32_t local_bar,
                                               uint32_t leader_bar, uint32_t dst, uint32_t src) {
@@ -318,100 +328,96 @@ __device__ __forceinline__ void signal_leader(uint32_t rank, uint32_t lane, uint
 // 3-D tensor load crediting a barrier that may live in the peer CTA: in
 // ptx.cuh (tma_load_3d_pair), as the 4-D one.
 
+// Copies that a CTA has issued: key tiles, value tiles, Q tiles.
 struct Issued {
-  uint32_t fills, qloads;
+  uint32_t keys, values, queries;
 };
 
 // ------------------------------------------------------------------ copies
-__device__ __forceinline__ Issued producer_role(const CUtensorMap* tmQ, const CUtensorMap* tmK,
-                                                const CUtensorMap* tmV, const Params& p, Walk& walk,
-                                                uint32_t base, const Bars& b, uint32_t rank,
-                                                uint32_t lane, int cluster,
-                                                volatile int* abort_flag) {
+// Keys and values each have a warp and a ring of their own: with pages of 16
+// rows a tile is 16 copies of 2 KB and one warp that issues both kinds falls
+// behind the MMAs (4096 tokens over 8192 in pages of 16: see paged_attn.cu).
+// Both CTAs fill their halves, crediting the leader's barriers; the leader
+// also arrives (expect_tx) for the pair.
+template <bool KEYS>
+__device__ __forceinline__ uint32_t fill_ring(const CUtensorMap* tmQ, const CUtensorMap* tm,
+                                              const Params& p, Walk& walk, uint32_t base,
+                                              const Bars& b, uint32_t rank, uint32_t lane,
+                                              int cluster, uint32_t* queries,
+                                              volatile int* abort_flag) {
   const uint32_t leader_q = ptx::map_to_cta(b.q_full, 0);
-  const uint32_t leader_full = ptx::map_to_cta(b.full, 0);
+  const uint32_t bar0 = KEYS ? 0u : 8u * RING;          // of this ring among full / empty
+  const uint32_t leader_full = ptx::map_to_cta(b.full + bar0, 0);
   const int cta_tokens = p.tile_tokens / 2;
   const uint32_t q_bytes = 4u * 128u * (uint32_t)(cta_tokens * p.group);
-  const int kg = MAX_ROWS / p.rows;            // groups of this CTA's half of a key block (1 .. 8)
-  // Keys: lane = chunk * 8 + group; values: lane = chunk * 16 + group.
-  const int k_chunk = (int)lane >> 3, k_in = (int)lane & 7;
-  const int k_group = (int)rank * kg + imin(k_in, kg - 1);
-  const int v_chunk = (int)lane >> 4, v_in = (int)lane & 15;
-  const int v_group = imin(v_in, 2 * kg - 1);
+  // Keys: this CTA's 64 of the block, lane = chunk * 8 + group of rows (4 x 1 .. 8).
+  // Values: all 128, this CTA's 128 numbers, lane = chunk * 16 + group (2 x 2 .. 16).
+  const int half_groups = MAX_ROWS / p.rows;
+  const int groups = KEYS ? half_groups : 2 * half_groups;
+  const int chunk = (int)lane / (KEYS ? 8 : 16), in = (int)lane % (KEYS ? 8 : 16);
+  const int group = (KEYS ? (int)rank * half_groups : 0) + imin(in, groups - 1);
+  const int col = KEYS ? 64 * chunk : (int)rank * 128 + 64 * chunk;
+  const uint32_t to = base + OFF_RING + (KEYS ? 0u : RING * SLOT_BYTES) +
+                      (uint32_t)chunk * (KEYS ? K_CHUNK : V_CHUNK) + (uint32_t)(in * p.rows) * 128u;
   RingPos pos{0, 0};
-  Issued n{0, 0};
+  uint32_t fills = 0, loads = 0;
   bool ok = true;
   while (ok && walk.next()) {
-    const int head = walk.cur_head;
-    if (n.qloads > 0)
-      ok = __all_sync(0xffffffffu, wait_suspend(b.q_empty, (n.qloads - 1) & 1u, p, abort_flag));
-    if (!ok) break;
-    if (lane == 0) {
-      if (rank == 0) ptx::mbar_arrive_expect_tx_relaxed(b.q_full, 2 * q_bytes);
+    if (KEYS) {
+      if (loads > 0)
+        ok = lane_wait(b.q_empty, (loads - 1) & 1u, lane, p, abort_flag);
+      if (!ok) break;
+      if (lane == 0) {
+        if (rank == 0) ptx::mbar_arrive_expect_tx_relaxed(b.q_full, 2 * q_bytes);
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        ptx::tma_load_3d_pair(base + OFF_Q + c * CHUNK_Q, tmQ, leader_q, 64 * c, head * p.group,
-                              walk.r.start + walk.i0 + (int)rank * cta_tokens);
-    }
-    ++n.qloads;
-    auto page_of = [&](int j, int g) {
-      return j < walk.j1 ? group_page(p, walk.s, walk.b, span_block(walk.s, j), g) : 0;
-    };
-    auto fill = [&](bool is_k, int j, int page) -> bool {
-      const int g = is_k ? k_group : v_group;
-      const int2 src = group_source(p, walk.s, span_block(walk.s, j), g, page);
-      if (!__all_sync(0xffffffffu, wait_suspend(b.empty + 8 * pos.stage, producer_wait_parity(pos),
-                                                p, abort_flag)))
-        return false;
-      if (rank == 0 && lane == 0)
-        ptx::mbar_arrive_expect_tx_relaxed(b.full + 8 * pos.stage, 2 * SLOT_BYTES);
-      __syncwarp();
-      if (!(n.fills == 0 && cluster == p.fault_unit && rank == 0)) {
-        const uint32_t dst = base + OFF_RING + pos.stage * SLOT_BYTES;
-        const uint32_t fb = leader_full + 8 * pos.stage;
-        if (is_k) {
-          if (k_in < kg)
-            ptx::tma_load_4d_pair(dst + k_chunk * K_CHUNK + (uint32_t)(k_in * p.rows) * 128u, tmK,
-                                  fb, 64 * k_chunk, src.y, head, src.x);
-        } else {
-          if (v_in < 2 * kg)
-            ptx::tma_load_4d_pair(dst + v_chunk * V_CHUNK + (uint32_t)(v_in * p.rows) * 128u, tmV,
-                                  fb, (int)rank * 128 + 64 * v_chunk, src.y, head, src.x);
-        }
+        for (int c = 0; c < 4; ++c)
+          ptx::tma_load_3d_pair(base + OFF_Q + c * CHUNK_Q, tmQ, leader_q, 64 * c,
+                                walk.cur_head * p.group,
+                                walk.r.start + walk.i0 + (int)rank * cta_tokens);
       }
-      ++n.fills;
-      ring_advance(pos, RING);
-      return true;
+      ++loads;
+    }
+    // Table entries are looked up two blocks ahead.
+    auto page_of = [&](int j) {
+      return j < walk.j1 ? group_page(p, walk.s, walk.b, span_block(walk.s, j), group) : 0;
     };
-    int kp = page_of(walk.j0, k_group), vp = page_of(walk.j0, v_group);
-    int kp1 = page_of(walk.j0 + 1, k_group);
-    ok = fill(true, walk.j0, kp);
-    for (int j = walk.j0; ok && j < walk.j1; ++j) {
-      const int kp2 = page_of(j + 2, k_group), vp1 = page_of(j + 1, v_group);
-      if (j + 1 < walk.j1) ok = fill(true, j + 1, kp1);
-      ok = ok && fill(false, j, vp);
-      kp1 = kp2;
-      vp = vp1;
+    int page = page_of(walk.j0), page1 = page_of(walk.j0 + 1);
+    for (int j = walk.j0; j < walk.j1; ++j) {
+      const int page2 = page_of(j + 2);
+      const int2 src = group_source(p, walk.s, span_block(walk.s, j), group, page);
+      page = page1;
+      page1 = page2;
+      ok = lane_wait(b.empty + bar0 + 8 * pos.stage, producer_wait_parity(pos), lane, p, abort_flag);
+      if (!ok) break;
+      if (rank == 0 && lane == 0)
+        ptx::mbar_arrive_expect_tx_relaxed(b.full + bar0 + 8 * pos.stage, 2 * SLOT_BYTES);
+      __syncwarp();
+      if (in < groups && !(KEYS && fills == 0 && cluster == p.fault_unit && rank == 0))
+        ptx::tma_load_4d_pair(to + pos.stage * SLOT_BYTES, tm, leader_full + 8 * pos.stage, col,
+                              src.y, walk.cur_head, src.x);
+      ++fills;
+      ring_advance(pos, RING);
     }
   }
-  return n;
+  *queries = loads;
+  return fills;
 }
 
 // ------------------------------------------------------------------ MMAs (leader)
 __device__ __forceinline__ void mma_role(const Params& p, Walk& walk, uint32_t base,
                                          uint32_t tmem_base, const Bars& b,
                                          volatile int* abort_flag) {
-  RingPos pos{0, 0};
+  RingPos kpos{0, 0}, vpos{0, 0};
   const uint32_t q_addr = base + OFF_Q;
   const uint32_t o_tmem = tmem_base + O_COL;
   auto issue_qk = [&](uint32_t gs, bool last_of_tile) -> bool {
     if (gs > 0) {
       if (!wait_suspend(b.s_free, (gs - 1) & 1u, p, abort_flag)) return false;
     }
-    if (!wait_suspend(b.full + 8 * pos.stage, consumer_wait_parity(pos), p, abort_flag))
+    if (!wait_suspend(b.full + 8 * kpos.stage, consumer_wait_parity(kpos), p, abort_flag))
       return false;
     ptx::tc_fence_after();
-    const uint32_t k_addr = base + OFF_RING + pos.stage * SLOT_BYTES;
+    const uint32_t k_addr = base + OFF_RING + kpos.stage * SLOT_BYTES;
 #pragma unroll
     for (int kk = 0; kk < HD / 16; ++kk) {
       const uint32_t off_q = (uint32_t)(kk >> 2) * CHUNK_Q + (uint32_t)(kk & 3) * 32u;
@@ -419,10 +425,10 @@ __device__ __forceinline__ void mma_role(const Params& p, Walk& walk, uint32_t b
       ptx::mma_f16_pair(tmem_base + S_COL, smem_desc_sw128(q_addr + off_q, 16, 1024),
                         smem_desc_sw128(k_addr + off_k, 16, 1024), IDESC_QK, kk > 0 ? 1u : 0u);
     }
-    ptx::mma_commit_pair(b.empty + 8 * pos.stage, 0x3);
+    ptx::mma_commit_pair(b.empty + 8 * kpos.stage, 0x3);
     ptx::mma_commit_pair(b.s_full, 0x3);
     if (last_of_tile) ptx::mma_commit_pair(b.q_empty, 0x3);
-    ring_advance(pos, RING);
+    ring_advance(kpos, RING);
     return true;
   };
   uint32_t g0 = 0, ki = 0;
@@ -440,7 +446,7 @@ __device__ __forceinline__ void mma_role(const Params& p, Walk& walk, uint32_t b
       }
       const uint32_t pb = gj & 1u;
       if (!wait_suspend(b.p_full + 8 * pb, (gj >> 1) & 1u, p, abort_flag) ||
-          !wait_suspend(b.full + 8 * pos.stage, consumer_wait_parity(pos), p, abort_flag)) {
+          !wait_suspend(b.full + 8 * (RING + vpos.stage), consumer_wait_parity(vpos), p, abort_flag)) {
         ok = false;
         break;
       }
@@ -449,16 +455,16 @@ __device__ __forceinline__ void mma_role(const Params& p, Walk& walk, uint32_t b
         break;
       }
       ptx::tc_fence_after();
-      const uint32_t v_addr = base + OFF_RING + pos.stage * SLOT_BYTES;
+      const uint32_t v_addr = base + OFF_RING + (RING + vpos.stage) * SLOT_BYTES;
       const uint32_t p_tmem = tmem_base + P_COL + pb * (BKV / 2);
 #pragma unroll
       for (int kk = 0; kk < BKV / 16; ++kk)
         ptx::mma_f16_pair_tmem_a(o_tmem, p_tmem + (uint32_t)kk * 8u,
                                  smem_desc_sw128(v_addr + (uint32_t)kk * 2048u, V_CHUNK, 1024),
                                  IDESC_PV, (j > 0 || kk > 0) ? 1u : 0u);
-      ptx::mma_commit_pair(b.empty + 8 * pos.stage, 0x3);
+      ptx::mma_commit_pair(b.empty + 8 * (RING + vpos.stage), 0x3);
       ptx::mma_commit_pair(b.o_done + 8 * pb, 0x3);
-      ring_advance(pos, RING);
+      ring_advance(vpos, RING);
     }
     g0 += (uint32_t)nb;
     ++ki;
@@ -603,9 +609,10 @@ __device__ __forceinline__ void softmax_role(const Params& p, Walk& walk, uint32
 // 64 numbers of each of a warp's 32 rows (one row per thread, FP32, times
 // `factor`) to O: through a box in shared memory, so that each row's 128 bytes
 // go out together.
-__device__ __forceinline__ void store_rows(const Params& p, const float (&f)[64], float factor,
+__device__ __forceinline__ void store_rows(const float (&f)[64], float factor,
                                            uint32_t box, const uint4* box_rows, uint32_t lane,
-                                           uint32_t quarter, int rows, __half* dst0, int cc) {
+                                           const int64_t (&row_off)[8], int rows, __half* dst0,
+                                           int cc) {
   const uint32_t lsw = lane & 7u;
 #pragma unroll
   for (uint32_t i = 0; i < 8; ++i)
@@ -620,9 +627,7 @@ __device__ __forceinline__ void store_rows(const Params& p, const float (&f)[64]
     const int r = i * 4 + (int)(lane >> 3);
     const uint4 v = box_rows[r * 8 + (int)((lane & 7u) ^ (uint32_t)(r & 7))];
     if (r < rows) {
-      const int rr = (int)quarter * 32 + r, tok = rr / p.group;
-      *(reinterpret_cast<uint4*>(dst0 + tok * p.o_tok + (int64_t)(rr - tok * p.group) * p.o_head +
-                                 cc * 64) + (lane & 7u)) = v;
+      *reinterpret_cast<uint4*>(dst0 + row_off[i] + cc * 64) = v;
     }
   }
   __syncwarp();
@@ -652,6 +657,13 @@ __device__ __forceinline__ void epilogue_role(const Params& p, const Sched& sc, 
   const uint4* box_rows = reinterpret_cast<const uint4*>(smem + OFF_STAGE + e * BOX);
   const int cta_tokens = p.tile_tokens / 2;
   const int sub = (int)rank * EP_WARPS + (int)quarter;      // these 32 rows among the pair's
+  // The rows that this thread writes (store_rows), and its 16 bytes of them.
+  int64_t row_off[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int rr = (int)(quarter * 32u + i * 4 + (lane >> 3)), tok = rr / p.group;
+    row_off[i] = tok * p.o_tok + (int64_t)(rr - tok * p.group) * p.o_head + (lane & 7u) * 8;
+  }
   uint32_t ki = 0, g_end = 0;
   bool ok = true;
   // 64 numbers of this thread's row of O; after the last ones O may be overwritten.
@@ -701,7 +713,7 @@ __device__ __forceinline__ void epilogue_role(const Params& p, const Sched& sc, 
       for (int cc = 0; cc < HD / 64; ++cc) {
         float f[64];
         load_o(cc, more, f);
-        store_rows(p, f, inv_l, box, box_rows, lane, quarter, rows, dst0, cc);
+        store_rows(f, inv_l, box, box_rows, lane, row_off, rows, dst0, cc);
       }
       continue;
     }
@@ -774,30 +786,29 @@ __device__ __forceinline__ void epilogue_role(const Params& p, const Sched& sc, 
           }
         }
       }
-      store_rows(p, acc, inv_l, box, box_rows, lane, quarter, rows, dst0, cc);
+      store_rows(acc, inv_l, box, box_rows, lane, row_off, rows, dst0, cc);
     }
   }
 }
 
-// See attn_pair.cuh: completes every phase a producer opened and waits
-// (bounded) for the copies that were issued.
+// See attn_pair.cuh: completes every phase a copy warp opened and waits
+// (bounded) for the copies that were issued.  Fill f of a ring used slot
+// f % RING in phase parity (f / RING) & 1.
+__device__ __forceinline__ void drain_ring(uint32_t bar0, uint32_t mine, uint32_t peer,
+                                           uint32_t slots, uint32_t bytes, uint64_t limit_ns) {
+  const uint32_t hi = mine > peer ? mine : peer;
+  for (uint32_t f = hi > slots ? hi - slots : 0u; f < hi; ++f) {
+    const uint32_t bar = bar0 + 8 * (f % slots);
+    if (f >= mine) ptx::mbar_arrive_expect_tx_relaxed(bar, bytes);
+    if (f >= peer) ptx::mbar_complete_tx(bar, bytes);
+    wait_drain(bar, (f / slots) & 1u, limit_ns);
+  }
+}
 __device__ __noinline__ void leader_drain(const Bars& b, Issued mine, Issued peer, uint32_t q_bytes,
                                           uint64_t limit_ns) {
-  const uint32_t hi = mine.fills > peer.fills ? mine.fills : peer.fills;
-  const uint32_t lo = hi > (uint32_t)RING ? hi - (uint32_t)RING : 0u;
-  for (uint32_t f = lo; f < hi; ++f) {
-    const uint32_t bar = b.full + 8 * (f % RING);
-    if (f >= mine.fills) ptx::mbar_arrive_expect_tx_relaxed(bar, SLOT_BYTES);
-    if (f >= peer.fills) ptx::mbar_complete_tx(bar, SLOT_BYTES);
-    wait_drain(bar, (f / RING) & 1u, limit_ns);
-  }
-  const uint32_t qhi = mine.qloads > peer.qloads ? mine.qloads : peer.qloads;
-  if (qhi > 0) {
-    const uint32_t q = qhi - 1;
-    if (q >= mine.qloads) ptx::mbar_arrive_expect_tx_relaxed(b.q_full, q_bytes);
-    if (q >= peer.qloads) ptx::mbar_complete_tx(b.q_full, q_bytes);
-    wait_drain(b.q_full, q & 1u, limit_ns);
-  }
+  drain_ring(b.full, mine.keys, peer.keys, RING, SLOT_BYTES, limit_ns);
+  drain_ring(b.full + 8 * RING, mine.values, peer.values, RING, SLOT_BYTES, limit_ns);
+  drain_ring(b.q_full, mine.queries, peer.queries, 1, q_bytes, limit_ns);
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
@@ -820,8 +831,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
   b.q_full = base + OFF_BAR;
   b.q_empty = b.q_full + 8;
   b.full = b.q_empty + 8;
-  b.empty = b.full + 8 * RING;
-  b.s_full = b.empty + 8 * RING;
+  b.empty = b.full + 8 * SLOTS;
+  b.s_full = b.empty + 8 * SLOTS;
   b.s_free = b.s_full + 8;
   b.p_full = b.s_free + 8;
   b.o_done = b.p_full + 16;
@@ -831,13 +842,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
   b.mma_done = b.l_free + 8;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_ABORT);
 
-  if (warp == COPY_WARP && lane == 0) {
+  if (warp == COPY_K_WARP && lane == 0) {
     ptx::prefetch_tmap(&tmQ);
     ptx::prefetch_tmap(&tmK);
     ptx::prefetch_tmap(&tmV);
     ptx::mbar_init(b.q_full, 1);
     ptx::mbar_init(b.q_empty, 1);
-    for (int s = 0; s < RING; ++s) {
+    for (int s = 0; s < SLOTS; ++s) {
       ptx::mbar_init(b.full + 8 * s, 1);
       ptx::mbar_init(b.empty + 8 * s, 1);
     }
@@ -852,8 +863,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     ptx::mbar_init(b.l_free, EP_WARPS);
     ptx::mbar_init(b.mma_done, 1);
     *abort_flag = 0;
-    *reinterpret_cast<volatile uint32_t*>(smem + OFF_PEER_FILLS) = 0;
-    *reinterpret_cast<volatile uint32_t*>(smem + OFF_PEER_QLOADS) = 0;
+    for (int k = 0; k < 6; ++k)
+      *reinterpret_cast<volatile uint32_t*>(smem + OFF_PEER + 4 * k) = 0;
     ptx::fence_mbar_init();
   }
   if (warp == MMA_WARP) {
@@ -875,7 +886,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
   const Sched& sc = *reinterpret_cast<const Sched*>(smem + OFF_SCHED);
   const int4* req = reinterpret_cast<const int4*>(smem + OFF_REQ);
 
-  Issued issued{0, 0};
   if (warp < SM_WARPS) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SM_REGS));
     Walk walk(p, sc, req);
@@ -889,9 +899,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                   abort_flag);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(IO_REGS));
-    if (warp == COPY_WARP) {
+    if (warp == COPY_K_WARP || warp == COPY_V_WARP) {
       Walk walk(p, sc, req);
-    issued = producer_role(&tmQ, &tmK, &tmV, p, walk, base, b, rank, lane, cluster, abort_flag);
+      uint32_t queries, fills;
+      if (warp == COPY_K_WARP)
+        fills = fill_ring<true>(&tmQ, &tmK, p, walk, base, b, rank, lane, cluster, &queries,
+                                abort_flag);
+      else
+        fills = fill_ring<false>(&tmQ, &tmV, p, walk, base, b, rank, lane, cluster, &queries,
+                                 abort_flag);
+      // What each CTA issued, for the leader's drain: its own beside the peer's.
+      if (lane == 0) {
+        const uint32_t at = base + (rank == 0 ? OFF_MINE : OFF_PEER);
+        if (warp == COPY_K_WARP) {
+          ptx::st_cluster_u32(ptx::map_to_cta(at, 0), fills);
+          ptx::st_cluster_u32(ptx::map_to_cta(at + 8, 0), queries);
+        } else {
+          ptx::st_cluster_u32(ptx::map_to_cta(at + 4, 0), fills);
+        }
+      }
     } else if (warp == MMA_WARP) {
       if (lane == 0 && rank == 0) {
         Walk walk(p, sc, req);
@@ -903,18 +929,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     }
   }
 
-  if (warp == COPY_WARP && lane == 0 && rank == 1) {
-    ptx::st_cluster_u32(ptx::map_to_cta(base + OFF_PEER_FILLS, 0), issued.fills);
-    ptx::st_cluster_u32(ptx::map_to_cta(base + OFF_PEER_QLOADS, 0), issued.qloads);
-  }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::cluster_sync();  // both CTAs have stopped issuing
-  if (warp == COPY_WARP && lane == 0 && rank == 0) {
-    const Issued peer{*reinterpret_cast<volatile uint32_t*>(smem + OFF_PEER_FILLS),
-                      *reinterpret_cast<volatile uint32_t*>(smem + OFF_PEER_QLOADS)};
-    leader_drain(b, issued, peer, 4u * 128u * (uint32_t)(p.tile_tokens / 2 * p.group),
-                 p.timeout_ns);
+  if (warp == COPY_K_WARP && lane == 0 && rank == 0) {
+    const volatile uint32_t* mine = reinterpret_cast<volatile uint32_t*>(smem + OFF_MINE);
+    const volatile uint32_t* peer = reinterpret_cast<volatile uint32_t*>(smem + OFF_PEER);
+    leader_drain(b, Issued{mine[0], mine[1], mine[2]}, Issued{peer[0], peer[1], peer[2]},
+                 4u * 128u * (uint32_t)(p.tile_tokens / 2 * p.group), p.timeout_ns);
   }
   ptx::cluster_sync();  // no copy into either CTA is still in flight
   if (warp == MMA_WARP) {
