@@ -5,7 +5,8 @@ kernels of ``csrc/``.  The functions keep the C names; raw pointers are
 Python ints.  ``matmul``, ``attention`` and the calls of a serving step over
 a paged cache (``paged_maps``, ``rotary``, ``rotary_to_cache``,
 ``paged_attention``) are conveniences that take torch tensors (PyTorch is
-used only for device memory and streams).
+used only for device memory and streams); the latter four marshal in C++
+(``csrc/torch_calls.cpp``), because a step makes them for every layer.
 
 The library is built in-tree by ``async_barrier_pipelined_gb300.build.build()``
 (``__graft_entry__.build()`` calls it).  If it is missing, loading fails
@@ -15,12 +16,12 @@ from __future__ import annotations
 
 import collections
 import ctypes
-import functools
+import importlib.util
 import math
 import os
 import threading
 
-from .build import LIB_PATH
+from .build import CALLS_NAME, CALLS_PATH, LIB_PATH
 
 __all__ = [
     "GemmError", "load", "gemm_f16_plan", "gemm_f16_run", "gemm_f16_run_host",
@@ -516,10 +517,7 @@ def attn_f16_paged_maps_validate(*args) -> int:
     return load().attn_f16_paged_maps_validate(*args)
 
 
-@functools.lru_cache(maxsize=1024)
 def _i64s(values):
-    """A tuple of strides as the C array that the library reads (and never
-    writes): the same tuples come back every step."""
     return None if values is None else (_c_i64 * len(values))(*[int(x) for x in values])
 
 
@@ -582,26 +580,33 @@ def attn_f16_paged_validate(batch, total_q, max_q, q_heads, kv_heads, head_dim, 
         table_stride, max_pages, starts, kv_lens, O, _i64s(o_strides), scale, window, sinks)
 
 
-def _need(X, name: str, dtype, dims: int, plan: Plan):
-    """A torch tensor of this type and rank on the plan's device, its last
-    dimension contiguous.  Returns its strides."""
-    if X.dtype is not dtype or X.dim() != dims:
-        raise ValueError(f"{name} must be a {dims}-dimensional {dtype} tensor")
-    if X.get_device() != plan.device:
-        raise ValueError(f"{name} must be on the plan's device")
-    st = X.stride()
-    if st[-1] != 1 and X.shape[-1] > 1:
-        raise ValueError(f"{name}'s last dimension must be contiguous")
-    return st
+_calls = None
 
 
-def _plan_stream(plan: Plan, stream) -> int:
-    """The handle of `stream`, by default torch's current one on the plan's device."""
-    if stream is not None:
-        return _stream_handle(stream)
-    import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # without a Stream object
-    return raw(plan.device) if raw else int(torch.cuda.current_stream(plan.device).cuda_stream)
+def _torch_calls():
+    """The paged-cache calls for torch tensors (raises if they have not been built)."""
+    global _calls
+    if _calls is None:
+        import torch  # noqa: F401  (the module links against it)
+        load()
+        with _lock:
+            if _calls is None:
+                if not os.path.exists(CALLS_PATH):
+                    raise ImportError(
+                        f"paged-cache calls not built ({CALLS_PATH} missing); run "
+                        "async_barrier_pipelined_gb300.build.build() first. "
+                        "There is no fallback implementation.")
+                spec = importlib.util.spec_from_file_location(CALLS_NAME, CALLS_PATH)
+                module = importlib.util.module_from_spec(spec)
+                spec.loader.exec_module(module)
+                _calls = module
+    return _calls
+
+
+def _result(r, where: str):
+    if type(r) is int:
+        raise GemmError(r, where)
+    return r
 
 
 PagedMaps = collections.namedtuple("PagedMaps", "starts kv_lens positions slots free_head")
@@ -621,38 +626,11 @@ def paged_maps(plan: Plan, cached, added, block_table, free_pages, free_head, pa
     (0 and -1 past the last token) and the new free_head [1], written into
     ``out`` (a PagedMaps of an earlier call) if given.
     """
-    import torch
-    i32 = torch.int32
-    _need(cached, "cached", i32, 1, plan)
-    _need(added, "added", i32, 1, plan)
-    table_st = _need(block_table, "block_table", i32, 2, plan)
-    _need(free_pages, "free_pages", i32, 1, plan)
-    _need(free_head, "free_head", i32, 1, plan)
-    batch = cached.shape[0]
-    rows, max_pages = block_table.shape
-    if added.shape[0] != batch or rows != batch or free_head.shape[0] != 1:
-        raise ValueError("shape mismatch: cached [B], added [B], block_table [B, P], free_head [1]")
-    if out is None:
-        room = (max(max_tokens, 0) + 3) // 4 * 4    # 16-byte pieces
-        buf = cached.new_empty(2 * room + 2 * batch + 2)
-        used = max(max_tokens, 0)
-        positions, _, slots, _, starts, kv_lens, head = buf.split_with_sizes(
-            (used, room - used, used, room - used, batch + 1, batch, 1))
-        out = PagedMaps(starts, kv_lens, positions, slots, head)
-    else:
-        for name, X, n in (("starts", out.starts, batch + 1), ("kv_lens", out.kv_lens, batch),
-                           ("positions", out.positions, max_tokens),
-                           ("slots", out.slots, max_tokens), ("free_head", out.free_head, 1)):
-            _need(X, "out." + name, i32, 1, plan)
-            if X.shape[0] != n:
-                raise ValueError(f"out.{name} must have {n} entries")
-    attn_f16_paged_maps(plan.handle, batch, cached.data_ptr(), added.data_ptr(),
-                        block_table.data_ptr(), table_st[0] if batch > 1 else max_pages,
-                        max_pages, free_pages.data_ptr(), free_pages.shape[0],
-                        free_head.data_ptr(), page_size, max_tokens, out.starts.data_ptr(),
-                        out.kv_lens.data_ptr(), out.positions.data_ptr(), out.slots.data_ptr(),
-                        out.free_head.data_ptr(), _plan_stream(plan, stream))
-    return out
+    return PagedMaps._make(_result(
+        (_calls or _torch_calls()).paged_maps(
+            plan.handle, plan.device, cached, added, block_table, free_pages, free_head, page_size,
+            max_tokens, out, stream if stream is None else _stream_handle(stream)),
+        "attn_f16_paged_maps"))
 
 
 def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none",
@@ -711,43 +689,6 @@ def _rope_layout(layout: str) -> int:
     raise ValueError("layout is 'half' or 'interleaved'")
 
 
-def _token_heads(X, name: str, plan: Plan, f16, tokens=None):
-    """[tokens, heads, 256] binary16; returns the (token, head) strides."""
-    st = _need(X, name, f16, 3, plan)
-    shape = X.shape
-    if shape[2] != ATTN_HEAD_DIM or (tokens is not None and shape[0] != tokens):
-        raise ValueError(f"{name} must be [tokens, heads, {ATTN_HEAD_DIM}]")
-    return st[:2]
-
-
-def _cache_pair(K_cache, V_cache, plan: Plan, f16):
-    """[pages, page_size, kv_heads, 256] binary16 each; their (page, row, head) strides."""
-    k_st = _need(K_cache, "K_cache", f16, 4, plan)
-    v_st = _need(V_cache, "V_cache", f16, 4, plan)
-    if K_cache.shape != V_cache.shape or K_cache.shape[3] != ATTN_HEAD_DIM:
-        raise ValueError(f"K_cache and V_cache must be [pages, page_size, kv_heads, "
-                         f"{ATTN_HEAD_DIM}]")
-    return k_st[:3], v_st[:3]
-
-
-def _output(X, out, name: str, plan: Plan, f16):
-    """`out`, or a new tensor of X's shape; and its (token, head) strides."""
-    if out is None:
-        shape = X.shape
-        return X.new_empty(shape), (shape[1] * ATTN_HEAD_DIM or ATTN_HEAD_DIM, ATTN_HEAD_DIM)
-    st = _token_heads(out, "out", plan, f16)
-    if out.shape != X.shape:
-        raise ValueError(f"out must have the shape of {name}")
-    return out, st
-
-
-def _rope_common(positions, turns, tokens, plan, torch):
-    _need(positions, "positions", torch.int32, 1, plan)
-    _need(turns, "turns", torch.int64, 1, plan)
-    if positions.shape[0] != tokens:
-        raise ValueError("positions must have one entry per token")
-
-
 def rotary(plan: Plan, X, positions, turns, out=None, layout: str = "half", factor: float = 1.0,
            inverse: bool = False, stream=None):
     """Rotary positions of X, float16 [tokens, heads, 256] (tokens and heads
@@ -758,16 +699,10 @@ def rotary(plan: Plan, X, positions, turns, out=None, layout: str = "half", fact
     rotates back: given the gradient of the output it returns the gradient
     of X.  ``out`` may be X.
     """
-    import torch
-    f16 = torch.float16
-    x_st = _token_heads(X, "X", plan, f16)
-    tokens, heads, dim = X.shape
-    _rope_common(positions, turns, tokens, plan, torch)
-    out, o_st = _output(X, out, "X", plan, f16)
-    attn_f16_rope(plan.handle, tokens, heads, 0, dim, 2 * turns.shape[0], _rope_layout(layout),
-                  int(inverse), factor, turns.data_ptr(), positions.data_ptr(), X.data_ptr(), x_st,
-                  out.data_ptr(), o_st, stream=_plan_stream(plan, stream))
-    return out
+    return _result(
+        (_calls or _torch_calls()).rotary(
+            plan.handle, plan.device, X, positions, turns, out, _rope_layout(layout), factor,
+            inverse, stream if stream is None else _stream_handle(stream)), "attn_f16_rope")
 
 
 def rotary_to_cache(plan: Plan, Q, K, V, positions, slots, turns, K_cache, V_cache, out=None,
@@ -781,27 +716,11 @@ def rotary_to_cache(plan: Plan, Q, K, V, positions, slots, turns, K_cache, V_cac
     contiguous.  positions, slots: int32 [tokens], from paged_maps (slot -1:
     nothing is written).  Returns the rotated Q (in ``out``, which may be Q).
     """
-    import torch
-    f16 = torch.float16
-    q_st = _token_heads(Q, "Q", plan, f16)
-    tokens, heads, dim = Q.shape
-    k_st = _token_heads(K, "K", plan, f16, tokens)
-    v_st = _token_heads(V, "V", plan, f16, tokens)
-    kc_st, vc_st = _cache_pair(K_cache, V_cache, plan, f16)
-    pages, page_size, kv_heads, _ = K_cache.shape
-    if K.shape != V.shape or K.shape[1] != kv_heads:
-        raise ValueError("K, V and the caches must have the same heads")
-    _rope_common(positions, turns, tokens, plan, torch)
-    _need(slots, "slots", torch.int32, 1, plan)
-    if slots.shape[0] != tokens:
-        raise ValueError("slots must have one entry per token")
-    out, o_st = _output(Q, out, "Q", plan, f16)
-    attn_f16_rope(plan.handle, tokens, heads, kv_heads, dim, 2 * turns.shape[0],
-                  _rope_layout(layout), 0, factor, turns.data_ptr(), positions.data_ptr(),
-                  Q.data_ptr(), q_st, out.data_ptr(), o_st, K.data_ptr(), k_st, V.data_ptr(), v_st,
-                  slots.data_ptr(), K_cache.data_ptr(), kc_st, V_cache.data_ptr(), vc_st, pages,
-                  page_size, _plan_stream(plan, stream))
-    return out
+    return _result(
+        (_calls or _torch_calls()).rotary_to_cache(
+            plan.handle, plan.device, Q, K, V, positions, slots, turns, K_cache, V_cache, out,
+            _rope_layout(layout), factor, stream if stream is None else _stream_handle(stream)),
+        "attn_f16_rope")
 
 
 def paged_attention(plan: Plan, Q, K_cache, V_cache, block_table, starts, kv_lens, max_q: int,
@@ -820,24 +739,8 @@ def paged_attention(plan: Plan, Q, K_cache, V_cache, block_table, starts, kv_len
     defaults to 1/sqrt(256).  Rows that see no key, and rows past the last
     request's, are 0.
     """
-    import torch
-    f16, i32 = torch.float16, torch.int32
-    q_st = _token_heads(Q, "Q", plan, f16)
-    kc_st, vc_st = _cache_pair(K_cache, V_cache, plan, f16)
-    table_st = _need(block_table, "block_table", i32, 2, plan)
-    _need(starts, "starts", i32, 1, plan)
-    _need(kv_lens, "kv_lens", i32, 1, plan)
-    batch = kv_lens.shape[0]
-    rows, max_pages = block_table.shape
-    if starts.shape[0] != batch + 1 or rows != batch:
-        raise ValueError("shape mismatch: block_table [B, P], starts [B + 1], kv_lens [B]")
-    out, o_st = _output(Q, out, "Q", plan, f16)
-    tokens, heads, dim = Q.shape
-    pages, page_size, kv_heads, _ = K_cache.shape
-    attn_f16_paged_fwd(plan.handle, batch, tokens, max_q, heads, kv_heads, dim, Q.data_ptr(), q_st,
-                       K_cache.data_ptr(), kc_st, V_cache.data_ptr(), vc_st, pages, page_size,
-                       block_table.data_ptr(), table_st[0] if batch > 1 else max_pages, max_pages,
-                       starts.data_ptr(), kv_lens.data_ptr(), out.data_ptr(), o_st,
-                       ATTN_HEAD_DIM ** -0.5 if scale is None else scale, window, sinks,
-                       _plan_stream(plan, stream))
-    return out
+    return _result(
+        (_calls or _torch_calls()).paged_attention(
+            plan.handle, plan.device, Q, K_cache, V_cache, block_table, starts, kv_lens, max_q, out,
+            ATTN_HEAD_DIM ** -0.5 if scale is None else scale, window, sinks,
+            stream if stream is None else _stream_handle(stream)), "attn_f16_paged_fwd")

@@ -5,12 +5,16 @@ Five translation units (plan and shared host code; the kernels and entry
 points of the GEMM, the attention, the paged-cache maps with rotary
 positions, and the attention over a paged cache) are compiled in parallel with one -gencode each and linked into one library, so a build
 takes seconds on either the x86 build host or the aarch64 GPU host.
+
+Beside it, _lib/paged_torch_calls.so: the paged-cache calls for torch tensors
+(csrc/torch_calls.cpp, host code only, compiled against the installed torch).
 """
 from __future__ import annotations
 
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
@@ -27,6 +31,10 @@ HEADERS = [os.path.join(CSRC, f) for f in ("host.h", "ptx.cuh", "schedule.h", "c
                                             "paged_small.cuh", "paged_large.cuh")]
 DEPENDS = SOURCES + HEADERS + [os.path.join(INCLUDE, "gemm_f16.h"),
                                os.path.join(INCLUDE, "attn_f16.h")]
+
+CALLS_NAME = "paged_torch_calls"
+CALLS_PATH = os.path.join(LIB_DIR, CALLS_NAME + ".so")
+CALLS_SOURCE = os.path.join(CSRC, "torch_calls.cpp")
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -49,12 +57,59 @@ def _compile_cmds(objs: list[str], verbose: bool) -> list[list[str]]:
     return cmds
 
 
+def _fresh(path: str, depends: list[str]) -> bool:
+    return os.path.exists(path) and all(os.path.getmtime(f) <= os.path.getmtime(path)
+                                        for f in depends)
+
+
+def _calls_cmd(obj: str) -> list[str]:
+    from torch.utils import cpp_extension as ext
+    cuda = os.path.dirname(os.path.dirname(nvcc_path()))
+    includes = [*ext.include_paths(), os.path.join(cuda, "include"),
+                sysconfig.get_paths()["include"], INCLUDE]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", f"-DTORCH_EXTENSION_NAME={CALLS_NAME}",
+            "-DTORCH_API_INCLUDE_EXTENSION_H", *[x for i in includes for x in ("-isystem", i)],
+            "-c", CALLS_SOURCE, "-o", obj]
+
+
+def _link_calls(obj: str, out: str) -> None:
+    from torch.utils import cpp_extension as ext
+    dirs = ext.library_paths()
+    subprocess.run(["g++", "-shared", obj, "-o", out, *[f"-L{d}" for d in dirs], "-L", LIB_DIR,
+                    "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python",
+                    "-l:" + os.path.basename(LIB_PATH), "-Wl,-rpath,$ORIGIN",
+                    *[f"-Wl,-rpath,{d}" for d in dirs]], check=True)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile the library if any source is newer than it; return its path."""
+    """Compile what is older than its sources; return the library's path."""
     os.makedirs(LIB_DIR, exist_ok=True)
+    calls = None
+    calls_obj = os.path.join(LIB_DIR, f"{CALLS_NAME}.tmp{os.getpid()}.o")
+    if force or not _fresh(CALLS_PATH, [CALLS_SOURCE, os.path.join(INCLUDE, "attn_f16.h"),
+                                        os.path.join(INCLUDE, "gemm_f16.h")]):
+        calls = subprocess.Popen(_calls_cmd(calls_obj))     # beside the library's units
+    try:
+        _build_library(force, verbose)
+        if calls is not None:
+            if calls.wait():
+                raise subprocess.CalledProcessError(calls.returncode, "g++ " + CALLS_SOURCE)
+            tmp = CALLS_PATH + f".tmp{os.getpid()}"
+            _link_calls(calls_obj, tmp)
+            os.replace(tmp, CALLS_PATH)
+    finally:
+        if calls is not None:
+            if calls.poll() is None:
+                calls.kill()
+                calls.wait()
+            if os.path.exists(calls_obj):
+                os.remove(calls_obj)
+    return LIB_PATH
+
+
+def _build_library(force: bool, verbose: bool) -> str:
     if not force and os.path.exists(LIB_PATH):
-        lib_t = os.path.getmtime(LIB_PATH)
-        if all(os.path.getmtime(f) <= lib_t for f in DEPENDS):
+        if _fresh(LIB_PATH, DEPENDS):
             return LIB_PATH
     tag = f".tmp{os.getpid()}"
     objs = [os.path.join(LIB_DIR, os.path.basename(s)[:-3] + tag + ".o") for s in SOURCES]

@@ -612,3 +612,37 @@ def test_attention_many_requests(g, plan):
         o = run_attention(g, plan, pr)
         done(plan)
         check(o, pr)
+
+
+def test_calls_take_a_stream_and_outputs(g, plan):
+    """`stream` (an object or a handle) and `out` of every call; a tensor that a
+    call allocates belongs to the call's stream."""
+    import torch
+    pr = ref.PagedProblem(ATTENTION["mixed"]["lens"], 8, 2, 16, seed=16)
+    q = pr.q.cuda()
+    want = run_attention(g, plan, pr, q=q)
+    freq = torch.tensor(g.rope_frequencies(64), dtype=torch.float64)
+    turns = g.rope_turns(freq).cuda()
+    pos = torch.arange(q.shape[0], dtype=torch.int32, device="cuda")
+    rotated = g.rotary(plan, q, pos, turns)
+    z = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")
+    added = z(3) + 2
+    table, free = z(3, 4) - 1, torch.arange(9, dtype=torch.int32, device="cuda")
+    maps = g.paged_maps(plan, z(3), added, table, free, z(1), 16, 7)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        o = run_attention(g, plan, pr, q=q, stream=stream)
+        y = g.rotary(plan, q, pos, turns, stream=stream)
+        m = g.paged_maps(plan, z(3), added, table, free, z(1), 16, 7, stream=stream)
+        side.synchronize()
+        assert torch.equal(o, want) and torch.equal(y, rotated)
+        assert all(torch.equal(a, b) for a, b in zip(m, maps))
+    again = g.paged_maps(plan, z(3), added, table, free, z(1), 16, 7, out=maps)
+    assert all(a.data_ptr() == b.data_ptr() for a, b in zip(again, maps))
+    for bad in (maps._replace(slots=z(6)), maps._replace(starts=z(4).float())):
+        with pytest.raises(ValueError):
+            g.paged_maps(plan, z(3), added, table, free, z(1), 16, 7, out=bad)
+    o = torch.empty_like(q)
+    assert run_attention(g, plan, pr, q=q, out=o) is o or torch.equal(o, want)
+    done(plan)
