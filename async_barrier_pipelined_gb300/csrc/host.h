@@ -112,7 +112,7 @@ struct gemm_f16_plan_s {
   int attn_pairs = 0;  // co-resident clusters of two for the pair attention kernel
   void* ws = nullptr;
   size_t ws_bytes = 0;
-  void* paged_ws = nullptr;  // attention over a paged cache: tile counters and partial sums
+  void* paged_ws = nullptr;  // attention over a paged cache: partial sums of cut tiles
   size_t paged_ws_bytes = 0;
   void* apack = nullptr;  // repacked copy of A (see pack_rows_kernel)
   size_t apack_bytes = 0;

@@ -70,33 +70,24 @@ namespace {
 
 constexpr int HEAD_DIM = 256;
 
-// Workspace of the attention over a paged cache: counters, zero between
-// calls, then the partials' offsets and sums, then their FP32 O; of the two
-// kernels' needs the larger.  Its size depends on the device alone.
+// Workspace of the attention over a paged cache: the cut tiles, the partials'
+// offsets and sums, and their FP32 O; of the two kernels' needs the larger.
+// Its size depends on the device alone.
 constexpr int SMALL_ROWS = 64;   // most rows of a request for the small kernel
 
 int ensure_workspace(gemm_f16_plan_s* p, cudaStream_t stream, paged::Params* prm) {
   const size_t small_slots = 2 * (size_t)p->num_sms, large_slots = 2 * (size_t)p->paged_pairs;
   const size_t rows = std::max(small_slots * SMALL_ROWS, large_slots * paged::large::PART_ROWS);
-  const size_t counters =
-      (std::max(small_slots * paged::small::MAX_GROUPS, large_slots * paged::large::COUNTERS) *
-           sizeof(int) + 255) / 256 * 256;
+  const size_t cut = (size_t)p->num_sms * sizeof(paged::CutTile);
   const size_t ml = rows * sizeof(float2);
-  const size_t bytes = counters + ml + rows * HEAD_DIM * sizeof(float);
-  if (p->paged_ws_bytes < bytes) {
-    const int rc = ensure_buffer(&p->paged_ws, &p->paged_ws_bytes, bytes, stream,
-                                 "paged attention workspace allocation");
-    if (rc) return rc;
-    const cudaError_t e = cudaMemsetAsync(p->paged_ws, 0, counters, stream);
-    if (e != cudaSuccess) {
-      p->paged_ws_bytes = 0;   // set up again by the next call
-      return cuda_fail(e, "clear paged attention counters");
-    }
-  }
+  const int rc = ensure_buffer(&p->paged_ws, &p->paged_ws_bytes,
+                               cut + ml + rows * HEAD_DIM * sizeof(float), stream,
+                               "paged attention workspace allocation");
+  if (rc) return rc;
   char* ws = static_cast<char*>(p->paged_ws);
-  prm->counters = reinterpret_cast<int*>(ws);
-  prm->part_ml = reinterpret_cast<float2*>(ws + counters);
-  prm->part = reinterpret_cast<float*>(ws + counters + ml);
+  prm->cut = reinterpret_cast<paged::CutTile*>(ws);
+  prm->part_ml = reinterpret_cast<float2*>(ws + cut);
+  prm->part = reinterpret_cast<float*>(ws + cut + ml);
   return GEMM_F16_OK;
 }
 
@@ -159,6 +150,22 @@ int encode_q(gemm_f16_plan_s* p, CUtensorMap* map, const void* ptr, int total_q,
                                  stride_bytes(st[0], total_q, HEAD_DIM)};
   const cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)tokens};
   return encode(p, key, map, 3, ptr, dims, strides, box);
+}
+
+// The merge of the tiles that `workers` cut.
+int launch_merge(void (*kernel)(const paged::Params), const char* what, int workers, int parts,
+                 int threads, cudaStream_t stream, const paged::Params& prm) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)workers, (unsigned)parts, 1);
+  cfg.blockDim = dim3((unsigned)threads, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute pdl;
+  pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &pdl;
+  cfg.numAttrs = 1;
+  GF16_CUDA(cudaLaunchKernelEx(&cfg, kernel, prm), what);
+  return GEMM_F16_OK;
 }
 
 using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap,
@@ -276,7 +283,7 @@ int attn_f16_paged_fwd(gemm_f16_plan_t p, int batch, int total_q, int max_q, int
   if ((rc = ensure_workspace(p, st, &prm))) return rc;
   CUtensorMap tmQ, tmK, tmV;
   const int page_rows = page_size & -page_size;   // the largest power of two in it
-  const int64_t rows = (int64_t)max_q * prm.group;
+  const int64_t rows = std::max<int64_t>(1, (int64_t)max_q * prm.group);
   // Requests of up to SMALL_ROWS rows (new tokens x group) are bound by
   // reading the cache and go to the small kernel, with room for the rows
   // that the step's largest has (16, 32 or 64).  Where some may be larger,
@@ -301,7 +308,13 @@ int attn_f16_paged_fwd(gemm_f16_plan_t p, int batch, int total_q, int max_q, int
     const int threads = n == 16 ? Cfg<16>::THREADS : (n == 32 ? Cfg<32>::THREADS : Cfg<64>::THREADS);
     const size_t smem = n == 16 ? Cfg<16>::SMEM : (n == 32 ? Cfg<32>::SMEM : Cfg<64>::SMEM);
     if ((rc = launch(p, kernel, "launch paged_small_kernel", ctas, threads, smem, st, tmQ, tmK,
-                     tmV, prm)))
+                     tmV, prm)) ||
+        (rc = launch_merge(n == 16 ? paged_small_merge_kernel<16>
+                                   : (n == 32 ? paged_small_merge_kernel<32>
+                                              : paged_small_merge_kernel<64>),
+                           "launch paged_small_merge_kernel", ctas,
+                           (int)ceil_div(std::min<int64_t>(n, rows), MERGE_ROWS), MERGE_THREADS,
+                           st, prm)))
       return rc;
     prm.skip_tokens = prm.tile_tokens;
   }
@@ -318,7 +331,9 @@ int attn_f16_paged_fwd(gemm_f16_plan_t p, int batch, int total_q, int max_q, int
     int pairs = p->paged_pairs;
     if (p->sm_limit > 0) pairs = std::max(1, std::min(pairs, p->sm_limit / 2));
     if ((rc = launch(p, paged_large_kernel, "launch paged_large_kernel", 2 * pairs, NUM_THREADS,
-                     SMEM_BYTES, st, tmQ, tmK, tmV, prm)))
+                     SMEM_BYTES, st, tmQ, tmK, tmV, prm)) ||
+        (rc = launch_merge(paged_large_merge_kernel, "launch paged_large_merge_kernel", pairs,
+                           PART_ROWS / 32, MERGE_THREADS, st, prm)))
       return rc;
   }
   return GEMM_F16_OK;

@@ -19,8 +19,7 @@
 //            keys that its row sees.
 //   dealing  the pairs get equal shares of the step's key blocks, whatever
 //            the lengths (causal tiles differ in cost); a tile that is cut
-//            leaves FP32 partials, and of each 32 rows the last warp to
-//            finish adds them up, counted as in the small kernel.
+//            leaves FP32 partials that a second kernel merges.
 // Barriers and signals are those of attn_pair.cuh.
 #pragma once
 
@@ -81,9 +80,8 @@ constexpr uint32_t IDESC_QK = (1u << 4) | ((uint32_t)(BKV >> 3) << 17) | ((uint3
 constexpr uint32_t IDESC_PV =
     (1u << 4) | (1u << 16) | ((uint32_t)(HD >> 3) << 17) | ((uint32_t)(2 * CQ >> 4) << 24);
 
-// Row r of the pair's partial of a slot; counters per slot, CTA and 32 rows.
+// Rows of a pair's partial.
 constexpr int PART_ROWS = 2 * CQ;
-constexpr int COUNTERS = 2 * EP_WARPS;
 
 struct Bars {
   uint32_t q_full, q_empty, full, empty, s_full, s_free, p_full, o_done, o_free, l_ready, l_free,
@@ -634,14 +632,9 @@ __device__ __forceinline__ void store_rows(const float (&f)[64], float factor,
 }
 
 // Per tile, each warp its 32 rows, a row per thread.  A tile that is the
-// cluster's alone: O out of tensor memory, normalised, to O.  Of a tile that
-// is cut, the last warp to finish these 32 rows adds its own part, still in
-// tensor memory, to those that the others left in the workspace; they are
-// written as [number / 4][row][4], so that a thread finds its own row's
-// numbers beside the other threads'.  (The part of a tile's end is done at the
-// beginning of a cluster's share and that of its beginning at the end of the
-// one before, so the merge mostly reads one part that has been there for long.)
-// The parts are added in their order, whoever adds them.
+// cluster's alone: O out of tensor memory, normalised, to O.  A part of a tile
+// that is cut: to the workspace, unnormalised, as [number / 4][row][4], so
+// that the threads of a warp write (and the merge reads) 512 bytes together.
 __device__ __forceinline__ void epilogue_role(const Params& p, const Sched& sc, Walk& walk,
                                               uint8_t* smem, uint32_t base, uint32_t tmem_base,
                                               const Bars& b, const float* l_rows, uint32_t rank,
@@ -680,10 +673,7 @@ __device__ __forceinline__ void epilogue_role(const Params& p, const Sched& sc, 
 #pragma unroll
     for (int i = 0; i < 64; ++i) f[i] = __uint_as_float(o[i]);
   };
-  auto part_of = [&](int slot, int cc) {   // its 16 pieces are 32 float4 apart
-    return reinterpret_cast<float4*>(p.part + ((int64_t)slot * PART_ROWS + sub * 32) * HD) +
-           cc * 16 * 32 + lane;
-  };
+  if (sub == 0 && lane == 0) p.cut[cluster].last = -1;
   while (walk.next()) {
     const int head = walk.cur_head;
     const bool more = walk.more();
@@ -717,78 +707,80 @@ __device__ __forceinline__ void epilogue_role(const Params& p, const Sched& sc, 
       }
       continue;
     }
-    const long long L = walk.line();
-    const int c0 = (int)(L / sc.per), c1 = (int)((L + walk.s.nb - 1) / sc.per);
-    const int first = part_slot(L, sc.per, c0), own = part_slot(L, sc.per, cluster);
-    int* counter = p.counters + first * COUNTERS + sub;
-    int before = 0;
-    if (lane == 0) before = atomicAdd(counter, 0);
-    before = __shfl_sync(0xffffffffu, before, 0);
-    bool in_tmem = before == c1 - c0;      // all the others are there
-    if (!in_tmem) {
-      if (ok) {
-        __stcg(p.part_ml + (int64_t)own * PART_ROWS + sub * 32 + lane, make_float2(m, l));
-#pragma unroll 1
-        for (int cc = 0; cc < HD / 64; ++cc) {
-          float f[64];
-          load_o(cc, more, f);
-          float4* dst = part_of(own, cc);
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            __stcg(dst + i * 32, make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]));
-        }
-      }
-      __threadfence();
-      __syncwarp();
-      if (lane == 0) before = atomicAdd(counter, 1);
-      before = __shfl_sync(0xffffffffu, before, 0);
-      if (before != c1 - c0) continue;
-    }
-    if (lane == 0) *counter = 0;
     if (!ok) continue;
-    __threadfence();
-    auto ml_of = [&](int c) {
-      if (in_tmem && c == cluster) return make_float2(m, l);
-      const int slot = c == c0 ? first : 2 * c;
-      return __ldcg(p.part_ml + (int64_t)slot * PART_ROWS + sub * 32 + lane);
-    };
-    float mx = NO_OFFSET, sum = 0.f;
-    for (int c = c0; c <= c1; ++c) mx = fmaxf(mx, ml_of(c).x);
-    for (int c = c0; c <= c1; ++c) {
-      const float2 ml = ml_of(c);
-      sum = fmaf(ptx::ex2_approx(ml.x - mx), ml.y, sum);
-    }
-    const float inv_l = sum > 0.f ? 1.f / sum : 0.f;
+    const long long L = walk.line();
+    const int own = part_slot(L, sc.per, cluster);
+    __stcg(p.part_ml + (int64_t)own * PART_ROWS + sub * 32 + lane, make_float2(m, l));
 #pragma unroll 1
     for (int cc = 0; cc < HD / 64; ++cc) {
-      float acc[64];
+      float f[64];
+      load_o(cc, more, f);
+      float4* dst = reinterpret_cast<float4*>(p.part + ((int64_t)own * PART_ROWS + sub * 32) * HD) +
+                    cc * 16 * 32 + lane;
 #pragma unroll
-      for (int i = 0; i < 64; ++i) acc[i] = 0.f;
-#pragma unroll 1
-      for (int c = c0; c <= c1; ++c) {
-        const float w = ptx::ex2_approx(ml_of(c).x - mx);
-        if (in_tmem && c == cluster) {
-          float f[64];
-          load_o(cc, more, f);
-#pragma unroll
-          for (int i = 0; i < 64; ++i) acc[i] = fmaf(w, f[i], acc[i]);
-        } else {
-          const float4* src = part_of(c == c0 ? first : 2 * c, cc);
-          float4 v[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = __ldcg(src + i * 32);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            acc[4 * i] = fmaf(w, v[i].x, acc[4 * i]);
-            acc[4 * i + 1] = fmaf(w, v[i].y, acc[4 * i + 1]);
-            acc[4 * i + 2] = fmaf(w, v[i].z, acc[4 * i + 2]);
-            acc[4 * i + 3] = fmaf(w, v[i].w, acc[4 * i + 3]);
-          }
-        }
-      }
-      store_rows(acc, inv_l, box, box_rows, lane, row_off, rows, dst0, cc);
+      for (int i = 0; i < 16; ++i)
+        __stcg(dst + i * 32, make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]));
+    }
+    if (sub == 0 && lane == 0 && L >= sc.w0 && walk.j1 < walk.s.nb) {
+      CutTile t = {};
+      t.last = (int)((L + walk.s.nb - 1) / sc.per);
+      t.first = own;
+      t.token = walk.r.start + walk.i0;
+      t.tokens = walk.cnt;
+      t.head = head;
+      p.cut[cluster] = t;
     }
   }
+}
+
+// Merges the cut tiles: block (w, y) rows 32y .. 32y + 31 of the pair's tile
+// that worker w began and others ended; a lane a row, a warp sixteen numbers of
+// each.  Launched behind the kernel below, whose end it waits for.
+constexpr int MERGE_THREADS = 512;
+__global__ void __launch_bounds__(MERGE_THREADS) paged_large_merge_kernel(const Params p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int w = (int)blockIdx.x, sub = (int)blockIdx.y;
+  const int lane = (int)threadIdx.x & 31, warp = (int)threadIdx.x >> 5;
+  const CutTile t = p.cut[w];
+  const int cta_tokens = p.tile_tokens / 2, rank = sub / EP_WARPS;
+  const int tokens = imin(imax(t.tokens - rank * cta_tokens, 0), cta_tokens);
+  const int rr = (sub % EP_WARPS) * 32 + lane;            // row within the CTA's 128
+  if (t.last < 0 || (sub % EP_WARPS) * 32 >= tokens * p.group) return;
+  auto row0 = [&](int c) { return (int64_t)(c == w ? t.first : 2 * c) * PART_ROWS + sub * 32; };
+  float mx = NO_OFFSET;
+#pragma unroll 4
+  for (int c = w; c <= t.last; ++c) mx = fmaxf(mx, __ldcg(p.part_ml + row0(c) + lane).x);
+  float acc[16] = {}, sum = 0.f;
+#pragma unroll 4
+  for (int c = w; c <= t.last; ++c) {
+    const float2 ml = __ldcg(p.part_ml + row0(c) + lane);
+    const float4* src = reinterpret_cast<const float4*>(p.part + row0(c) * HD) + warp * 4 * 32 + lane;
+    float4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __ldcg(src + i * 32);
+    const float wgt = ptx::ex2_approx(ml.x - mx);
+    sum = fmaf(wgt, ml.y, sum);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      acc[4 * i] = fmaf(wgt, v[i].x, acc[4 * i]);
+      acc[4 * i + 1] = fmaf(wgt, v[i].y, acc[4 * i + 1]);
+      acc[4 * i + 2] = fmaf(wgt, v[i].z, acc[4 * i + 2]);
+      acc[4 * i + 3] = fmaf(wgt, v[i].w, acc[4 * i + 3]);
+    }
+  }
+  if (rr >= tokens * p.group) return;
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const int tok = rr / p.group;
+  uint4* dst = reinterpret_cast<uint4*>(
+      p.O + (int64_t)(t.token + rank * cta_tokens + tok) * p.o_tok +
+      (int64_t)(t.head * p.group + rr - tok * p.group) * p.o_head + warp * 16);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    dst[i] = make_uint4(pack_half2(acc[8 * i] * inv, acc[8 * i + 1] * inv),
+                        pack_half2(acc[8 * i + 2] * inv, acc[8 * i + 3] * inv),
+                        pack_half2(acc[8 * i + 4] * inv, acc[8 * i + 5] * inv),
+                        pack_half2(acc[8 * i + 6] * inv, acc[8 * i + 7] * inv));
 }
 
 // See attn_pair.cuh: completes every phase a copy warp opened and waits

@@ -25,15 +25,15 @@
 // row until a tile ends.
 //
 // A tile that is cut between CTAs: each writes its unnormalised FP32 O with
-// its offsets and sums, and the last to finish (a counter per tile, which it
-// sets back to zero) merges the parts in their order, so the result does not
-// depend on which CTA that is.
+// its offsets and sums, and a second kernel merges the parts in their order.
+// (A merge by the last CTA to finish, found with a counter, took 5 to 17 us at
+// the end of the kernel, where one CTA reads what all the others wrote; the
+// second launch takes 3 and spreads the rows over the GPU.)
 //
 // Barriers: q_full / q_empty, full[s] / empty[s] (ring of 32 KB: half a key
 // block by 128 numbers, then half a value block by 128 numbers), s_full[2],
 // p_full[2], o_done[2] (the O products of a block).  Every wait is bounded;
-// after an abort the roles stop issuing, the copies in flight are waited for,
-// and the counters are still served, so that a later call finds them at zero.
+// after an abort the roles stop issuing and the copies in flight are waited for.
 #pragma once
 
 namespace gf16 {
@@ -43,7 +43,18 @@ constexpr int HD = 256;
 constexpr float RESCALE_LOG2 = 8.f;
 constexpr float NO_OFFSET = -3.0e38f;   // offset of a row without a finite score
 
-// What both kernels get.
+// The tile whose blocks go on past a worker's share, having begun in it: what
+// the merge kernel needs (last < 0: there is none).
+struct CutTile {
+  int last;      // last worker with a part of it
+  int first;     // slot of its first part; worker c's is 2c after that
+  int token;     // row in O of its first token
+  int tokens;
+  int head;      // key/value head
+  int pad[3];
+};
+
+// What the kernels get.
 struct Params {
   int batch, total_q, max_q, q_heads, kv_heads, group;   // group: query heads per key/value head
   int num_pages, page_size, max_pages;
@@ -57,9 +68,9 @@ struct Params {
   int tile_tokens;                // tokens that a tile (small kernel: a request) can hold
   int skip_tokens;                // large kernel: requests with at most this many are not its own
   int zero_rows;                  // whether this launch writes the rows past the last request's
-  float* part;                    // partial O, FP32 [slot][row][256]
+  float* part;                    // partial O, FP32, a slot's rows together
   float2* part_ml;                // their offsets and sums [slot][row]
-  int* counters;
+  CutTile* cut;                   // [worker]
   int* status;
   unsigned long long timeout_ns;
   int fault_unit;                 // test only: CTA whose first ring fill gets no copy
@@ -141,7 +152,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, uint
 namespace small {
 
 constexpr int WIN = 192;                // requests kept in shared memory
-constexpr int MAX_GROUPS = 4;           // softmax groups, and counters per partial slot
 constexpr int COLS = 16;                // rows of the tile (columns of S^T) per softmax group
 constexpr uint32_t CHUNK = 128 * 128;   // 128 keys x 64 numbers: 16 KB
 constexpr uint32_t SLOT = 2 * CHUNK;
@@ -550,6 +560,7 @@ __global__ void __launch_bounds__(Cfg<N>::THREADS, 1)
     const float sl2 = p.scale_log2;
     if (p.zero_rows)
       zero_tail(p, cta * 4 * C::GROUPS + (int)warp - 2, ctas * 4 * C::GROUPS);
+    if (warp == 2 && lane == 0) p.cut[cta].last = -1;
     uint32_t g = 0;
     bool ok = true;
     while (walk.next()) {
@@ -706,74 +717,18 @@ __global__ void __launch_bounds__(Cfg<N>::THREADS, 1)
               __stcg(p.part_ml + (int64_t)slot * N + col0 + n, make_float2(m[n], l[n]));
         }
       }
+      if (ok && warp == 2 && lane == 0 && L >= sc.w0 && walk.j1 < walk.s.nb) {
+        CutTile t = {};
+        t.last = (int)((L + walk.s.nb - 1) / sc.per);
+        t.first = slot;
+        t.token = walk.r.start;
+        t.tokens = walk.r.n;
+        t.head = head;
+        p.cut[cta] = t;
+      }
       // The next tile's first O product overwrites O; it follows this
       // thread's next arrival on p_full.
       ptx::tc_fence_before();
-      if (!whole) {
-        // Whichever CTA's group comes last merges the group's rows.
-        const int c0 = (int)(L / sc.per), c1 = (int)((L + walk.s.nb - 1) / sc.per);
-        const int first = part_slot(L, sc.per, c0);
-        __threadfence();
-        group_sync(grp);
-        bool last = false;
-        if (key_row == 0) {
-          int* counter = p.counters + first * MAX_GROUPS + grp;
-          last = atomicAdd(counter, 1) == c1 - c0;
-          if (last) *counter = 0;
-        }
-        if (group_or(grp, last)) {
-          __threadfence();
-          // One warp per row, eight numbers per lane.
-          for (int n = (int)quarter; n < rows; n += 4) {
-            const int64_t at = col0 + n;
-            float mx = NO_OFFSET;
-            for (int c = c0 + (int)lane; c <= c1; c += 32) {
-              const int sl = c == c0 ? first : 2 * c;
-              mx = fmaxf(mx, __ldcg(p.part_ml + (int64_t)sl * N + at).x);
-            }
-            mx = warp_max(mx);
-            float sum = 0.f, acc[8] = {};
-            for (int cb = c0; cb <= c1; cb += 32) {
-              float wgt = 0.f;
-              if (cb + (int)lane <= c1) {
-                const int c = cb + (int)lane, sl = c == c0 ? first : 2 * c;
-                const float2 ml = __ldcg(p.part_ml + (int64_t)sl * N + at);
-                wgt = ptx::ex2_approx(ml.x - mx);
-                sum += wgt * ml.y;
-              }
-              const int cnt = imin(32, c1 - cb + 1);
-#pragma unroll 4
-              for (int i = 0; i < cnt; ++i) {
-                const int c = cb + i, sl = c == c0 ? first : 2 * c;
-                const float wi = __shfl_sync(0xffffffffu, wgt, i);
-                const float4* src =
-                    reinterpret_cast<const float4*>(p.part + ((int64_t)sl * N + at) * HD) + lane * 2;
-                const float4 a = __ldcg(src), b = __ldcg(src + 1);
-                acc[0] = fmaf(wi, a.x, acc[0]);
-                acc[1] = fmaf(wi, a.y, acc[1]);
-                acc[2] = fmaf(wi, a.z, acc[2]);
-                acc[3] = fmaf(wi, a.w, acc[3]);
-                acc[4] = fmaf(wi, b.x, acc[4]);
-                acc[5] = fmaf(wi, b.y, acc[5]);
-                acc[6] = fmaf(wi, b.z, acc[6]);
-                acc[7] = fmaf(wi, b.w, acc[7]);
-              }
-            }
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-            const float inv = sum > 0.f ? 1.f / sum : 0.f;
-            const int tok = (int)at / p.group;
-            uint4 out;
-            out.x = pack_half2(acc[0] * inv, acc[1] * inv);
-            out.y = pack_half2(acc[2] * inv, acc[3] * inv);
-            out.z = pack_half2(acc[4] * inv, acc[5] * inv);
-            out.w = pack_half2(acc[6] * inv, acc[7] * inv);
-            *reinterpret_cast<uint4*>(p.O + (int64_t)(walk.r.start + tok) * p.o_tok +
-                                      (int64_t)(head * p.group + (int)at - tok * p.group) * p.o_head +
-                                      lane * 8) = out;
-          }
-        }
-      }
     }
   }
 
@@ -789,6 +744,71 @@ __global__ void __launch_bounds__(Cfg<N>::THREADS, 1)
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, C::TMEM_COLS);
   }
+}
+
+// Merges the cut tiles: block (w, y) rows 4y .. 4y + 3 of the tile that
+// worker w began and others ended.  Four warps per row share its parts; a
+// lane has eight numbers.  Launched behind the kernel above, whose end it
+// waits for.
+constexpr int MERGE_ROWS = 4, MERGE_SHARE = 4;
+constexpr int MERGE_THREADS = 32 * MERGE_ROWS * MERGE_SHARE;
+
+template <int N>
+__global__ void __launch_bounds__(MERGE_THREADS) paged_small_merge_kernel(const Params p) {
+  __shared__ float part_sum[MERGE_SHARE][MERGE_ROWS][32][9];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int w = (int)blockIdx.x, lane = (int)threadIdx.x & 31, warp = (int)threadIdx.x >> 5;
+  const int in = warp % MERGE_ROWS, share = warp / MERGE_ROWS;
+  const int n = (int)blockIdx.y * MERGE_ROWS + in;       // row of the tile
+  const CutTile t = p.cut[w];
+  const int rows = t.tokens * p.group;
+  if (t.last < 0 || (int)blockIdx.y * MERGE_ROWS >= rows) return;   // all of the block
+  auto slot = [&](int c) { return (int64_t)(c == w ? t.first : 2 * c); };
+  float acc[8] = {}, sum = 0.f;
+  if (n < rows) {
+    float mx = NO_OFFSET;
+    for (int c = w + lane; c <= t.last; c += 32)
+      mx = fmaxf(mx, __ldcg(p.part_ml + slot(c) * N + n).x);
+    mx = warp_max(mx);
+#pragma unroll 4
+    for (int c = w + share; c <= t.last; c += MERGE_SHARE) {
+      const float2 ml = __ldcg(p.part_ml + slot(c) * N + n);
+      const float4* src = reinterpret_cast<const float4*>(p.part + (slot(c) * N + n) * HD) + lane * 2;
+      const float4 a = __ldcg(src), b = __ldcg(src + 1);
+      const float wgt = ptx::ex2_approx(ml.x - mx);
+      sum = fmaf(wgt, ml.y, sum);
+      acc[0] = fmaf(wgt, a.x, acc[0]);
+      acc[1] = fmaf(wgt, a.y, acc[1]);
+      acc[2] = fmaf(wgt, a.z, acc[2]);
+      acc[3] = fmaf(wgt, a.w, acc[3]);
+      acc[4] = fmaf(wgt, b.x, acc[4]);
+      acc[5] = fmaf(wgt, b.y, acc[5]);
+      acc[6] = fmaf(wgt, b.z, acc[6]);
+      acc[7] = fmaf(wgt, b.w, acc[7]);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) part_sum[share][in][lane][k] = acc[k];
+  part_sum[share][in][lane][8] = sum;
+  __syncthreads();
+  if (share != 0 || n >= rows) return;
+#pragma unroll
+  for (int o = 1; o < MERGE_SHARE; ++o) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) acc[k] += part_sum[o][in][lane][k];
+    sum += part_sum[o][in][lane][8];
+  }
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const int tok = n / p.group;
+  uint4 out;
+  out.x = pack_half2(acc[0] * inv, acc[1] * inv);
+  out.y = pack_half2(acc[2] * inv, acc[3] * inv);
+  out.z = pack_half2(acc[4] * inv, acc[5] * inv);
+  out.w = pack_half2(acc[6] * inv, acc[7] * inv);
+  *(reinterpret_cast<uint4*>(p.O + (int64_t)(t.token + tok) * p.o_tok +
+                             (int64_t)(t.head * p.group + n - tok * p.group) * p.o_head) + lane) =
+      out;
 }
 
 }  // namespace small

@@ -108,6 +108,17 @@ py::object done(int rc, py::object result) {
   return rc < 0 ? py::object(py::int_(rc)) : std::move(result);
 }
 
+// Numbers at .. at + n - 1 of a one-dimensional tensor, as narrow() gives them
+// but without the dispatcher (five of these are most of a call's time with it).
+Tensor piece(const Tensor& x, int64_t at, int64_t n) {
+  const int64_t one = 1;
+  Tensor t = at::detail::make_tensor<c10::TensorImpl>(
+      c10::TensorImpl::VIEW, c10::Storage(x.storage()), x.key_set(), x.dtype());
+  t.unsafeGetTensorImpl()->set_sizes_and_strides(c10::IntArrayRef(&n, 1),
+                                                 c10::IntArrayRef(one), x.storage_offset() + at);
+  return t;
+}
+
 // -> (starts, kv_lens, positions, slots, free_head), or an error code.
 py::object paged_maps(int64_t plan, int device, const Tensor& cached, const Tensor& added,
                       const Tensor& table, const Tensor& free_pages, const Tensor& free_head,
@@ -143,11 +154,11 @@ py::object paged_maps(int64_t plan, int device, const Tensor& cached, const Tens
     // One allocation; positions and slots begin at 16-byte boundaries.
     const int64_t room = (most + 3) / 4 * 4;
     const Tensor buf = at::empty({2 * room + 2 * batch + 2}, cached.options());
-    positions = buf.narrow(0, 0, most);
-    slots = buf.narrow(0, room, most);
-    starts = buf.narrow(0, 2 * room, batch + 1);
-    lens = buf.narrow(0, 2 * room + batch + 1, batch);
-    head = buf.narrow(0, 2 * room + 2 * batch + 1, 1);
+    positions = piece(buf, 0, most);
+    slots = piece(buf, room, most);
+    starts = piece(buf, 2 * room, batch + 1);
+    lens = piece(buf, 2 * room + batch + 1, batch);
+    head = piece(buf, 2 * room + 2 * batch + 1, 1);
   }
   const int rc = attn_f16_paged_maps(
       plan_of(plan), narrow(batch, "batch"), ints(cached), ints(added), ints_out(table),

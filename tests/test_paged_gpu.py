@@ -574,9 +574,8 @@ def test_step_in_a_graph(g, plan):
 @pytest.mark.parametrize("lens", [[(500, 1), (900, 1)], [(500, 3), (900, 700)], [(500, 400)]],
                          ids=["few", "both", "many"])
 def test_attention_bounded_wait(g, lens):
-    """The first copy of worker 0 is left out (the test-only fault option):
-    the call must end with ERR_TIMEOUT, and the next ones, which find the
-    tile counters where the failed call left them, must be right."""
+    """The first copy of worker 0 or 1 is left out (the test-only fault option):
+    the call must end with ERR_TIMEOUT, and the next ones must be right."""
     pr = ref.PagedProblem(lens, 8, 2, 16, seed=13)
     with g.Plan(0) as own:
         run_attention(g, own, pr)
