@@ -406,7 +406,9 @@ __device__ __forceinline__ void mma_role(const Params& p, Walk& walk, uint32_t b
                                          uint32_t tmem_base, const Bars& b,
                                          volatile int* abort_flag) {
   RingPos kpos{0, 0}, vpos{0, 0};
-  const uint32_t q_addr = base + OFF_Q;
+  const uint32_t q_low = desc_low(base + OFF_Q, 16);
+  const uint32_t k_ring = desc_low(base + OFF_RING, 16);
+  const uint32_t v_ring = desc_low(base + OFF_RING + RING * SLOT_BYTES, V_CHUNK);
   const uint32_t o_tmem = tmem_base + O_COL;
   auto issue_qk = [&](uint32_t gs, bool last_of_tile) -> bool {
     if (gs > 0) {
@@ -415,13 +417,13 @@ __device__ __forceinline__ void mma_role(const Params& p, Walk& walk, uint32_t b
     if (!wait_suspend(b.full + 8 * kpos.stage, consumer_wait_parity(kpos), p, abort_flag))
       return false;
     ptx::tc_fence_after();
-    const uint32_t k_addr = base + OFF_RING + kpos.stage * SLOT_BYTES;
+    const uint32_t k_low = k_ring + kpos.stage * (SLOT_BYTES >> 4);
 #pragma unroll
     for (int kk = 0; kk < HD / 16; ++kk) {
       const uint32_t off_q = (uint32_t)(kk >> 2) * CHUNK_Q + (uint32_t)(kk & 3) * 32u;
       const uint32_t off_k = (uint32_t)(kk >> 2) * K_CHUNK + (uint32_t)(kk & 3) * 32u;
-      ptx::mma_f16_pair(tmem_base + S_COL, smem_desc_sw128(q_addr + off_q, 16, 1024),
-                        smem_desc_sw128(k_addr + off_k, 16, 1024), IDESC_QK, kk > 0 ? 1u : 0u);
+      ptx::mma_f16_pair(tmem_base + S_COL, desc(q_low + off_q / 16), desc(k_low + off_k / 16),
+                        IDESC_QK, kk > 0 ? 1u : 0u);
     }
     ptx::mma_commit_pair(b.empty + 8 * kpos.stage, 0x3);
     ptx::mma_commit_pair(b.s_full, 0x3);
@@ -453,12 +455,12 @@ __device__ __forceinline__ void mma_role(const Params& p, Walk& walk, uint32_t b
         break;
       }
       ptx::tc_fence_after();
-      const uint32_t v_addr = base + OFF_RING + (RING + vpos.stage) * SLOT_BYTES;
+      const uint32_t v_low = v_ring + vpos.stage * (SLOT_BYTES >> 4);
       const uint32_t p_tmem = tmem_base + P_COL + pb * (BKV / 2);
 #pragma unroll
       for (int kk = 0; kk < BKV / 16; ++kk)
         ptx::mma_f16_pair_tmem_a(o_tmem, p_tmem + (uint32_t)kk * 8u,
-                                 smem_desc_sw128(v_addr + (uint32_t)kk * 2048u, V_CHUNK, 1024),
+                                 desc(v_low + (uint32_t)kk * 128u),
                                  IDESC_PV, (j > 0 || kk > 0) ? 1u : 0u);
       ptx::mma_commit_pair(b.empty + 8 * (RING + vpos.stage), 0x3);
       ptx::mma_commit_pair(b.o_done + 8 * pb, 0x3);

@@ -112,6 +112,20 @@ __device__ __forceinline__ void zero_tail(const Params& p, int worker, int worke
   }
 }
 
+// Shared-memory matrix descriptors (common.cuh, smem_desc_sw128) as two words:
+// within a tile only the address in the low word moves, by a constant per MMA.
+// Built from scratch each time, 24 pairs of them were half of the MMA thread's
+// time for a block.
+constexpr uint32_t DESC_HIGH = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_low(uint32_t saddr, uint32_t lbo) {
+  return ((saddr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16);
+}
+__device__ __forceinline__ uint64_t desc(uint32_t low) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(low), "r"(DESC_HIGH));
+  return d;
+}
+
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&h);
@@ -490,6 +504,7 @@ __global__ void __launch_bounds__(Cfg<N>::THREADS, 1)
       RingPos pos{0, 0};
       bool ok = true;
       uint32_t g0 = 0, tiles = 0;     // blocks and tiles done
+      const uint32_t ring_low = desc_low(base + C::OFF_RING, 0);
       while (ok && walk.next()) {
         const uint32_t nb = (uint32_t)(walk.j1 - walk.j0);
         ok = wait_phase(q_full, tiles & 1u, p, abort_flag);
@@ -498,14 +513,14 @@ __global__ void __launch_bounds__(Cfg<N>::THREADS, 1)
             if (!wait_phase(full + 8 * pos.stage, consumer_wait_parity(pos), p, abort_flag))
               return false;
             ptx::tc_fence_after();
-            const uint32_t k_addr = base + C::OFF_RING + pos.stage * SLOT;
-            const uint32_t q_addr = base + C::OFF_Q + (uint32_t)half * 2u * C::Q_CHUNK;
+            const uint32_t k_low = ring_low + pos.stage * (SLOT >> 4) + (1u << 16);   // LBO 16
+            const uint32_t q_low =
+                desc_low(base + C::OFF_Q + (uint32_t)half * 2u * C::Q_CHUNK, 16);
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
               ptx::mma_f16(tmem + C::S_COL + (gs & 1u) * N,
-                           smem_desc_sw128(k_addr + (kk >> 2) * CHUNK + (kk & 3) * 32u, 16, 1024),
-                           smem_desc_sw128(q_addr + (kk >> 2) * C::Q_CHUNK + (kk & 3) * 32u, 16,
-                                           1024),
+                           desc(k_low + ((kk >> 2) * CHUNK + (kk & 3) * 32u) / 16),
+                           desc(q_low + ((kk >> 2) * C::Q_CHUNK + (kk & 3) * 32u) / 16),
                            C::IDESC_S, (half > 0 || kk > 0) ? 1u : 0u);
             ptx::mma_commit(empty + 8 * pos.stage);
             ring_advance(pos, C::RING);
@@ -523,14 +538,13 @@ __global__ void __launch_bounds__(Cfg<N>::THREADS, 1)
             ok = wait_phase(full + 8 * pos.stage, consumer_wait_parity(pos), p, abort_flag);
             if (!ok) break;
             ptx::tc_fence_after();
-            const uint32_t v_addr = base + C::OFF_RING + pos.stage * SLOT;
-            const uint32_t p_addr = base + C::OFF_P + pb * C::P_BYTES;
+            const uint32_t v_low = ring_low + pos.stage * (SLOT >> 4) + ((CHUNK >> 4) << 16);
+            const uint32_t p_low = desc_low(base + C::OFF_P + pb * C::P_BYTES, 16);
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)   // 16 keys each
               ptx::mma_f16(tmem + C::O_COL + (uint32_t)half * N,
-                           smem_desc_sw128(v_addr + (uint32_t)kk * 2048u, CHUNK, 1024),
-                           smem_desc_sw128(p_addr + (kk >> 2) * C::P_CHUNK + (kk & 3) * 32u, 16,
-                                           1024),
+                           desc(v_low + (uint32_t)kk * 128u),
+                           desc(p_low + ((kk >> 2) * C::P_CHUNK + (kk & 3) * 32u) / 16),
                            C::IDESC_O, (j > 0 || kk > 0) ? 1u : 0u);
             ptx::mma_commit(empty + 8 * pos.stage);
             ring_advance(pos, C::RING);
