@@ -131,7 +131,14 @@ int attn_f16_validate(int batch, int heads, int seq_q, int seq_kv, int head_dim,
  *
  * Every call below is asynchronous on `stream` and can be captured into a
  * CUDA graph (attn_f16_paged_fwd after one eager call on the plan, which
- * allocates its workspace).
+ * allocates its workspace: partial sums of tiles of queries that are cut
+ * between workers, about 40 MB on a GB300 whatever the step).  The maps and
+ * the rotation are one kernel launch each, the attention two (its kernel and
+ * the merge of cut tiles) or, where some requests may have many new tokens and
+ * others few, four.  GEMM_F16_OPT_SM_LIMIT bounds the attention's kernels,
+ * GEMM_F16_OPT_KERNEL_TIMING times them (not the merges),
+ * GEMM_F16_OPT_FAULT_UNIT names the CTA or CTA pair whose first key copy is
+ * left out; results do not depend on the number of SMs beyond rounding.
  */
 
 /*
@@ -233,8 +240,8 @@ int attn_f16_rope_turns(const double *radians, int n, uint64_t *turns);
  * reads key/value head h / (q_heads / kv_heads):
  *     O[t,h,:] = sum_j softmax_j(scale * Q[t,h,:] . K[j,:]) * V[j,:]
  * FP32 scores, softmax statistics and accumulation, O rounded to binary16.
- * A row that sees no key (kv_lens[b] < n) is 0, and so are the rows from
- * starts[batch] to total_q - 1.  Rows of a page that no position of the
+ * A row that sees no key (kv_lens[b] < n), or only keys whose scores are -inf,
+ * is 0, and so are the rows from starts[batch] to total_q - 1.  Rows of a page that no position of the
  * request has reached, pages past it, and pages that no query of it sees
  * may hold anything (NaN included) and their table entries are not used;
  * an infinity or NaN in a V row that some queries of the request see and
