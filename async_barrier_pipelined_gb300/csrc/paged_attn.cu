@@ -55,7 +55,7 @@ int paged_plan_init(gemm_f16_plan_s* p, const cudaDeviceProp& prop) {
   int clusters = 0;
   GF16_CUDA(cudaOccupancyMaxActiveClusters(&clusters, paged::large::paged_large_kernel, &cfg),
             "cudaOccupancyMaxActiveClusters(paged attention kernel)");
-  p->paged_pairs = clusters > 1 ? clusters : 1;
+  p->paged_pairs = std::min(std::max(clusters, 1), paged::large::MAX_CLUSTERS);
   return GEMM_F16_OK;
 }
 

@@ -182,6 +182,29 @@ GF16_HD int64_t per_worker(int64_t blocks, int workers) {
   return lmax(1, (blocks + workers - 1) / workers);
 }
 
+// Where the large kernel deals out whole tiles first, as many of its `tiles` as
+// make full rounds of the workers but one, so that the rest (one to two rounds)
+// holds a tile for each of them; none with fewer than two rounds, or with more
+// tiles than its prologue should add up.
+constexpr int MOST_TILES = 16384;
+GF16_HD int whole_tiles(int tiles, int workers) {
+  return tiles > MOST_TILES || tiles < 2 * workers ? 0 : (tiles / workers - 1) * workers;
+}
+
+// The blocks of the rest bring every worker, `load` blocks of whole tiles before
+// it, to a common level, and are one at least for each.  Shares at the level
+// deal_level_enough are enough for the rest; where they are more than it, the
+// last workers give the difference up: worker c's share begins `before` blocks
+// (the shares of those before it) into the rest, or as far as leaves a block to
+// each worker from it on.
+GF16_HD int deal_share(int level, int load) { return imax(1, level - load); }
+GF16_HD int deal_level_enough(int most_load, int rest, int workers) {
+  return most_load + (rest + workers - 1) / workers;
+}
+GF16_HD int deal_start(int before, int rest, int workers, int c) {
+  return imin(before, rest - (workers - c));
+}
+
 // Partial sums: at most two per worker, of the tile that its range begins in
 // (slot 2w) and of the one that it ends in (slot 2w + 1) if that is another.
 // The parts of a tile whose blocks are L .. L + nb - 1 belong to the workers

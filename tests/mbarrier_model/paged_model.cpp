@@ -2,6 +2,7 @@
 // lengths, which blocks, pages and rows their copies touch, and which keys
 // their masks let through, against plain loops over every key.
 // Prints "ok <cases>" or the first thing that is wrong.
+#include <algorithm>
 #include <cstdio>
 #include <cstdlib>
 #include <map>
@@ -113,6 +114,69 @@ static void check_line(const std::vector<int>& tiles, int workers) {
   }
 }
 
+// Whole tiles in turn, the rest by blocks to a common level.
+static void check_deal(const std::vector<int>& tiles, int workers) {
+  const int n = (int)tiles.size(), whole = whole_tiles(n, workers);
+  CHECK(whole % workers == 0 && (whole == 0) == (n < 2 * workers || n > MOST_TILES));
+  if (whole == 0) return;
+  CHECK(n - whole >= workers && n - whole < 2 * workers);
+  std::vector<int> load(workers, 0), start(workers + 1);
+  int dealt = 0, rest = 0, biggest = 0;
+  for (int i = 0; i < n; ++i) {
+    biggest = std::max(biggest, tiles[i]);
+    if (i < whole) {
+      load[i % workers] += tiles[i];
+      dealt += tiles[i];
+    } else {
+      rest += tiles[i];
+    }
+  }
+  const int least = *std::min_element(load.begin(), load.end());
+  const int most = *std::max_element(load.begin(), load.end());
+  auto shares = [&](int level) {
+    int64_t sum = 0;
+    for (int l : load) sum += deal_share(level, l);
+    return sum;
+  };
+  int lo = least, hi = deal_level_enough(most, rest, workers);
+  CHECK(shares(hi) >= rest);
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (shares(mid) < rest) lo = mid; else hi = mid;
+  }
+  CHECK(shares(hi) >= rest);
+  int before = 0;
+  for (int c = 0; c < workers; ++c) {
+    start[c] = dealt + deal_start(before, rest, workers, c);
+    before += deal_share(hi, load[c]);
+  }
+  start[workers] = dealt + rest;
+  CHECK(start[0] == dealt);
+  for (int c = 0; c < workers; ++c) {
+    const int share = start[c + 1] - start[c];
+    CHECK(share >= 1);
+    CHECK(load[c] + share <= std::max(hi, most + 1));   // nobody is over the level
+  }
+  // Parts: slot 2c + 1 of the tile that worker c begins, 2c of one begun before.
+  std::map<int, int> slot_users;
+  int L = dealt;
+  for (int i = whole; i < n; L += tiles[i], ++i) {
+    int c0 = 0, done = 0;
+    while (start[c0 + 1] <= L) ++c0;
+    int last = c0;
+    while (start[last + 1] < L + tiles[i]) ++last;
+    CHECK(last < workers);
+    for (int c = c0; c <= last; ++c) {
+      const int a = std::max(L, start[c]), b = std::min(L + tiles[i], start[c + 1]);
+      CHECK(b > a);
+      done += b - a;
+      if (b - a < tiles[i]) CHECK(++slot_users[2 * c + (a == L ? 1 : 0)] == 1);
+      CHECK((a == L) == (c == c0));
+    }
+    CHECK(done == tiles[i]);
+  }
+}
+
 int main() {
   std::mt19937 rng(1);
   auto pick = [&](int a, int b) { return (int)(a + rng() % (unsigned)(b - a + 1)); };
@@ -130,6 +194,15 @@ int main() {
     std::vector<int> tiles(pick(1, 60));
     for (int& t : tiles) t = pick(1, pick(1, 3) == 1 ? 200 : 4);
     check_line(tiles, pick(1, 160));
+  }
+  for (int i = 0; i < 2000; ++i, ++cases) {
+    const int workers = pick(1, 128);
+    std::vector<int> tiles(pick(0, 5) == 0 ? pick(1, 300) : workers * pick(2, 9) + pick(-1, workers));
+    const int mode = pick(0, 3);
+    for (size_t t = 0; t < tiles.size(); ++t)
+      tiles[t] = mode == 0 ? 1 : mode == 1 ? pick(1, 300) : mode == 2 ? 1 + (int)t % 40
+                                                               : (t + 1 == tiles.size() ? 100000 : 1);
+    check_deal(tiles, workers);
   }
   const int edge[] = {-2147483647 - 1, -5, -1, 0, 1, 7, 100, 2147483000, 2147483647};
   for (int s0 : edge)

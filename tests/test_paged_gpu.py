@@ -604,6 +604,24 @@ def test_attention_sm_limit(g, limit):
             check(o, pr)
 
 
+@pytest.mark.parametrize("what", [
+    dict(lens=[(1300 + 37 * i, 700) for i in range(8)], q_heads=16, kv_heads=4, page=16),
+    dict(lens=[(3000, 400), (0, 1), (10, 0), (2000, 1111), (50, 3), (2500, 600)], q_heads=12,
+         kv_heads=6, page=64),
+    dict(lens=[(2500, 2500), (100, 1)], q_heads=8, kv_heads=4, page=24, window=1500, sinks=9),
+    dict(lens=[(1400 + i, 30) for i in range(300)], q_heads=8, kv_heads=1, page=32)],
+    ids=["many", "mixed", "window", "short queries"])
+@pytest.mark.parametrize("limit", [0, 6, 30])
+def test_attention_many_long_tiles(g, limit, what):
+    """Steps whose tiles are dealt out whole (with all workers or some of them)."""
+    with g.Plan(0) as own:
+        own.set_option(g.OPT_SM_LIMIT, limit)
+        pr = ref.PagedProblem(**what, seed=16)
+        o = run_attention(g, own, pr)
+        done(own)
+        check(o, pr)
+
+
 def test_attention_many_requests(g, plan):
     """More requests than the kernels keep in shared memory, empty ones among them."""
     for most in (1, 90):

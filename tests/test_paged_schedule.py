@@ -1,7 +1,7 @@
 """The integer arithmetic behind the attention over a paged cache
 (csrc/paged_schedule.h) against plain loops over every key, on the host: the
 clamping of lengths, the blocks and rows that copies touch, the masks, and
-the dealing out of blocks to workers (mbarrier_model/paged_model.cpp).  A
+the dealing out of blocks and whole tiles to workers (mbarrier_model/paged_model.cpp).  A
 planted mistake in the model must make it fail."""
 from __future__ import annotations
 
@@ -35,6 +35,8 @@ def test_schedule_holds(tmp_path):
 @pytest.mark.parametrize("right,wrong", [
     ("any |= sees(r.len - r.n + t, k, m);\n    CHECK", "any |= sees(r.len - r.n + t + 1, k, m);\n    CHECK"),
     ("CHECK(done == nb);", "CHECK(done == nb + 1);"),
+    ("load[c] + share <= std::max(hi, most + 1)", "load[c] + share < std::min(hi, most + 1)"),
+    ("if (shares(mid) < rest) lo", "if (shares(mid) < rest - workers - 9) lo"),
     ("v = sees(r.len - r.n + t, k, m);\n            any", "v = sees(r.len - r.n + t - 1, k, m);\n            any"),
 ])
 def test_a_planted_mistake_is_found(tmp_path, right, wrong):
