@@ -168,6 +168,12 @@ int launch_merge(void (*kernel)(const paged::Params), const char* what, int work
   return GEMM_F16_OK;
 }
 
+template <int N>
+auto merge_kernel(int rows) {
+  return rows == 2 ? paged::small::paged_small_merge_kernel<N, 2>
+                   : paged::small::paged_small_merge_kernel<N, 4>;
+}
+
 using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap,
                         const paged::Params);
 
@@ -307,14 +313,14 @@ int attn_f16_paged_fwd(gemm_f16_plan_t p, int batch, int total_q, int max_q, int
                                   : (n == 32 ? paged_small_kernel<32> : paged_small_kernel<64>);
     const int threads = n == 16 ? Cfg<16>::THREADS : (n == 32 ? Cfg<32>::THREADS : Cfg<64>::THREADS);
     const size_t smem = n == 16 ? Cfg<16>::SMEM : (n == 32 ? Cfg<32>::SMEM : Cfg<64>::SMEM);
+    const int per_block = merge_rows((int64_t)batch * kv_heads, ctas);
     if ((rc = launch(p, kernel, "launch paged_small_kernel", ctas, threads, smem, st, tmQ, tmK,
                      tmV, prm)) ||
-        (rc = launch_merge(n == 16 ? paged_small_merge_kernel<16>
-                                   : (n == 32 ? paged_small_merge_kernel<32>
-                                              : paged_small_merge_kernel<64>),
+        (rc = launch_merge(n == 16 ? merge_kernel<16>(per_block)
+                                   : (n == 32 ? merge_kernel<32>(per_block) : merge_kernel<64>(per_block)),
                            "launch paged_small_merge_kernel", ctas,
-                           (int)ceil_div(std::min<int64_t>(n, rows), MERGE_ROWS), MERGE_THREADS,
-                           st, prm)))
+                           (int)ceil_div(std::min<int64_t>(n, rows), per_block), MERGE_THREADS, st,
+                           prm)))
       return rc;
     prm.skip_tokens = prm.tile_tokens;
   }

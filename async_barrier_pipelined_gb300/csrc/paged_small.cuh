@@ -760,24 +760,30 @@ __global__ void __launch_bounds__(Cfg<N>::THREADS, 1)
   }
 }
 
-// Merges the cut tiles: block (w, y) rows 4y .. 4y + 3 of the tile that
-// worker w began and others ended.  Four warps per row share its parts; a
-// lane has eight numbers.  Launched behind the kernel above, whose end it
-// waits for.
-constexpr int MERGE_ROWS = 4, MERGE_SHARE = 4;
-constexpr int MERGE_THREADS = 32 * MERGE_ROWS * MERGE_SHARE;
+// Merges the cut tiles: block (w, y) rows ROWS * y .. ROWS * y + ROWS - 1 of
+// the tile that worker w began and others ended.  16 / ROWS warps per row share
+// its parts; a lane has eight numbers.  Launched behind the kernel above, whose
+// end it waits for.
+constexpr int MERGE_WARPS = 16, MERGE_THREADS = 32 * MERGE_WARPS;
+// Rows of a block.  Where a tile has few parts, four warps a row are enough and
+// fewer blocks are better (40 drafts under a window: 45.4 us; 49.0 with two
+// rows a block).  With fewer than a tile for every four workers the parts are
+// many, and the time is the reading of them by few SMs (one token over 100,000
+// keys of one head: 38.3 -> 34.7 us with two rows, 4 x 20,000 keys 26.2 -> 25.0).
+constexpr int merge_rows(int64_t tiles, int workers) { return tiles * 4 <= workers ? 2 : 4; }
 
-template <int N>
+template <int N, int ROWS>
 __global__ void __launch_bounds__(MERGE_THREADS) paged_small_merge_kernel(const Params p) {
-  __shared__ float part_sum[MERGE_SHARE][MERGE_ROWS][32][9];
+  constexpr int SHARE = MERGE_WARPS / ROWS;
+  __shared__ float part_sum[SHARE][ROWS][32][9];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int w = (int)blockIdx.x, lane = (int)threadIdx.x & 31, warp = (int)threadIdx.x >> 5;
-  const int in = warp % MERGE_ROWS, share = warp / MERGE_ROWS;
-  const int n = (int)blockIdx.y * MERGE_ROWS + in;       // row of the tile
+  const int in = warp % ROWS, share = warp / ROWS;
+  const int n = (int)blockIdx.y * ROWS + in;       // row of the tile
   const CutTile t = p.cut[w];
   const int rows = t.tokens * p.group;
-  if (t.last < 0 || (int)blockIdx.y * MERGE_ROWS >= rows) return;   // all of the block
+  if (t.last < 0 || (int)blockIdx.y * ROWS >= rows) return;   // all of the block
   auto slot = [&](int c) { return (int64_t)(c == w ? t.first : 2 * c); };
   float acc[8] = {}, sum = 0.f;
   if (n < rows) {
@@ -786,7 +792,7 @@ __global__ void __launch_bounds__(MERGE_THREADS) paged_small_merge_kernel(const 
       mx = fmaxf(mx, __ldcg(p.part_ml + slot(c) * N + n).x);
     mx = warp_max(mx);
 #pragma unroll 4
-    for (int c = w + share; c <= t.last; c += MERGE_SHARE) {
+    for (int c = w + share; c <= t.last; c += SHARE) {
       const float2 ml = __ldcg(p.part_ml + slot(c) * N + n);
       const float4* src = reinterpret_cast<const float4*>(p.part + (slot(c) * N + n) * HD) + lane * 2;
       const float4 a = __ldcg(src), b = __ldcg(src + 1);
@@ -808,7 +814,7 @@ __global__ void __launch_bounds__(MERGE_THREADS) paged_small_merge_kernel(const 
   __syncthreads();
   if (share != 0 || n >= rows) return;
 #pragma unroll
-  for (int o = 1; o < MERGE_SHARE; ++o) {
+  for (int o = 1; o < SHARE; ++o) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) acc[k] += part_sum[o][in][lane][k];
     sum += part_sum[o][in][lane][8];
