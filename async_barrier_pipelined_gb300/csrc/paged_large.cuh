@@ -657,8 +657,9 @@ __device__ __forceinline__ void mma_role(const Params& p, bool more, const volat
 }
 
 // ------------------------------------------------------------------ softmax
-// New exponent offset of one row for a key block (base-2 units): it moves
-// only when the block's maximum passes it by more than RESCALE_LOG2.
+// New exponent offset of one row for a key block (base-2 units): it moves, to
+// TAIL_LOG2 below the block's maximum, only when that passes it by more than
+// OVER_LOG2.
 __device__ __forceinline__ float block_offset(const uint32_t (&s)[BKV], float sl2, float m,
                                               float* alpha) {
   float r8[8];
@@ -675,14 +676,16 @@ __device__ __forceinline__ float block_offset(const uint32_t (&s)[BKV], float sl
 #pragma unroll
     for (int k = 1; k < 8; ++k) r8[0] = fminf(r8[0], r8[k]);
   }
-  const float mx = r8[0] * sl2;
-  const float m_new = (mx > m + RESCALE_LOG2) ? mx : m;
+  const float to = fmaf(r8[0], sl2, -TAIL_LOG2);
+  const float m_new = (to > m + (OVER_LOG2 - TAIL_LOG2)) ? to : m;
   *alpha = (m_new == m) ? 1.f : ptx::ex2_approx(m - m_new);
   return m_new;
 }
 
 // Weights 2^(sl2 s - m) as binary16 pairs (the product with V takes binary16;
-// half a step of 2^-11 each), and their FP32 sum before that rounding.
+// half a step each: 2^-11 of the weight, or 2^-25 below the normal range, which
+// TAIL_LOG2 keeps 2^-32 below the row's largest), and their FP32 sum before that
+// rounding.
 __device__ __forceinline__ float block_weights(const uint32_t (&s)[BKV], float sl2, float neg_m,
                                                uint32_t (&pk)[BKV / 2]) {
   float l4[4] = {0.f, 0.f, 0.f, 0.f};

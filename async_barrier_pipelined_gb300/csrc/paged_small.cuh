@@ -20,7 +20,7 @@
 // others (a thread that held all 64 rows of the widest tile spilled its
 // registers and took 13 us for a block).  Per block the threads only agree on
 // whether some score passed the exponent offset in use by more than
-// RESCALE_LOG2 (one barrier with an OR); only then do they take the block's
+// OVER_LOG2 (one barrier with an OR); only then do they take the block's
 // maximum, move the offset and rescale O.  Row sums stay one per thread and
 // row until a tile ends.
 //
@@ -40,7 +40,14 @@ namespace gf16 {
 namespace paged {
 
 constexpr int HD = 256;
-constexpr float RESCALE_LOG2 = 8.f;
+// Weights are 2^(score - offset), in FP32 for the row sum and rounded to binary16
+// for the product with V.  A new offset lies TAIL_LOG2 below the largest score
+// and stays until a score passes it by OVER_LOG2, so the row's largest weight is
+// 2^7 .. 2^15 (binary16 ends at 2^16) and a weight disappears from the product
+// only below 2^-25 / 2^7 = 2^-32 of it.  (With the offset at the largest score
+// the limit was 2^-25: a key that scores 2^25.5 times above 100,000 others took
+// half to all of their 0.2 % from O.)
+constexpr float TAIL_LOG2 = 7.f, OVER_LOG2 = 15.f;
 constexpr float NO_OFFSET = -3.0e38f;   // offset of a row without a finite score
 
 // The tile whose blocks go on past a worker's share, having begun in it: what
@@ -612,7 +619,7 @@ __global__ void __launch_bounds__(Cfg<N>::THREADS, 1)
             float x = __uint_as_float(s[n]) * sl2;
             if (!full_block) x = (n >= lo && n < hi) ? x : -INFINITY;
             s[n] = __float_as_uint(x);
-            over |= x > m[n] + RESCALE_LOG2;
+            over |= x > m[n] + OVER_LOG2;
           }
           // P buffer sb was last read by the O products of block g - 2.
           if (g >= 2 && !__all_sync(0xffffffffu, wait_phase(o_done + 8 * sb, ((g - 2) >> 1) & 1u, p,
@@ -635,7 +642,7 @@ __global__ void __launch_bounds__(Cfg<N>::THREADS, 1)
             for (int n = 0; n < COLS; ++n) {
               const float mx = fmaxf(fmaxf(red[n], red[COLS + n]),
                                      fmaxf(red[2 * COLS + n], red[3 * COLS + n]));
-              const float mn = mx > m[n] + RESCALE_LOG2 ? mx : m[n];
+              const float mn = mx > m[n] + OVER_LOG2 ? mx - TAIL_LOG2 : m[n];
               alpha[n] = ptx::ex2_approx(m[n] - mn);
               l[n] *= alpha[n];
               m[n] = mn;
@@ -660,7 +667,8 @@ __global__ void __launch_bounds__(Cfg<N>::THREADS, 1)
           for (int n = 0; n < COLS; ++n) {
             const float w = ptx::ex2_approx(__uint_as_float(s[n]) - m[n]);
             l[n] += w;
-            // The product with V takes binary16 weights (half a step of 2^-11 each).
+            // The product with V takes binary16 weights: half a step each, 2^-11 of
+            // the weight or 2^-25 below the normal range (see TAIL_LOG2).
             const unsigned short h = __half_as_ushort(__float2half_rn(w));
             asm volatile(
                 "st.shared.u16 [%0], %1;" ::"r"(p_buf + n * 128u + ((p_col ^ (n & 7)) << 4)), "h"(h)

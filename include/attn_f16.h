@@ -239,7 +239,9 @@ int attn_f16_rope_turns(const double *radians, int n, uint64_t *turns);
  * with window > 0 only those with j > p - window or j < sinks.  Query head h
  * reads key/value head h / (q_heads / kv_heads):
  *     O[t,h,:] = sum_j softmax_j(scale * Q[t,h,:] . K[j,:]) * V[j,:]
- * FP32 scores, softmax statistics and accumulation, O rounded to binary16.
+ * FP32 scores, softmax statistics and accumulation, O rounded to binary16.  The
+ * softmax weights are rounded to binary16 for the product with V (not for their
+ * sum): each is off by at most 2^-11 of itself, or 2^-32 of the row's largest.
  * A row that sees no key (kv_lens[b] < n), or only keys whose scores are -inf,
  * is 0, and so are the rows from starts[batch] to total_q - 1.  Rows of a page that no position of the
  * request has reached, pages past it, and pages that no query of it sees
