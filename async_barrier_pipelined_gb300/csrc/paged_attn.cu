@@ -289,7 +289,7 @@ int attn_f16_paged_fwd(gemm_f16_plan_t p, int batch, int total_q, int max_q, int
   if ((rc = ensure_workspace(p, st, &prm))) return rc;
   CUtensorMap tmQ, tmK, tmV;
   const int page_rows = page_size & -page_size;   // the largest power of two in it
-  const int64_t rows = std::max<int64_t>(1, (int64_t)max_q * prm.group);
+  const int64_t rows = std::max<int64_t>(1, max_q) * prm.group;   // room for a token at least
   // Requests of up to SMALL_ROWS rows (new tokens x group) are bound by
   // reading the cache and go to the small kernel, with room for the rows
   // that the step's largest has (16, 32 or 64).  Where some may be larger,
