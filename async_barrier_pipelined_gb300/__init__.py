@@ -36,7 +36,8 @@ __all__ = [
     "attn_f16_key_ranges", "gemm_f16_run_info", "gemm_f16_run_choice", "attn_f16_fwd_host", "attention_host",
     "attention", "ATTN_HEAD_DIM", "gemm_f16_kernel_time",
     "LAYOUT_NN", "LAYOUT_TN", "LAYOUT_NT", "LAYOUT_TT",
-    "ERR_BAD_INDEX", "attn_f16_paged_maps", "attn_f16_paged_maps_validate", "attn_f16_rope",
+    "ERR_BAD_INDEX", "attn_f16_paged_maps", "attn_f16_paged_maps_validate",
+    "attn_f16_paged_maps_overlap", "attn_f16_rope",
     "attn_f16_rope_validate", "attn_f16_rope_turns", "attn_f16_paged_fwd",
     "attn_f16_paged_validate", "ROPE_HALF", "ROPE_INTERLEAVED", "PagedMaps", "paged_maps",
     "rope_frequencies", "rope_turns", "rotary", "rotary_to_cache", "paged_attention",
@@ -132,6 +133,7 @@ _SIGNATURES = {
                                    _vp, ctypes.c_float, _vp]),
     "attn_f16_paged_maps": (_c_int, [_vp, *_MAPS_ARGS, _vp]),
     "attn_f16_paged_maps_validate": (_c_int, _MAPS_ARGS),
+    "attn_f16_paged_maps_overlap": (_c_int, _MAPS_ARGS[:9] + _MAPS_ARGS[10:]),
     "attn_f16_rope": (_c_int, [_vp] + [_c_int] * 7 + [ctypes.c_float, *_ROPE_TAIL, _vp]),
     "attn_f16_rope_validate": (_c_int, [_c_int] * 6 + [ctypes.c_float, *_ROPE_TAIL]),
     "attn_f16_rope_turns": (_c_int, [ctypes.POINTER(ctypes.c_double), _c_int,
@@ -517,6 +519,12 @@ def attn_f16_paged_maps_validate(*args) -> int:
     return load().attn_f16_paged_maps_validate(*args)
 
 
+def attn_f16_paged_maps_overlap(*args) -> int:
+    """Whether buffers of a maps call overlap (attn_f16_paged_maps_validate's
+    arguments without page_size)."""
+    return load().attn_f16_paged_maps_overlap(*args)
+
+
 def _i64s(values):
     return None if values is None else (_c_i64 * len(values))(*[int(x) for x in values])
 
@@ -624,7 +632,9 @@ def paged_maps(plan: Plan, cached, added, block_table, free_pages, free_head, pa
     (int32 [n]) at free_head (int32 [1]) and written into it.  Returns
     starts [batch + 1], kv_lens [batch], positions and slots [max_tokens]
     (0 and -1 past the last token) and the new free_head [1], written into
-    ``out`` (a PagedMaps of an earlier call) if given.
+    ``out`` (a PagedMaps of an earlier call) if given.  Nothing is advanced
+    in place: ``out`` may not hold a tensor that is also an input (its
+    kv_lens as ``cached``, its free_head as ``free_head``).
     """
     return PagedMaps._make(_result(
         (_calls or _torch_calls()).paged_maps(

@@ -382,6 +382,23 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const RopeParams p) 
 
 bool off(const void* p, uintptr_t mask) { return ((uintptr_t)p & mask) != 0; }
 
+// The 32-bit integers of a buffer that a call reads or writes.
+struct Ints {
+  const int32_t* at;
+  int64_t n;
+};
+bool meet(const Ints& a, const Ints& b) {
+  return a.n > 0 && b.n > 0 && a.at < b.at + b.n && b.at < a.at + a.n;
+}
+// Whether it meets one of a table's rows (`wide` entries, `stride` apart).
+bool meets_rows(const Ints& a, const int32_t* table, int rows, int64_t stride, int wide) {
+  if (a.n <= 0) return false;
+  const int64_t o = a.at - table;
+  if (o < 0) return o + a.n > 0;
+  const int64_t r = o / stride, in = o - r * stride;
+  return r < rows && (in < wide || (r + 1 < rows && a.n > stride - in));
+}
+
 // Strides of [a][b][256] or [a][b][c][256] storage: positive and at least a
 // head's length where the dimension's extent is above 1.
 int check_strides(const int64_t* st, const int* extent, int n) {
@@ -434,6 +451,29 @@ int attn_f16_paged_maps_validate(int batch, const int32_t* cached, const int32_t
   return GEMM_F16_OK;
 }
 
+int attn_f16_paged_maps_overlap(int batch, const int32_t* cached, const int32_t* added,
+                                const int32_t* block_table, int64_t table_stride, int max_pages,
+                                const int32_t* free_pages, int num_free, const int32_t* free_head,
+                                int max_tokens, const int32_t* starts, const int32_t* kv_lens,
+                                const int32_t* positions, const int32_t* slots,
+                                const int32_t* free_head_out) {
+  const Ints written[] = {{starts, (int64_t)batch + 1}, {kv_lens, batch}, {positions, max_tokens},
+                          {slots, max_tokens}, {free_head_out, 1}};
+  const Ints read[] = {{cached, batch}, {added, batch}, {free_pages, num_free}, {free_head, 1}};
+  const int n = sizeof(written) / sizeof(written[0]);
+  for (int i = 0; i < n; ++i) {
+    for (int j = i + 1; j < n; ++j)
+      if (meet(written[i], written[j])) return GEMM_F16_ERR_INVALID_ARG;
+    for (const Ints& r : read)
+      if (meet(written[i], r)) return GEMM_F16_ERR_INVALID_ARG;
+    if (meets_rows(written[i], block_table, batch, table_stride, max_pages))
+      return GEMM_F16_ERR_INVALID_ARG;
+  }
+  for (const Ints& r : read)
+    if (meets_rows(r, block_table, batch, table_stride, max_pages)) return GEMM_F16_ERR_INVALID_ARG;
+  return GEMM_F16_OK;
+}
+
 int attn_f16_paged_maps(gemm_f16_plan_t p, int batch, const int32_t* cached, const int32_t* added,
                         int32_t* block_table, int64_t table_stride, int max_pages,
                         const int32_t* free_pages, int num_free, const int32_t* free_head,
@@ -441,10 +481,14 @@ int attn_f16_paged_maps(gemm_f16_plan_t p, int batch, const int32_t* cached, con
                         int32_t* positions, int32_t* slots, int32_t* free_head_out,
                         gemm_f16_stream_t stream) {
   if (!p) return GEMM_F16_ERR_INVALID_ARG;
-  const int rc = attn_f16_paged_maps_validate(batch, cached, added, block_table, table_stride,
-                                              max_pages, free_pages, num_free, free_head,
-                                              page_size, max_tokens, starts, kv_lens, positions,
-                                              slots, free_head_out);
+  int rc = attn_f16_paged_maps_validate(batch, cached, added, block_table, table_stride, max_pages,
+                                        free_pages, num_free, free_head, page_size, max_tokens,
+                                        starts, kv_lens, positions, slots, free_head_out);
+  if (rc) return rc;
+  // Each block reads all lengths while others write: no buffer may serve twice.
+  rc = attn_f16_paged_maps_overlap(batch, cached, added, block_table, table_stride, max_pages,
+                                   free_pages, num_free, free_head, max_tokens, starts, kv_lens,
+                                   positions, slots, free_head_out);
   if (rc) return rc;
   DeviceGuard g(p->device);
   MapsParams prm;

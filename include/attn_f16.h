@@ -158,9 +158,13 @@ int attn_f16_validate(int batch, int heads, int seq_q, int seq_kv, int head_dim,
  *   block_table  batch rows of max_pages entries (1 .. 2^24), table_stride
  *                >= max_pages apart.
  *   free_pages   num_free >= 0 page numbers (may be NULL when 0).  free_head
- *                and free_head_out are single integers on the device and
- *                must not be the same address; taking the call again with
- *                the same free_head gives the same maps.
+ *                and free_head_out are single integers on the device; taking
+ *                the call again with the same free_head gives the same maps.
+ *   No buffer that the call writes (starts, kv_lens, positions, slots,
+ *   free_head_out, the rows of block_table) may overlap another one of the
+ *   call: the lengths are read while the maps are written, so a step cannot
+ *   advance them in place (kv_lens is not `cached`, free_head_out not
+ *   free_head).  Overlaps are refused.
  * Out of range on the device, each reported: a negative length counts as 0;
  * cached and added tokens past max_pages * page_size are cut off (the
  * request then has fewer new tokens); a page that the free list does not
@@ -280,6 +284,14 @@ int attn_f16_paged_maps_validate(int batch, const int32_t *cached, const int32_t
                                  const int32_t *starts, const int32_t *kv_lens,
                                  const int32_t *positions, const int32_t *slots,
                                  const int32_t *free_head_out);
+/* Whether buffers of a maps call (arguments that passed the check above)
+ * overlap where they must not: GEMM_F16_OK or GEMM_F16_ERR_INVALID_ARG. */
+int attn_f16_paged_maps_overlap(int batch, const int32_t *cached, const int32_t *added,
+                                const int32_t *block_table, int64_t table_stride, int max_pages,
+                                const int32_t *free_pages, int num_free,
+                                const int32_t *free_head, int max_tokens, const int32_t *starts,
+                                const int32_t *kv_lens, const int32_t *positions,
+                                const int32_t *slots, const int32_t *free_head_out);
 int attn_f16_rope_validate(int tokens, int q_heads, int kv_heads, int head_dim, int rot_dim,
                            int layout, float factor, const uint64_t *turns,
                            const int32_t *positions, const void *Q, const int64_t q_strides[2],
