@@ -428,7 +428,7 @@ def matmul(plan: Plan, A, B, C=None, split_k: int = 1, stream=None):
 
     A and B may each be row-major or the transpose of a row-major tensor
     (``X.t()``); the matching operand layout is passed to the kernel, so no
-    copy is made.  C must be row-major.
+    copy is made.  C must be row-major.  Forward only: C carries no gradient.
     """
     import torch
     if A.dtype != torch.float16 or B.dtype != torch.float16:
@@ -453,7 +453,8 @@ def attention(plan: Plan, Q, K, V, O=None, scale=None, stream=None):
     """softmax(scale * Q K^T) V for float16 CUDA tensors of shape
     [batch, heads, seq, 256] (the last dimension contiguous; other strides
     free, so ``x.transpose(1, 2)`` of a [batch, seq, heads, 256] tensor works).
-    ``scale`` defaults to 1/sqrt(256).  O is allocated if None."""
+    ``scale`` defaults to 1/sqrt(256).  O is allocated if None.  Forward only:
+    O carries no gradient."""
     import torch
     for name, X in (("Q", Q), ("K", K), ("V", V)):
         if X.dtype != torch.float16 or X.dim() != 4 or X.stride(3) != 1:
@@ -699,6 +700,41 @@ def _rope_layout(layout: str) -> int:
     raise ValueError("layout is 'half' or 'interleaved'")
 
 
+_Rotary = None
+
+
+def _rotary_function():
+    """rotary as an autograd function (made on first use: torch is not loaded
+    with this module).  Its backward pass is the rotation back, by this
+    function again, so that gradients of gradients exist too."""
+    global _Rotary
+    if _Rotary is None:
+        import torch
+
+        class Rotary(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, X, positions, turns, plan, layout, factor, inverse):
+                ctx.save_for_backward(positions, turns)
+                ctx.call = plan, layout, factor, inverse
+                return rotary(plan, X, positions, turns, layout=layout, factor=factor,
+                              inverse=inverse)
+
+            @staticmethod
+            def backward(ctx, dY):
+                positions, turns = ctx.saved_tensors
+                plan, layout, factor, inverse = ctx.call
+                # A gradient may be laid out in ways that X may not (one number for
+                # all of it, say).
+                dY = dY.contiguous()
+                if dY.data_ptr() % 16:
+                    dY = dY.clone()
+                return (rotary(plan, dY, positions, turns, layout=layout, factor=factor,
+                               inverse=not inverse), None, None, None, None, None, None)
+
+        _Rotary = Rotary
+    return _Rotary
+
+
 def rotary(plan: Plan, X, positions, turns, out=None, layout: str = "half", factor: float = 1.0,
            inverse: bool = False, stream=None):
     """Rotary positions of X, float16 [tokens, heads, 256] (tokens and heads
@@ -707,8 +743,24 @@ def rotary(plan: Plan, X, positions, turns, out=None, layout: str = "half", fact
     layout "interleaved", (2i, 2i + 1), and multiplied by ``factor``; the rest
     is copied.  turns: int64, from rope_turns, on the device.  ``inverse``
     rotates back: given the gradient of the output it returns the gradient
-    of X.  ``out`` may be X.
+    of X.  ``out`` may be X.  Where X requires a gradient the result carries
+    it (``out`` cannot be given then); ``plan`` must last until the backward
+    pass.
     """
+    if getattr(X, "requires_grad", False):
+        import torch
+        if torch.is_grad_enabled():
+            if out is not None:
+                raise ValueError("out cannot be given where X requires a gradient")
+            call = (X, positions, turns, plan, layout, factor, inverse)
+            if stream is None:
+                return _rotary_function().apply(*call)
+            # The backward pass runs on the stream that is current here.
+            handle = _stream_handle(stream)
+            on = (torch.cuda.ExternalStream(handle, device=plan.device) if handle
+                  else torch.cuda.default_stream(plan.device))
+            with torch.cuda.stream(on):
+                return _rotary_function().apply(*call)
     return _result(
         (_calls or _torch_calls()).rotary(
             plan.handle, plan.device, X, positions, turns, out, _rope_layout(layout), factor,
@@ -725,6 +777,7 @@ def rotary_to_cache(plan: Plan, Q, K, V, positions, slots, turns, K_cache, V_cac
     [pages, page_size, kv_heads, 256], any strides with the last dimension
     contiguous.  positions, slots: int32 [tokens], from paged_maps (slot -1:
     nothing is written).  Returns the rotated Q (in ``out``, which may be Q).
+    Forward only: neither it nor the caches carry a gradient.
     """
     return _result(
         (_calls or _torch_calls()).rotary_to_cache(
@@ -747,7 +800,7 @@ def paged_attention(plan: Plan, Q, K_cache, V_cache, block_table, starts, kv_len
     is fine).  A token at position p sees the keys at j <= p; with ``window``
     only j > p - window and the first ``sinks`` of its request.  ``scale``
     defaults to 1/sqrt(256).  Rows that see no key, and rows past the last
-    request's, are 0.
+    request's, are 0.  Forward only: the result carries no gradient.
     """
     return _result(
         (_calls or _torch_calls()).paged_attention(
