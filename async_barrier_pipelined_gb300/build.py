@@ -3,17 +3,23 @@
 Output: async_barrier_pipelined_gb300/_lib/libgemm_f16.so (git-ignored).
 Five translation units (plan and shared host code; the kernels and entry
 points of the GEMM, the attention, the paged-cache maps with rotary
-positions, and the attention over a paged cache) are compiled in parallel with one -gencode each and linked into one library, so a build
-takes seconds on either the x86 build host or the aarch64 GPU host.
+positions, and the attention over a paged cache) are compiled in parallel
+with one -gencode each and linked into one library, so a build takes seconds
+on either the x86 build host or the aarch64 GPU host.
 
 Beside it, _lib/paged_torch_calls.so: the paged-cache calls for torch tensors
-(csrc/torch_calls.cpp, host code only, compiled against the installed torch).
+(csrc/torch_calls.cpp, host code only, compiled against the installed torch,
+and again when another torch or Python is installed).  Without torch the
+library alone is built: its C ABI needs none.
 """
 from __future__ import annotations
 
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -35,6 +41,7 @@ DEPENDS = SOURCES + HEADERS + [os.path.join(INCLUDE, "gemm_f16.h"),
 CALLS_NAME = "paged_torch_calls"
 CALLS_PATH = os.path.join(LIB_DIR, CALLS_NAME + ".so")
 CALLS_SOURCE = os.path.join(CSRC, "torch_calls.cpp")
+CALLS_STAMP = os.path.join(LIB_DIR, CALLS_NAME + ".for")   # the torch that they were built for
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -62,6 +69,30 @@ def _fresh(path: str, depends: list[str]) -> bool:
                                         for f in depends)
 
 
+def _torch_stamp() -> str | None:
+    """What the torch calls are compiled against (found without importing
+    torch), or None where torch is not installed."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return None
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        version = "?"
+    return f"torch {version} at {spec.origin}, Python {sys.version}\n"
+
+
+def _calls_fresh(stamp: str) -> bool:
+    if not _fresh(CALLS_PATH, [CALLS_SOURCE, os.path.join(INCLUDE, "attn_f16.h"),
+                               os.path.join(INCLUDE, "gemm_f16.h")]):
+        return False
+    try:
+        with open(CALLS_STAMP) as f:
+            return f.read() == stamp
+    except OSError:
+        return False
+
+
 def _calls_cmd(obj: str) -> list[str]:
     from torch.utils import cpp_extension as ext
     cuda = os.path.dirname(os.path.dirname(nvcc_path()))
@@ -86,8 +117,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(LIB_DIR, exist_ok=True)
     calls = None
     calls_obj = os.path.join(LIB_DIR, f"{CALLS_NAME}.tmp{os.getpid()}.o")
-    if force or not _fresh(CALLS_PATH, [CALLS_SOURCE, os.path.join(INCLUDE, "attn_f16.h"),
-                                        os.path.join(INCLUDE, "gemm_f16.h")]):
+    stamp = _torch_stamp()
+    if stamp is not None and (force or not _calls_fresh(stamp)):
         calls = subprocess.Popen(_calls_cmd(calls_obj))     # beside the library's units
     try:
         _build_library(force, verbose)
@@ -97,6 +128,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
             tmp = CALLS_PATH + f".tmp{os.getpid()}"
             _link_calls(calls_obj, tmp)
             os.replace(tmp, CALLS_PATH)
+            with open(CALLS_STAMP + f".tmp{os.getpid()}", "w") as f:
+                f.write(stamp)
+            os.replace(f.name, CALLS_STAMP)
     finally:
         if calls is not None:
             if calls.poll() is None:
