@@ -30,7 +30,7 @@ __all__ = [
     "gemm_f16_tile_order", "gemm_f16_tile_shape", "Plan", "matmul",
     "OK", "ERR_INVALID_ARG", "ERR_MISALIGNED", "ERR_UNSUPPORTED_DEVICE",
     "ERR_OOM", "ERR_CUDA", "ERR_TIMEOUT", "ERR_SCRATCH_TOO_SMALL", "gemm_f16_run_noalloc", "gemm_f16_noalloc_status",
-    "OPT_TIMEOUT_NS", "OPT_TILE_ORDER", "OPT_FAULT_UNIT", "OPT_KERNEL", "OPT_TILE_WIDTH", "OPT_SM_LIMIT", "OPT_ATTN_KERNEL", "OPT_ATTN_SPLIT", "OPT_A_REPACK", "OPT_KERNEL_TIMING", "INFO_NUM_SMS", "INFO_MAX_PAIRS", "INFO_MAX_QUADS",
+    "OPT_TIMEOUT_NS", "OPT_TILE_ORDER", "OPT_FAULT_UNIT", "OPT_KERNEL", "OPT_TILE_WIDTH", "OPT_SM_LIMIT", "OPT_ATTN_KERNEL", "OPT_ATTN_SPLIT", "OPT_A_REPACK", "OPT_MULTICAST", "OPT_KERNEL_TIMING", "INFO_NUM_SMS", "INFO_MAX_PAIRS", "INFO_MAX_QUADS",
     "gemm_f16_get_option", "gemm_f16_pair_tiles", "EXPORTED_SYMBOLS",
     "gemm_f16_run_ex", "gemm_f16_validate_ex", "attn_f16_fwd", "attn_f16_validate",
     "attn_f16_key_ranges", "gemm_f16_run_info", "gemm_f16_run_choice", "attn_f16_fwd_host", "attention_host",
@@ -63,6 +63,7 @@ OPT_ATTN_KERNEL = 7
 OPT_ATTN_SPLIT = 8
 OPT_A_REPACK = 9
 OPT_KERNEL_TIMING = 10
+OPT_MULTICAST = 11
 INFO_NUM_SMS = 100
 INFO_MAX_PAIRS = 101
 INFO_MAX_QUADS = 102
@@ -374,6 +375,9 @@ class Plan:
     def __init__(self, device: int = 0):
         self.device = device
         self.handle = gemm_f16_plan(device)
+        if int(os.environ.get("WORLD_SIZE") or 1) > 1:
+            # One of several processes, each with its GPU: no multicast copies.
+            self.set_option(OPT_MULTICAST, 0)
 
     def close(self):
         if self.handle:

@@ -1007,7 +1007,7 @@ RunChoice choose_run(const gemm_f16_plan_s* p, int layout, int M, int N, int K, 
   const int64_t a_elems = (int64_t)M * K;
   const bool a_off_lines = (lda * 2) % 128 != 0;
   const bool large = N >= 2048 && a_elems >= ((int64_t)1 << 22);
-  const bool quad_fits = c.use_pair && layout == 0 && p->max_quads > 0 &&
+  const bool quad_fits = c.use_pair && layout == 0 && p->max_quads > 0 && p->multicast &&
                          ceil_div(N, quad::QN) <= 0xFFFF && ceil_div(M, pair::PM) <= 0xFFFF;
   const int64_t quad_waves =
       ceil_div(ceil_div(M, pair::PM) * ceil_div(N, quad::QN) * (int64_t)split_k,

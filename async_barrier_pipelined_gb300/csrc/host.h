@@ -108,6 +108,7 @@ struct gemm_f16_plan_s {
   int a_repack = 0;    // repack A with a pitch off 128-byte lines: 0 auto, 1 never, 2 always
   int max_pairs = 0;   // co-resident clusters of two for the pair kernel
   int max_quads = 0;   // co-resident clusters of four for the cluster-of-four kernel
+  int multicast = 1;   // whether that kernel, whose copies are multicast, may run
   int paged_pairs = 0; // co-resident clusters of two for the paged attention kernel
   int attn_pairs = 0;  // co-resident clusters of two for the pair attention kernel
   void* ws = nullptr;

@@ -306,6 +306,10 @@ int gemm_f16_set_option(gemm_f16_plan_t p, int option, int64_t value) {
       if (value == 3 && p->max_quads <= 0) return GEMM_F16_ERR_UNSUPPORTED_DEVICE;
       p->kernel = (int)value;
       return GEMM_F16_OK;
+    case GEMM_F16_OPT_MULTICAST:
+      if (value != 0 && value != 1) return GEMM_F16_ERR_INVALID_ARG;
+      p->multicast = (int)value;
+      return GEMM_F16_OK;
     default:
       return GEMM_F16_ERR_INVALID_ARG;
   }
@@ -324,6 +328,7 @@ int gemm_f16_get_option(gemm_f16_plan_t p, int option, int64_t* value) {
     case GEMM_F16_OPT_ATTN_SPLIT: *value = p->attn_split; return GEMM_F16_OK;
     case GEMM_F16_OPT_A_REPACK: *value = p->a_repack; return GEMM_F16_OK;
     case GEMM_F16_OPT_KERNEL_TIMING: *value = p->kernel_timing; return GEMM_F16_OK;
+    case GEMM_F16_OPT_MULTICAST: *value = p->multicast; return GEMM_F16_OK;
     case GEMM_F16_INFO_NUM_SMS: *value = p->num_sms; return GEMM_F16_OK;
     case GEMM_F16_INFO_MAX_PAIRS: *value = p->max_pairs; return GEMM_F16_OK;
     case GEMM_F16_INFO_MAX_QUADS: *value = p->max_quads; return GEMM_F16_OK;

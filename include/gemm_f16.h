@@ -163,7 +163,15 @@ typedef enum gemm_f16_option {
      * into a graph, or once 65536 pairs are waiting to be read.  Events come
      * from a plan-owned pool that grows on demand (cudaEventCreate) and is
      * freed with the plan. */
-    GEMM_F16_OPT_KERNEL_TIMING = 10
+    GEMM_F16_OPT_KERNEL_TIMING = 10,
+    /* Whether the cluster-of-four kernel may run: 1 = yes (default), 0 = no,
+     * the CTA-pair kernel runs in its place, also where GEMM_F16_OPT_KERNEL
+     * is 3.  Its operand copies are multicast within a cluster, which is for
+     * programs that use one GPU: one that uses several (a process per GPU,
+     * or plans on several devices) sets this to 0 on every plan.  The Python
+     * Plan does so where WORLD_SIZE, as a launcher of several processes sets
+     * it, is above 1. */
+    GEMM_F16_OPT_MULTICAST = 11
 } gemm_f16_option;
 
 /*
