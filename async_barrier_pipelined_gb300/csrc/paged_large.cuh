@@ -284,19 +284,17 @@ __device__ __forceinline__ void deal_tiles(const Params& p, const int4* req, Dea
     const int dealt = __reduce_add_sync(0xffffffffu, sum), rest = total - dealt;
     least = __reduce_min_sync(0xffffffffu, least);
     most = __reduce_max_sync(0xffffffffu, most);
-    int lo = least, hi = deal_level_enough(most, rest, workers);
-    auto shares = [&](int level) {
+    auto shares = [&](int level) {           // of the lane's workers
       int n = 0;
 #pragma unroll
       for (int k = 0; k < EACH; ++k)
         if (lane * EACH + k < workers) n += deal_share(level, load[k]);
       return n;
     };
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (__reduce_add_sync(0xffffffffu, shares(mid)) < rest) lo = mid; else hi = mid;
-    }
-    sum = shares(hi);
+    const int level = deal_level(least, most, rest, workers, [&](int at_level) {
+      return __reduce_add_sync(0xffffffffu, shares(at_level));
+    });
+    sum = shares(level);
     int at = sum;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -309,7 +307,7 @@ __device__ __forceinline__ void deal_tiles(const Params& p, const int4* req, Dea
       const int c = lane * EACH + k;
       if (c < workers) {
         deal->start[c] = dealt + deal_start(at, rest, workers, c);
-        at += deal_share(hi, load[k]);
+        at += deal_share(level, load[k]);
       }
     }
     if (lane == 0) deal->start[workers] = total;

@@ -201,6 +201,20 @@ GF16_HD int deal_share(int level, int load) { return imax(1, level - load); }
 GF16_HD int deal_level_enough(int most_load, int rest, int workers) {
   return most_load + (rest + workers - 1) / workers;
 }
+// The lowest level above the `least` load at which the shares of all workers,
+// shares(level), are enough for the rest.
+#ifdef __CUDACC__
+#pragma nv_exec_check_disable
+#endif
+template <typename Shares>
+GF16_HD int deal_level(int least, int most, int rest, int workers, const Shares& shares) {
+  int lo = least, hi = deal_level_enough(most, rest, workers);
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (shares(mid) < rest) lo = mid; else hi = mid;
+  }
+  return hi;
+}
 GF16_HD int deal_start(int before, int rest, int workers, int c) {
   return imin(before, rest - (workers - c));
 }

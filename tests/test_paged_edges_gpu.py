@@ -62,3 +62,67 @@ def test_maps_are_not_advanced_in_place(g, plan):
     torch.cuda.synchronize()
     assert plan.status() == 0
     assert all(torch.equal(a, b) for a, b in zip((*m, table), kept))
+
+
+def step_calls(g, plan):
+    """name -> call(stream, out), of each paged-cache call on the same inputs."""
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    rand = lambda *s: torch.randn(s, generator=gen, device="cuda").half()
+    cached, added = i32([30, 0, 7]), i32([1, 90, 2])
+    free = torch.arange(20, dtype=torch.int32, device="cuda").flip(0).contiguous()
+    start = g.paged_maps(plan, i32([0, 0, 0]), cached, i32([[-1] * 8] * 3), free, i32([0]), 16, 40)
+    table = i32([[-1] * 8] * 3)
+    g.paged_maps(plan, i32([0, 0, 0]), cached, table, free, i32([0]), 16, 40)
+    m = g.paged_maps(plan, cached, added, table, free, start.free_head, 16, 100)
+    kc, vc = rand(20, 16, 2, D), rand(20, 16, 2, D)
+    q, k, v = rand(100, 8, D), rand(100, 2, D), rand(100, 2, D)
+    turns = g.rope_turns(g.rope_frequencies(128)).cuda()
+    own = kc.clone(), vc.clone()
+    return {
+        "maps": lambda stream, out: g.paged_maps(plan, cached, added, table, free,
+                                                 start.free_head, 16, 100, out=out, stream=stream),
+        "rotary": lambda stream, out: g.rotary(plan, q, m.positions, turns, out=out, stream=stream),
+        "to cache": lambda stream, out: g.rotary_to_cache(plan, q, k, v, m.positions, m.slots,
+                                                          turns, *own, out=out, stream=stream),
+        "attention": lambda stream, out: g.paged_attention(plan, q, kc, vc, table, m.starts,
+                                                           m.kv_lens, 90, out=out, stream=stream),
+    }
+
+
+@pytest.mark.parametrize("name", ["maps", "rotary", "to cache", "attention"])
+def test_given_outputs_are_written(g, plan, name):
+    """Into the tensors given, every number of them (they hold something else before)."""
+    import torch
+    call = step_calls(g, plan)[name]
+    want = call(None, None)
+    if name == "maps":
+        out = type(want)(*[torch.full_like(x, -77) for x in want])
+        got = call(None, out)
+        assert all(a.data_ptr() == b.data_ptr() for a, b in zip(got, out))
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+    else:
+        out = torch.full_like(want, float("nan"))
+        got = call(None, out)
+        assert got.data_ptr() == out.data_ptr()
+        assert torch.equal(out, want)
+    torch.cuda.synchronize()
+    assert plan.status() == 0
+
+
+@pytest.mark.parametrize("name", ["maps", "rotary", "to cache", "attention"])
+def test_given_streams_are_ordered(g, plan, name):
+    """On another stream, given as an object or a handle: behind what that
+    stream was told to wait for, with the tensors made here."""
+    import torch
+    call = step_calls(g, plan)[name]
+    want = call(None, None)
+    flat = lambda r: list(r) if name == "maps" else [r]
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        side.wait_stream(torch.cuda.current_stream())
+        got = call(stream, None)
+        torch.cuda.current_stream().wait_stream(side)
+        assert all(torch.equal(a, b) for a, b in zip(flat(got), flat(want)))
+    torch.cuda.synchronize()
+    assert plan.status() == 0
