@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstdio>
 
@@ -278,9 +279,11 @@ int attn_f16_paged_fwd(gemm_f16_plan_t p, int batch, int total_q, int max_q, int
   prm.O = static_cast<__half*>(O);
   prm.o_tok = o_strides[0];
   prm.o_head = o_strides[1];
-  // In base 2.  A scale of 0 becomes one whose products with any binary16
-  // scores vanish beside 1, so that a masked score may be an infinity.
-  prm.scale_log2 = scale == 0.f ? 1e-30f : scale * 1.4426950408889634f;
+  // In base 2, and finite: an infinity would make a score of 0 a NaN.  A scale
+  // of 0 becomes one whose products with any binary16 scores vanish beside 1,
+  // so that a masked score may be an infinity.
+  prm.scale_log2 = scale == 0.f ? 1e-30f
+                                : std::clamp(scale * 1.4426950408889634f, -FLT_MAX, FLT_MAX);
   prm.masks.window = window;
   prm.masks.sinks = sinks;
   prm.status = p->status_dev;

@@ -126,3 +126,25 @@ def test_given_streams_are_ordered(g, plan, name):
         assert all(torch.equal(a, b) for a, b in zip(flat(got), flat(want)))
     torch.cuda.synchronize()
     assert plan.status() == 0
+
+
+@pytest.mark.parametrize("scale", [3e38, -3e38, 1e-44])
+@pytest.mark.parametrize("new", [1, 90], ids=["few", "many"])
+def test_scales_at_the_ends_of_their_range(g, plan, new, scale):
+    """All scores 0: O is the mean of the values seen, whatever the scale (times
+    log2 e the largest ones do not fit FP32).  Half a binary16 step of O, and
+    FP32 sums of n numbers (2^-24 each of their magnitudes)."""
+    import torch
+    n = 200 + new
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    kc, vc = (torch.randn(16, 32, 1, D, generator=gen, device="cuda").half() for _ in range(2))
+    q = torch.zeros(new, 2, D, dtype=torch.float16, device="cuda")
+    table = torch.arange(16, dtype=torch.int32, device="cuda")[None]
+    o = g.paged_attention(plan, q, kc, vc, table, i32([0, new]), i32([n]), new, scale=scale)
+    torch.cuda.synchronize()
+    assert plan.status() == 0
+    seen = torch.arange(n - new + 1, n + 1, device="cuda").double()[:, None]
+    v = vc.view(-1, D)[:n].double()
+    mean, mag = (x.cumsum(0)[n - new:] / seen for x in (v, v.abs()))
+    bound = 2.0 ** -11 * mean.abs() + 2.0 ** -25 + 2 * n * 2.0 ** -24 * mag
+    assert ((o.double() - mean[:, None]).abs() <= bound[:, None]).all()
