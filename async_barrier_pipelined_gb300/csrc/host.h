@@ -114,7 +114,6 @@ struct gemm_f16_plan_s {
   void* ws = nullptr;
   size_t ws_bytes = 0;
   void* paged_ws = nullptr;  // attention over a paged cache: partial sums of cut tiles
-  size_t paged_ws_bytes = 0;
   void* apack = nullptr;  // repacked copy of A (see pack_rows_kernel)
   size_t apack_bytes = 0;
   // FP32 values of the K halves of the pair kernel's last-wave tiles.

@@ -73,18 +73,25 @@ constexpr int HEAD_DIM = 256;
 
 // Workspace of the attention over a paged cache: the cut tiles, the partials'
 // offsets and sums, and their FP32 O; of the two kernels' needs the larger.
-// Its size depends on the device alone.
+// Its size depends on the device alone: allocated by the plan's first call and
+// kept.  Not on the call's stream: an allocation that the stream records while
+// it is captured into a graph belongs to the graph's replays, and a call outside
+// them would use memory that is not there.
 constexpr int SMALL_ROWS = 64;   // most rows of a request for the small kernel
 
-int ensure_workspace(gemm_f16_plan_s* p, cudaStream_t stream, paged::Params* prm) {
+int ensure_workspace(gemm_f16_plan_s* p, paged::Params* prm) {
   const size_t small_slots = 2 * (size_t)p->num_sms, large_slots = 2 * (size_t)p->paged_pairs;
   const size_t rows = std::max(small_slots * SMALL_ROWS, large_slots * paged::large::PART_ROWS);
   const size_t cut = (size_t)p->num_sms * sizeof(paged::CutTile);
   const size_t ml = rows * sizeof(float2);
-  const int rc = ensure_buffer(&p->paged_ws, &p->paged_ws_bytes,
-                               cut + ml + rows * HEAD_DIM * sizeof(float), stream,
-                               "paged attention workspace allocation");
-  if (rc) return rc;
+  if (!p->paged_ws) {
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;   // this thread may be capturing
+    GF16_CUDA(cudaThreadExchangeStreamCaptureMode(&mode), "cudaThreadExchangeStreamCaptureMode");
+    const cudaError_t e = cudaMalloc(&p->paged_ws, cut + ml + rows * HEAD_DIM * sizeof(float));
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    if (e != cudaSuccess) p->paged_ws = nullptr;
+    GF16_CUDA(e, "paged attention workspace allocation");
+  }
   char* ws = static_cast<char*>(p->paged_ws);
   prm->cut = reinterpret_cast<paged::CutTile*>(ws);
   prm->part_ml = reinterpret_cast<float2*>(ws + cut);
@@ -289,7 +296,7 @@ int attn_f16_paged_fwd(gemm_f16_plan_t p, int batch, int total_q, int max_q, int
   prm.status = p->status_dev;
   prm.timeout_ns = p->timeout_ns;
   prm.fault_unit = p->fault_unit;
-  if ((rc = ensure_workspace(p, st, &prm))) return rc;
+  if ((rc = ensure_workspace(p, &prm))) return rc;
   CUtensorMap tmQ, tmK, tmV;
   const int page_rows = page_size & -page_size;   // the largest power of two in it
   const int64_t rows = std::max<int64_t>(1, max_q) * prm.group;   // room for a token at least

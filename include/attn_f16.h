@@ -130,9 +130,10 @@ int attn_f16_validate(int batch, int heads, int seq_q, int seq_kv, int head_dim,
  * described with each call.  Other requests are not affected.
  *
  * Every call below is asynchronous on `stream` and can be captured into a
- * CUDA graph (attn_f16_paged_fwd after one eager call on the plan, which
- * allocates its workspace: partial sums of tiles of queries that are cut
- * between workers, about 40 MB on a GB300 whatever the step).  The maps and
+ * CUDA graph, as the plan's first call too (the plan must outlive the graph's
+ * replays).  The first attn_f16_paged_fwd of a plan allocates its workspace:
+ * partial sums of tiles of queries that are cut between workers, about 40 MB
+ * on a GB300 whatever the step.  The maps and
  * the rotation are one kernel launch each, the attention two (its kernel and
  * the merge of cut tiles) or, where some requests may have many new tokens and
  * others few, four.  GEMM_F16_OPT_SM_LIMIT bounds the attention's kernels,

@@ -148,3 +148,38 @@ def test_scales_at_the_ends_of_their_range(g, plan, new, scale):
     mean, mag = (x.cumsum(0)[n - new:] / seen for x in (v, v.abs()))
     bound = 2.0 ** -11 * mean.abs() + 2.0 ** -25 + 2 * n * 2.0 ** -24 * mag
     assert ((o.double() - mean[:, None]).abs() <= bound[:, None]).all()
+
+
+@pytest.mark.parametrize("replay_first", [True, False])
+@pytest.mark.parametrize("name", ["few", "many", "both"])
+def test_a_plan_whose_first_call_is_captured(g, plan, name, replay_first):
+    """Its workspace (all these steps cut tiles) serves the graph's replays and
+    calls outside them, in either order."""
+    import torch
+    lens = {"few": [(3000, 1)], "many": [(900, 700)], "both": [(2000, 1), (500, 300)]}[name]
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    kc, vc = (torch.randn(300, 16, 2, D, generator=gen, device="cuda").half() for _ in range(2))
+    total = sum(n for _, n in lens)
+    q = torch.randn(total, 4, D, generator=gen, device="cuda").half()
+    table = torch.arange(300, dtype=torch.int32, device="cuda").view(1, 300).repeat(len(lens), 1)
+    starts = i32([0] + [sum(n for _, n in lens[:b + 1]) for b in range(len(lens))])
+    kv_lens, most = i32([c + n for c, n in lens]), max(n for _, n in lens)
+    call = lambda p, out: g.paged_attention(p, q, kc, vc, table, starts, kv_lens, most, out=out)
+    want = call(plan, None)
+    torch.cuda.synchronize()
+    with g.Plan(0) as fresh:
+        out = torch.full_like(q, float("nan"))
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call(fresh, out)
+        for replay in (replay_first, not replay_first, replay_first):
+            if replay:
+                out.fill_(float("nan"))
+                graph.replay()
+                got = out
+            else:
+                got = call(fresh, None)
+            torch.cuda.synchronize()
+            assert fresh.status() == 0
+            assert torch.equal(got, want)
+        del graph
