@@ -109,11 +109,12 @@ static_assert(sizeof(Sched) <= 64, "room for the schedule");
 // blocks of the last one to two rounds of tiles make up for the differences.
 // With equal shares a cluster takes neighbouring tiles one after another, and
 // the head's keys have left L2 from one to the next.  Measured, equal shares ->
-// whole tiles: a mixed step of 50 requests 418 -> 374 us, four prompts of 4000
-// tokens 384 -> 357.  Short tiles stay with equal shares (their keys have not
-// left L2, and the prologue is longer): 32 prompts of 200 (1.5 blocks a tile) 68
-// -> 74, eight of 2000 (8.5) 234 -> 231, one of 4001 with a window (10) 86 -> 90;
-// and so do fewer tiles than two for each cluster.
+// whole tiles, in us (floor): a mixed step of 50 requests 418 -> 374 (160), four
+// prompts of 4000 tokens 384 -> 357 (269).  Short tiles stay with equal shares
+// (their keys have not left L2, and the prologue is longer): 32 prompts of 200
+// (1.5 blocks a tile) 68 -> 74 (19), eight of 2000 (8.5) 234 -> 231 (134), one of
+// 4001 with a window (10) 86 -> 90 (35); and so do fewer tiles than two for each
+// cluster.
 struct Deal {
   int start[MAX_CLUSTERS + 1];   // where each cluster's share of the rest begins
   int load[MAX_CLUSTERS];        // blocks of its whole tiles
@@ -483,9 +484,6 @@ __device__ __forceinline__ void signal_leader(uint32_t rank, uint32_t lane, uint
   }
 }
 
-// 3-D tensor load crediting a barrier that may live in the peer CTA: in
-// ptx.cuh (tma_load_3d_pair), as the 4-D one.
-
 // Copies that a CTA has issued: key tiles, value tiles, Q tiles.
 struct Issued {
   uint32_t keys, values, queries;
@@ -500,7 +498,8 @@ __device__ __forceinline__ uint32_t blocks_note(int blocks, bool more) {
 // ------------------------------------------------------------------ copies
 // Keys and values each have a warp and a ring of their own: with pages of 16
 // rows a tile is 16 copies of 2 KB and one warp that issues both kinds falls
-// behind the MMAs (4096 tokens over 8192 in pages of 16: see paged_attn.cu).
+// behind the MMAs (4096 tokens over 8192 in pages of 16, when this was split:
+// 598 us with one warp, 518 with two).
 // Both CTAs fill their halves, crediting the leader's barriers; the leader
 // also arrives (expect_tx) for the pair.
 template <bool KEYS>

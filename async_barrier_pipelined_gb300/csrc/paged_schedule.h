@@ -126,7 +126,7 @@ GF16_HD uint32_t bits(int a, int b) {
 }
 
 // Which rows of block `blk` hold keys that the query at position p (of the
-// tile of span s) sees, as 128 bits.
+// tile of span s) sees, as 128 bits (right for groups of up to 128 rows).
 GF16_HD void seen_words(const Span& s, int blk, int rows, int p, const Masks& m,
                         uint32_t (&see)[4]) {
   // Keys of the query's window and its sinks as rows lo .. hi - 1 and 0 .. sk - 1
@@ -154,7 +154,7 @@ GF16_HD void seen_words(const Span& s, int blk, int rows, int p, const Masks& m,
   const int shift = rows - over;
   uint64_t late0 = ((uint64_t)(see[1] & bits(gs - 32, BLOCK_KEYS)) << 32) | (see[0] & bits(gs, BLOCK_KEYS));
   uint64_t late1 = ((uint64_t)(see[3] & bits(gs - 96, BLOCK_KEYS)) << 32) | (see[2] & bits(gs - 64, BLOCK_KEYS));
-  if (shift >= 64) {
+  if (shift >= 64) {            // only with rows of 128: the chunk kernel's are at most 64
     late1 = late0 << (shift - 64);
     late0 = 0;
   } else {                      // shift >= 1

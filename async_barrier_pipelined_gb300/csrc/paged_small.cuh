@@ -30,8 +30,8 @@
 // the end of the kernel, where one CTA reads what all the others wrote; the
 // second launch takes 3 and spreads the rows over the GPU.)
 //
-// Barriers: q_full / q_empty, full[s] / empty[s] (ring of 32 KB: half a key
-// block by 128 numbers, then half a value block by 128 numbers), s_full[2],
+// Barriers: q_full / q_empty, full[s] / empty[s] (ring of 32 KB slots, 128 keys
+// by 128 numbers each: a block's keys take two, then its values two), s_full[2],
 // p_full[2], o_done[2] (the O products of a block).  Every wait is bounded;
 // after an abort the roles stop issuing and the copies in flight are waited for.
 #pragma once

@@ -8,7 +8,9 @@
  *     O[b,h,i,:] = sum_j softmax_j(scale * Q[b,h,i,:] . K[b,h,j,:]) * V[b,h,j,:]
  *
  * with binary16 Q, K, V, O, FP32 scores, softmax statistics and
- * accumulation, and O rounded to binary16 (round to nearest even).  This is
+ * accumulation, softmax weights rounded to binary16 for the product with V
+ * (the sum is of the FP32 weights; one below 2^-25 of the row's largest may be 0
+ * in the product), and O rounded to binary16 (round to nearest even).  This is
  * the flash-attention ("SDP") kernel of the "Xe2 Nbarrier Pipelining" page,
  * section "Proven Pattern: SDP Kernel Split Barrier B" (head dimension 256):
  * per block of 64 keys, S = Q K^T, a softmax with a running row maximum,
@@ -248,11 +250,13 @@ int attn_f16_rope_turns(const double *radians, int n, uint64_t *turns);
  * softmax weights are rounded to binary16 for the product with V (not for their
  * sum): each is off by at most 2^-11 of itself, or 2^-32 of the row's largest.
  * A row that sees no key (kv_lens[b] < n), or only keys whose scores are -inf,
- * is 0, and so are the rows from starts[batch] to total_q - 1.  Rows of a page that no position of the
- * request has reached, pages past it, and pages that no query of it sees
- * may hold anything (NaN included) and their table entries are not used;
- * an infinity or NaN in a V row that some queries of the request see and
- * others do not may reach both.
+ * is 0, and so are the rows from starts[batch] to total_q - 1; rows before
+ * starts[0] are not written.  Rows of a page that no position of the request
+ * has reached, pages past it, and pages that no query of it sees may hold
+ * anything (NaN included) and their table entries are not used.  On a page
+ * that some query of the request sees, an infinity or NaN in a V row at a
+ * position that the request has reached may reach all of the request's rows,
+ * whether they see that key or not (a weight of 0 times infinity).
  *   batch        1 .. 65535.   total_q >= 0: rows of Q and O (0: nothing is
  *                enqueued).   max_q >= 0: the largest n, or more.
  *   q_heads      a multiple of kv_heads, at most 64 times as many;
