@@ -118,3 +118,17 @@ def test_an_output_cannot_be_given(g, plan):
     with torch.no_grad():
         out = torch.empty_like(dy)
         assert g.rotary(plan, x, pos, turns, out=out) is not None
+
+
+def test_positions_of_a_step(g, plan):
+    """Positions that paged_maps made are kept for the backward pass."""
+    import torch
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    m = g.paged_maps(plan, i32([5, 0]), i32([2, 4]), i32([[0, 1], [2, 3]]), i32([4, 5, 6]),
+                     i32([0]), 16, 6)
+    x, dy, _, _, turns = setup(g, 6, 2, 64, 5)
+    x.requires_grad_()
+    g.rotary(plan, x, m.positions, turns).backward(dy)
+    assert torch.equal(x.grad, g.rotary(plan, dy, i32([5, 6, 0, 1, 2, 3]), turns, inverse=True))
+    torch.cuda.synchronize()
+    assert plan.status() == 0
