@@ -15,6 +15,7 @@ loudly; there is no fallback implementation.
 from __future__ import annotations
 
 import collections
+import contextlib
 import ctypes
 import importlib.util
 import math
@@ -41,6 +42,13 @@ __all__ = [
     "attn_f16_rope_validate", "attn_f16_rope_turns", "attn_f16_paged_fwd",
     "attn_f16_paged_validate", "ROPE_HALF", "ROPE_INTERLEAVED", "PagedMaps", "paged_maps",
     "rope_frequencies", "rope_turns", "rotary", "rotary_to_cache", "paged_attention",
+    "EXPORTED_SYMBOLS_F8", "GemmF8Operand", "F8_E4M3", "F8_E5M2", "F8_DENSE", "F8_BY_ROWS",
+    "F8_BY_INNER", "gemm_f8_quantize", "gemm_f8_quantize_validate", "gemm_f8_run",
+    "gemm_f8_workspace", "gemm_f8_validate", "experts_maps", "experts_maps_validate",
+    "experts_max_rows", "experts_gather", "experts_gather_validate", "experts_combine",
+    "experts_combine_validate", "experts_combine_gradient",
+    "experts_combine_gradient_validate", "Blocks", "quantize", "matmul_f8", "linear_f8",
+    "ExpertMaps", "expert_maps", "expert_gather", "expert_combine",
 ]
 
 OK = 0
@@ -77,6 +85,11 @@ LAYOUT_TT = 3
 
 ROPE_HALF = 0
 ROPE_INTERLEAVED = 1
+
+F8_E4M3, F8_E5M2 = 0, 1
+F8_F16, F8_BF16, F8_F32 = 0, 1, 2
+F8_ROWS, F8_COLUMNS, F8_TILES, F8_BOTH = 0, 1, 2, 3
+F8_DENSE, F8_BY_ROWS, F8_BY_INNER = 0, 1, 2
 
 _c_int, _c_i64, _vp = ctypes.c_int, ctypes.c_int64, ctypes.c_void_p
 
@@ -145,6 +158,43 @@ _SIGNATURES = {
 }
 EXPORTED_SYMBOLS = tuple(_SIGNATURES)
 
+
+class GemmF8Operand(ctypes.Structure):
+    """gemm_f8_operand of gemm_f8.h."""
+    _fields_ = [("data", _vp), ("ld", _c_i64), ("batch", _c_i64), ("scales", _vp),
+                ("s_outer", _c_i64), ("s_inner", _c_i64), ("s_batch", _c_i64),
+                ("format", _c_int), ("transposed", _c_int), ("tiles", _c_int)]
+
+
+_operandp = ctypes.POINTER(GemmF8Operand)
+_F8_QUANTIZE = [_c_int] * 6 + [_vp, _c_i64, _c_i64, _vp, _c_int, _c_int, _vp, _c_i64, _c_i64, _vp,
+                               _vp, _vp]
+_F8_RUN = [_c_int] * 5 + [_vp, _operandp, _operandp, _vp, _c_i64, _c_i64, _c_int, _c_int]
+_EXPERTS_MAPS = [_c_int, _vp, _c_int, _c_int, _c_int, _c_int, _vp, _vp, _vp]
+_EXPERTS_GATHER = [_c_int] * 3 + [_vp, _c_i64, _c_int, _c_int, _vp, _vp, _c_i64]
+_EXPERTS_COMBINE = [_c_int] * 4 + [_vp, _c_i64, _c_int, _vp, _vp, _c_int, _vp, _c_i64]
+_EXPERTS_GRADIENT = [_c_int] * 4 + [_vp, _c_i64, _vp, _c_i64, _c_int, _vp, _vp, _vp, _c_int, _vp,
+                                    _c_i64, _vp]
+
+#: the same for include/gemm_f8.h
+_SIGNATURES_F8 = {
+    "gemm_f8_quantize": (_c_int, [_vp, *_F8_QUANTIZE, _vp]),
+    "gemm_f8_quantize_validate": (_c_int, _F8_QUANTIZE),
+    "gemm_f8_run": (_c_int, [_vp, *_F8_RUN, _vp, ctypes.c_size_t, _vp]),
+    "gemm_f8_workspace": (ctypes.c_size_t, [_vp] + [_c_int] * 6),
+    "gemm_f8_validate": (_c_int, _F8_RUN),
+    "experts_maps": (_c_int, [_vp, *_EXPERTS_MAPS, _vp]),
+    "experts_maps_validate": (_c_int, _EXPERTS_MAPS),
+    "experts_max_rows": (_c_i64, [_c_int] * 3),
+    "experts_gather": (_c_int, [_vp, *_EXPERTS_GATHER, _vp]),
+    "experts_gather_validate": (_c_int, _EXPERTS_GATHER),
+    "experts_combine": (_c_int, [_vp, *_EXPERTS_COMBINE, _vp]),
+    "experts_combine_validate": (_c_int, _EXPERTS_COMBINE),
+    "experts_combine_gradient": (_c_int, [_vp, *_EXPERTS_GRADIENT, _vp]),
+    "experts_combine_gradient_validate": (_c_int, _EXPERTS_GRADIENT),
+}
+EXPORTED_SYMBOLS_F8 = tuple(_SIGNATURES_F8)
+
 _lock = threading.Lock()
 _lib = None
 
@@ -173,7 +223,7 @@ def load() -> ctypes.CDLL:
                     "async_barrier_pipelined_gb300.build.build() first. "
                     "There is no fallback implementation.")
             lib = ctypes.CDLL(LIB_PATH)
-            for name, (res, args) in _SIGNATURES.items():
+            for name, (res, args) in (*_SIGNATURES.items(), *_SIGNATURES_F8.items()):
                 fn = getattr(lib, name)
                 fn.restype = res
                 fn.argtypes = args
@@ -811,3 +861,340 @@ def paged_attention(plan: Plan, Q, K_cache, V_cache, block_table, starts, kv_len
             plan.handle, plan.device, Q, K_cache, V_cache, block_table, starts, kv_lens, max_q, out,
             ATTN_HEAD_DIM ** -0.5 if scale is None else scale, window, sinks,
             stream if stream is None else _stream_handle(stream)), "attn_f16_paged_fwd")
+
+
+# ---------------------------------------------------------------- 8-bit products
+def gemm_f8_quantize(plan: int, blocks: int, format: int, type: int, batch: int, rows: int,
+                     cols: int, X: int, ldx: int, x_batch: int, source: int, choices: int,
+                     x_rows: int, Q: int, ldq: int, q_batch: int, S: int, Q2: int = 0, S2: int = 0,
+                     stream: int = 0) -> None:
+    """Enqueue a quantisation into blocks of 128 (device pointers; see gemm_f8.h)."""
+    _check(load().gemm_f8_quantize(plan, blocks, format, type, batch, rows, cols, X, ldx, x_batch,
+                                   source, choices, x_rows, Q, ldq, q_batch, S, Q2, S2, stream),
+           "gemm_f8_quantize")
+
+
+def gemm_f8_quantize_validate(*args) -> int:
+    """The argument check of gemm_f8_quantize (its arguments without plan and stream)."""
+    return load().gemm_f8_quantize_validate(*args)
+
+
+def gemm_f8_run(plan: int, form: int, M: int, N: int, K: int, experts: int, starts: int,
+                A: GemmF8Operand, B: GemmF8Operand, C: int, ldc: int, c_batch: int, type: int,
+                accumulate: int = 0, workspace: int = 0, workspace_bytes: int = 0,
+                stream: int = 0) -> None:
+    """Enqueue a product of 8-bit operands with block scales (see gemm_f8.h)."""
+    _check(load().gemm_f8_run(plan, form, M, N, K, experts, starts, ctypes.byref(A),
+                              ctypes.byref(B), C, ldc, c_batch, type, accumulate, workspace,
+                              workspace_bytes, stream), "gemm_f8_run")
+
+
+def gemm_f8_workspace(plan: int, form: int, M: int, N: int, K: int, experts: int = 1,
+                      a_transposed: int = 0) -> int:
+    """Bytes of workspace that gemm_f8_run needs for these sizes."""
+    return load().gemm_f8_workspace(plan, form, M, N, K, experts, a_transposed)
+
+
+def gemm_f8_validate(form, M, N, K, experts, starts, A, B, C, ldc, c_batch, type,
+                     accumulate=0) -> int:
+    return load().gemm_f8_validate(form, M, N, K, experts, starts, A and ctypes.byref(A),
+                                   B and ctypes.byref(B), C, ldc, c_batch, type, accumulate)
+
+
+def experts_maps(plan: int, entries: int, experts: int, wide: int, num_experts: int, align: int,
+                 max_rows: int, starts: int, rows: int, source: int, stream: int = 0) -> None:
+    """Enqueue the sort of entries by expert (device pointers; see gemm_f8.h)."""
+    _check(load().experts_maps(plan, entries, experts, wide, num_experts, align, max_rows, starts,
+                               rows, source, stream), "experts_maps")
+
+
+def experts_maps_validate(*args) -> int:
+    return load().experts_maps_validate(*args)
+
+
+def experts_max_rows(entries: int, num_experts: int, align: int = 1) -> int:
+    """Rows that hold any choice of experts."""
+    return _check(load().experts_max_rows(entries, num_experts, align), "experts_max_rows")
+
+
+def experts_gather(plan: int, type: int, rows: int, cols: int, X: int, ldx: int, x_rows: int,
+                   choices: int, source: int, Y: int, ldy: int, stream: int = 0) -> None:
+    """Enqueue the gather of rows in the experts' order (see gemm_f8.h)."""
+    _check(load().experts_gather(plan, type, rows, cols, X, ldx, x_rows, choices, source, Y, ldy,
+                                 stream), "experts_gather")
+
+
+def experts_gather_validate(*args) -> int:
+    return load().experts_gather_validate(*args)
+
+
+def experts_combine(plan: int, type: int, tokens: int, choices: int, cols: int, S: int, lds: int,
+                    s_rows: int, rows: int, weights: int, weights_type: int, Y: int, ldy: int,
+                    stream: int = 0) -> None:
+    """Enqueue the weighted sums of the experts' rows (see gemm_f8.h)."""
+    _check(load().experts_combine(plan, type, tokens, choices, cols, S, lds, s_rows, rows, weights,
+                                  weights_type, Y, ldy, stream), "experts_combine")
+
+
+def experts_combine_validate(*args) -> int:
+    return load().experts_combine_validate(*args)
+
+
+def experts_combine_gradient(plan: int, type: int, tokens: int, choices: int, cols: int, dY: int,
+                             lddy: int, S: int, lds: int, s_rows: int, rows: int, source: int,
+                             weights: int, weights_type: int, dS: int, ldds: int, dw: int,
+                             stream: int = 0) -> None:
+    """Enqueue experts_combine's gradients (see gemm_f8.h)."""
+    _check(load().experts_combine_gradient(plan, type, tokens, choices, cols, dY, lddy, S, lds,
+                                           s_rows, rows, source, weights, weights_type, dS, ldds,
+                                           dw, stream), "experts_combine_gradient")
+
+
+def experts_combine_gradient_validate(*args) -> int:
+    return load().experts_combine_gradient_validate(*args)
+
+
+class Blocks(collections.namedtuple("Blocks", "data scales")):
+    """8-bit codes with a scale for each block of 128: data, float8_e4m3fn or
+    float8_e5m2 [.., rows, cols], and scales, float32 with an entry for each
+    block (see quantize).  ``t()`` is the transposed matrix, without a copy."""
+    __slots__ = ()
+
+    def t(self) -> "Blocks":
+        return Blocks(self.data.transpose(-1, -2), self.scales.transpose(-1, -2))
+
+
+_F8_BLOCKS = {"rows": F8_ROWS, "columns": F8_COLUMNS, "tiles": F8_TILES, "both": F8_BOTH}
+
+
+def _f8_format(dtype) -> int:
+    import torch
+    if dtype is None or dtype == torch.float8_e4m3fn:
+        return F8_E4M3
+    if dtype == torch.float8_e5m2:
+        return F8_E5M2
+    raise TypeError("dtype must be torch.float8_e4m3fn or torch.float8_e5m2")
+
+
+def _f8_type(dtype) -> int:
+    import torch
+    if dtype is None or dtype == torch.float16:
+        return F8_F16
+    if dtype == torch.bfloat16:
+        return F8_BF16
+    if dtype == torch.float32:
+        return F8_F32
+    raise TypeError("dtype must be torch.float16, bfloat16 or float32")
+
+
+def quantize(plan: Plan, X, blocks: str = "rows", dtype=None, maps=None, stream=None):
+    """X (float16, bfloat16 or float32, [rows, cols] or [matrices, rows, cols],
+    row-major or a transposed view) as 8-bit codes with a scale for each block
+    of 128: ``blocks`` "rows" (128 numbers along a row; scales [rows,
+    ceil(cols / 128)]), "columns" (along a column; [ceil(rows / 128), cols]) or
+    "tiles" (128 x 128).  "both" returns two Blocks, "rows" and "columns", from
+    one reading.  dtype: torch.float8_e4m3fn (if None) or float8_e5m2.
+
+    scale = max(largest finite magnitude, 2^-100) / the format's largest number;
+    a code is the nearest to x / scale (computed as x times the rounded
+    reciprocal).  Infinities and NaN become NaN.  With ``maps`` (an ExpertMaps)
+    X's rows are those of tokens, and the result's are in the experts' order,
+    as of expert_gather(X).  The codes carry no gradient.
+    """
+    if blocks not in _F8_BLOCKS:
+        raise ValueError("blocks is 'rows', 'columns', 'tiles' or 'both'")
+    source, choices = None, 1
+    if maps is not None:
+        source, choices = maps.source, maps.rows.shape[1]
+        if X.dim() != 2 or X.shape[0] != maps.rows.shape[0]:
+            raise ValueError("X must have a row for each token of the maps")
+    r = _result((_calls or _torch_calls()).quantize(
+        plan.handle, plan.device, X, _F8_BLOCKS[blocks], _f8_format(dtype), source, choices,
+        stream if stream is None else _stream_handle(stream)), "gemm_f8_quantize")
+    return (Blocks(r[0], r[1]), Blocks(r[2], r[3])) if len(r) == 4 else Blocks(r[0], r[1])
+
+
+def matmul_f8(plan: Plan, A, B, C=None, dtype=None, starts=None, accumulate: bool = False,
+              stream=None):
+    """C = A @ B for Blocks A [M, K] and B [K, N] whose blocks lie along K or
+    are tiles (both row-major or transposed views; codes on 16-byte boundaries,
+    as quantize makes them).  C: float16 (if None), bfloat16 or float32 by
+    ``dtype``, or given; FP32 sums, rounded once.  ``accumulate`` adds to a
+    given float32 C.
+
+    With ``starts`` (int32 [experts + 1], from expert_maps) the product is by
+    expert.  B [experts, K, N]: rows starts[e] to starts[e + 1] - 1 of A times
+    B[e], and rows past the last expert's are 0.  B [K, N]: C [experts, M, N],
+    each of A's columns and B's rows starts[e] to starts[e + 1] - 1 (starts are
+    multiples of 128), 0 where there are none: the gradient of weights.
+    Forward only: C carries no gradient (linear_f8 does).
+    """
+    return _result((_calls or _torch_calls()).matmul_f8(
+        plan.handle, plan.device, A.data, A.scales, B.data, B.scales, C, _f8_type(dtype), starts,
+        accumulate, stream if stream is None else _stream_handle(stream)), "gemm_f8_run")
+
+
+def _on_stream(plan: Plan, stream):
+    """A context in which ``stream`` (None: no change) is the current one: an
+    autograd function's backward pass runs on its forward pass's stream."""
+    if stream is None:
+        return contextlib.nullcontext()
+    import torch
+    handle = _stream_handle(stream)
+    return torch.cuda.stream(torch.cuda.ExternalStream(handle, device=plan.device) if handle
+                             else torch.cuda.default_stream(plan.device))
+
+
+_f8_functions = None
+
+
+def _autograd_f8():
+    """The autograd functions (made on first use: torch is not loaded with this
+    module)."""
+    global _f8_functions
+    if _f8_functions is not None:
+        return _f8_functions
+    import torch
+    from torch.autograd.function import once_differentiable
+
+    class Linear(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, X, W, codes, scales, starts, plan, formats, training):
+            want_x, want_w = (training and n for n in ctx.needs_input_grad[:2])
+            ctx.call = plan, formats, X.dtype, W.dtype if codes is None else None
+            Q = quantize(plan, W, "tiles", formats[0]) if codes is None else Blocks(codes, scales)
+            if want_w:
+                R, C = quantize(plan, X, "both", formats[0])
+            else:
+                R, C = quantize(plan, X, "rows", formats[0]), (None, None)
+            ctx.save_for_backward(*(C if want_w else (None, None)),
+                                  *(Q if want_x else (None, None)), starts)
+            return matmul_f8(plan, R, Q.t(), dtype=X.dtype, starts=starts)
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, dY):
+            xc, xs, wc, ws, starts = ctx.saved_tensors
+            plan, formats, x_type, w_type = ctx.call
+            dY = dY.contiguous()
+            dX = dW = R = C = None
+            if wc is not None and xc is not None:
+                R, C = quantize(plan, dY, "both", formats[1])
+            elif wc is not None:
+                R = quantize(plan, dY, "rows", formats[1])
+            elif xc is not None:
+                C = quantize(plan, dY, "columns", formats[1])
+            if R is not None:
+                dX = matmul_f8(plan, R, Blocks(wc, ws), dtype=x_type, starts=starts)
+            if C is not None:
+                dW = matmul_f8(plan, C.t(), Blocks(xc, xs), dtype=w_type, starts=starts)
+            return dX, dW, None, None, None, None, None, None
+
+    class Gather(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, X, starts, rows, source, plan):
+            ctx.save_for_backward(starts, rows, source)
+            ctx.plan = plan
+            return _result((_calls or _torch_calls()).expert_gather(
+                plan.handle, plan.device, X, rows, source, None), "experts_gather")
+
+        @staticmethod
+        def backward(ctx, dY):
+            maps = ExpertMaps._make(ctx.saved_tensors)
+            return expert_combine(ctx.plan, dY.contiguous(), maps), None, None, None, None
+
+    class Combine(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, S, weights, starts, rows, source, plan):
+            ctx.save_for_backward(S if weights is not None and ctx.needs_input_grad[1] else None,
+                                  weights, starts, rows, source)
+            ctx.plan = plan
+            return _result((_calls or _torch_calls()).expert_combine(
+                plan.handle, plan.device, S, rows, source, weights, None), "experts_combine")
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, dY):
+            S, weights, starts, rows, source = ctx.saved_tensors
+            plan, dY = ctx.plan, dY.contiguous()
+            if weights is None:
+                return (expert_gather(plan, dY, ExpertMaps(starts, rows, source)), None, None, None,
+                        None, None)
+            want_s, want_w = ctx.needs_input_grad[:2]
+            dS, dw = _result((_calls or _torch_calls()).expert_combine_gradient(
+                plan.handle, plan.device, dY, S, rows, source, weights, want_s, want_w, None),
+                "experts_combine_gradient")
+            return dS, dw, None, None, None, None
+
+    _f8_functions = Linear, Gather, Combine
+    return _f8_functions
+
+
+def linear_f8(plan: Plan, X, W, starts=None, dtype=None, grad_dtype=None, stream=None):
+    """X @ W^T in 8 bits, with its gradients: X [.., K] and W [N, K], float16,
+    bfloat16 or float32, each quantised here (X by rows, W by tiles); or W as
+    Blocks of tiles ([N, K], from quantize), which then carries no gradient.
+    The result has X's type.  Backward, the gradient of the result is quantised
+    by rows for X's gradient and along the rows' dimension, like X, for W's;
+    ``dtype`` and ``grad_dtype`` are the formats of X and W and of that
+    gradient (float8_e4m3fn if None).  X's gradient has X's type, W's W's.
+
+    With ``starts`` X is [rows, K], sorted by expert, and W [experts, N, K]; for
+    W's gradient the starts are multiples of 128 (expert_maps with align=128)
+    and rows that no expert has are 0, as expert_gather leaves them.  ``plan``
+    must last until the backward pass, which runs on the stream of the call.
+    """
+    frozen = isinstance(W, Blocks)
+    shape = X.shape
+    if starts is None:
+        X = X.reshape(-1, shape[-1])
+    elif X.dim() != 2:
+        raise ValueError("X must be [rows, K] where starts are given")
+    if (W.data if frozen else W).dim() != (2 if starts is None else 3):
+        raise ValueError("W must be [N, K], or [experts, N, K] with starts")
+    import torch
+    formats = dtype or torch.float8_e4m3fn, grad_dtype or torch.float8_e4m3fn
+    with _on_stream(plan, stream):
+        Y = _autograd_f8()[0].apply(X, None if frozen else W, W.data if frozen else None,
+                                    W.scales if frozen else None, starts, plan, formats,
+                                    torch.is_grad_enabled())
+        return Y if starts is not None else Y.view(*shape[:-1], Y.shape[-1])
+
+
+# ---------------------------------------------------------------- experts
+ExpertMaps = collections.namedtuple("ExpertMaps", "starts rows source")
+ExpertMaps.__doc__ = """The order of tokens' choices by expert (see expert_maps)."""
+
+
+def expert_maps(plan: Plan, experts, num_experts: int, align: int = 1, stream=None) -> ExpertMaps:
+    """The order by expert of the choices of a router: experts, int32 or int64
+    [tokens, choices], the expert that each choice goes to (negative: none).
+
+    Returns starts [num_experts + 1], each expert's first row, a multiple of
+    ``align``; rows [tokens, choices], the row of each choice (-1: none), by
+    expert and then by token; and source [rows], the choice (token * choices +
+    choice) at each row, -1 for those that fill an expert's rows up and those
+    past the last expert.  There are as many rows as any router can need
+    (experts_max_rows), so that a step's shapes do not depend on its tokens.
+    """
+    return ExpertMaps._make(_result((_calls or _torch_calls()).expert_maps(
+        plan.handle, plan.device, experts, num_experts, align,
+        stream if stream is None else _stream_handle(stream)), "experts_maps"))
+
+
+def expert_gather(plan: Plan, X, maps: ExpertMaps, stream=None):
+    """The rows of X (float16, bfloat16 or float32 [tokens, cols]) in the
+    experts' order: row r is that of the token of maps.source[r], 0 where there
+    is none.  Differentiable (the gradient is expert_combine's sum)."""
+    with _on_stream(plan, stream):
+        return _autograd_f8()[1].apply(X, *maps, plan)
+
+
+def expert_combine(plan: Plan, S, maps: ExpertMaps, weights=None, stream=None):
+    """Each token's sum over its choices of weights times rows of S (float16,
+    bfloat16 or float32 [rows, cols], in the experts' order): FP32 sums in the
+    choices' order, rounded once.  weights: [tokens, choices], float32 or of
+    S's type (None: all 1); choices without a row are left out.  Differentiable
+    in S and weights."""
+    with _on_stream(plan, stream):
+        return _autograd_f8()[2].apply(S, weights, *maps, plan)

@@ -1,14 +1,15 @@
 """Build the gemm_f16 shared library in-tree with nvcc for sm_103a.
 
 Output: async_barrier_pipelined_gb300/_lib/libgemm_f16.so (git-ignored).
-Five translation units (plan and shared host code; the kernels and entry
+Eight translation units (plan and shared host code; the kernels and entry
 points of the GEMM, the attention, the paged-cache maps with rotary
-positions, and the attention over a paged cache) are compiled in parallel
-with one -gencode each and linked into one library, so a build takes seconds
-on either the x86 build host or the aarch64 GPU host.
+positions, the attention over a paged cache, the 8-bit products, the
+quantisation, and the rows of layers of experts) are compiled in parallel
+with one -gencode each and linked into one library, so a build takes less than
+a minute on either the x86 build host or the aarch64 GPU host.
 
-Beside it, _lib/paged_torch_calls.so: the paged-cache calls for torch tensors
-(csrc/torch_calls.cpp, host code only, compiled against the installed torch,
+Beside it, _lib/paged_torch_calls.so: the paged-cache and 8-bit calls for torch
+tensors (csrc/torch_calls.cpp, host code only, compiled against the installed torch,
 and again when another torch or Python is installed).  Without torch the
 library alone is built: its C ABI needs none.
 """
@@ -30,17 +31,20 @@ LIB_DIR = os.path.join(PKG_DIR, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libgemm_f16.so")
 
 SOURCES = [os.path.join(CSRC, f) for f in ("plan.cu", "gemm_f16.cu", "attn_f16.cu",
-                                             "paged_f16.cu", "paged_attn.cu")]
+                                             "paged_f16.cu", "paged_attn.cu", "f8_gemm.cu",
+                                             "f8_quant.cu", "experts.cu")]
 HEADERS = [os.path.join(CSRC, f) for f in ("host.h", "ptx.cuh", "schedule.h", "common.cuh",
                                             "gemm_pair.cuh", "gemm_quad.cuh", "attn_f16.cuh",
                                             "attn_pair.cuh", "paged_schedule.h",
-                                            "paged_small.cuh", "paged_large.cuh")]
+                                            "paged_small.cuh", "paged_large.cuh", "f8.cuh",
+                                            "f8_large.cuh", "f8_small.cuh")]
 DEPENDS = SOURCES + HEADERS + [os.path.join(INCLUDE, "gemm_f16.h"),
-                               os.path.join(INCLUDE, "attn_f16.h")]
+                               os.path.join(INCLUDE, "attn_f16.h"),
+                               os.path.join(INCLUDE, "gemm_f8.h")]
 
 CALLS_NAME = "paged_torch_calls"
 CALLS_PATH = os.path.join(LIB_DIR, CALLS_NAME + ".so")
-CALLS_SOURCE = os.path.join(CSRC, "torch_calls.cpp")
+CALLS_SOURCE = os.path.join(CSRC, "torch_calls.cpp")   # with torch_f8.h
 CALLS_STAMP = os.path.join(LIB_DIR, CALLS_NAME + ".for")   # the torch that they were built for
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -83,8 +87,10 @@ def _torch_stamp() -> str | None:
 
 
 def _calls_fresh(stamp: str) -> bool:
-    if not _fresh(CALLS_PATH, [CALLS_SOURCE, os.path.join(INCLUDE, "attn_f16.h"),
-                               os.path.join(INCLUDE, "gemm_f16.h")]):
+    if not _fresh(CALLS_PATH, [CALLS_SOURCE, os.path.join(CSRC, "torch_f8.h"),
+                               os.path.join(INCLUDE, "attn_f16.h"),
+                               os.path.join(INCLUDE, "gemm_f16.h"),
+                               os.path.join(INCLUDE, "gemm_f8.h")]):
         return False
     try:
         with open(CALLS_STAMP) as f:

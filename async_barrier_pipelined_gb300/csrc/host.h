@@ -16,6 +16,7 @@
 
 #include "attn_f16.h"
 #include "gemm_f16.h"
+#include "gemm_f8.h"
 
 namespace gf16 {
 namespace host {
@@ -110,6 +111,7 @@ struct gemm_f16_plan_s {
   int max_quads = 0;   // co-resident clusters of four for the cluster-of-four kernel
   int multicast = 1;   // whether that kernel, whose copies are multicast, may run
   int paged_pairs = 0; // co-resident clusters of two for the paged attention kernel
+  int f8_pairs = 0;    // co-resident clusters of two for the 8-bit product's large kernel
   int attn_pairs = 0;  // co-resident clusters of two for the pair attention kernel
   void* ws = nullptr;
   size_t ws_bytes = 0;
@@ -174,6 +176,8 @@ int attn_plan_init(gemm_f16_plan_s* p, const cudaDeviceProp& prop);
 void attn_plan_release(gemm_f16_plan_s* p);
 int paged_plan_init(gemm_f16_plan_s* p, const cudaDeviceProp& prop);
 void paged_plan_release(gemm_f16_plan_s* p);
+int f8_plan_init(gemm_f16_plan_s* p, const cudaDeviceProp& prop);   // nothing to release
+int experts_plan_init(gemm_f16_plan_s* p, const cudaDeviceProp& prop);
 
 }  // namespace host
 }  // namespace gf16

@@ -215,6 +215,8 @@ int gemm_f16_plan(gemm_f16_plan_t* out, int device) {
   int rc = gemm_plan_init(p, prop);
   if (!rc) rc = attn_plan_init(p, prop);
   if (!rc) rc = paged_plan_init(p, prop);
+  if (!rc) rc = f8_plan_init(p, prop);
+  if (!rc) rc = experts_plan_init(p, prop);
   if (rc) {
     delete p;
     return rc;

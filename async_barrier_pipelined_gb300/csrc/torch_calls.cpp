@@ -247,10 +247,13 @@ py::object paged_attention(int64_t plan, int device, const Tensor& q, const Tens
 
 }  // namespace
 
+#include "torch_f8.h"
+
 PYBIND11_MODULE(TORCH_EXTENSION_NAME, m) {
-  m.doc() = "attn_f16.h's paged-cache calls for torch tensors";
+  m.doc() = "attn_f16.h's paged-cache calls and gemm_f8.h's calls for torch tensors";
   m.def("paged_maps", &paged_maps);
   m.def("rotary", &rotary);
   m.def("rotary_to_cache", &rotary_to_cache);
   m.def("paged_attention", &paged_attention);
+  add_f8_calls(m);
 }

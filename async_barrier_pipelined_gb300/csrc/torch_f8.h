@@ -1,0 +1,312 @@
+// gemm_f8.h's calls for torch tensors: argument checks, output tensors and the
+// C ABI call, in C++ for the same reason as torch_calls.cpp (a generation
+// step makes several of them per layer).  Nothing is computed here.  A bad
+// tensor raises ValueError; a code of the C ABI is returned as a number for
+// the caller to raise.
+//
+// Part of torch_calls.cpp (and of its module), after the helpers there.
+#pragma once
+
+#include "gemm_f8.h"
+
+namespace {
+
+void on_device(const Tensor& x, const char* name, int device) {
+  if (!x.is_cuda() || x.get_device() != device)
+    refuse(std::string(name) + " must be on the plan's device");
+}
+
+// GEMM_F8_F16, _BF16 or _F32.
+int type_of(at::ScalarType t, const char* name) {
+  if (t == at::kHalf) return GEMM_F8_F16;
+  if (t == at::kBFloat16) return GEMM_F8_BF16;
+  if (t == at::kFloat) return GEMM_F8_F32;
+  refuse(std::string(name) + " must be float16, bfloat16 or float32");
+}
+
+int format_of(at::ScalarType t, const char* name) {
+  if (t == at::kFloat8_e4m3fn) return GEMM_F8_E4M3;
+  if (t == at::kFloat8_e5m2) return GEMM_F8_E5M2;
+  refuse(std::string(name) + " must be float8_e4m3fn or float8_e5m2");
+}
+
+int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+int64_t blocks_of(int64_t n) { return (n + 127) / 128; }
+
+// ------------------------------------------------------------------ quantize
+
+// -> (codes, scales) or, for BOTH, (codes, scales, codes, scales).
+py::object quantize(int64_t plan, int device, const Tensor& x_, int blocks, at::ScalarType dtype,
+                    const c10::optional<Tensor>& source, int64_t choices,
+                    const c10::optional<int64_t>& stream) {
+  const int type = type_of(x_.scalar_type(), "X"), format = format_of(dtype, "dtype");
+  on_device(x_, "X", device);
+  if (x_.dim() != 2 && x_.dim() != 3) refuse("X must be [rows, cols] or [matrices, rows, cols]");
+  if (x_.dim() == 3 && (blocks == GEMM_F8_BOTH || source))
+    refuse("several matrices have blocks of one kind and no maps");
+  // A transposed view is quantised as it is stored.
+  const bool turned = !(x_.size(-1) <= 1 || x_.stride(-1) == 1) && x_.stride(-2) == 1;
+  if (turned && source) refuse("X must be row-major where maps are given");
+  const Tensor x = turned ? x_.transpose(-1, -2) : x_;
+  if (x.size(-1) > 1 && x.stride(-1) != 1) refuse("X must be row-major or a transposed row-major view");
+  const int64_t cols = x.size(-1), batch = x.dim() == 3 ? x.size(0) : 1;
+  if (cols < 1) refuse("X must have columns");
+  if (turned) blocks = blocks == GEMM_F8_ROWS ? GEMM_F8_COLUMNS : blocks == GEMM_F8_COLUMNS ? GEMM_F8_ROWS : blocks;
+  if (source) need(*source, "maps.source", at::kInt, 1, device);
+  const int64_t rows = source ? source->size(0) : x.size(-2);
+  OnStream on(stream, device);
+  const int64_t pitch = up(cols, 16);
+  const auto codes = [&] {
+    Tensor q = x.dim() == 3 ? at::empty({batch, rows, pitch}, x.options().dtype(dtype))
+                            : at::empty({rows, pitch}, x.options().dtype(dtype));
+    return pitch == cols ? q : q.narrow(-1, 0, cols);
+  };
+  const auto scales = [&](int kind) {
+    const int64_t r = kind == GEMM_F8_ROWS ? rows : blocks_of(rows);
+    const int64_t c = kind == GEMM_F8_COLUMNS ? cols : blocks_of(cols);
+    return x.dim() == 3 ? at::empty({batch, r, c}, x.options().dtype(at::kFloat))
+                        : at::empty({r, c}, x.options().dtype(at::kFloat));
+  };
+  const bool both = blocks == GEMM_F8_BOTH;
+  Tensor q = codes(), s = scales(both ? GEMM_F8_ROWS : blocks), q2, s2;
+  if (both) {
+    q2 = codes();
+    s2 = scales(GEMM_F8_COLUMNS);
+  }
+  const int rc = gemm_f8_quantize(
+      plan_of(plan), blocks, format, type, narrow(batch, "matrices"), narrow(rows, "rows"),
+      narrow(cols, "cols"), x.const_data_ptr(), x.size(-2) > 1 ? x.stride(-2) : pitch,
+      batch > 1 ? x.stride(0) : 0, source ? ints(*source) : nullptr, narrow(choices, "choices"),
+      narrow(x.size(-2), "rows"), q.data_ptr(), pitch, rows * pitch, s.data_ptr<float>(),
+      both ? q2.data_ptr() : nullptr, both ? s2.data_ptr<float>() : nullptr, on.raw());
+  if (rc < 0) return py::int_(rc);
+  if (turned) {
+    q = q.transpose(-1, -2);
+    s = s.transpose(-1, -2);
+    if (both) {
+      q2 = q2.transpose(-1, -2);
+      s2 = s2.transpose(-1, -2);
+      return py::make_tuple(q2, s2, q, s);
+    }
+  }
+  return both ? py::make_tuple(q, s, q2, s2) : py::make_tuple(q, s);
+}
+
+// ------------------------------------------------------------------ product
+
+// Codes [.., rows, cols] with scales; `inner_last`: the inner dimension is the
+// last one (A), else the one before (B).
+gemm_f8_operand operand(const Tensor& x, const Tensor& s, const char* name, bool inner_last,
+                        int device) {
+  gemm_f8_operand o = {};
+  o.format = format_of(x.scalar_type(), name);
+  on_device(x, name, device);
+  on_device(s, name, device);
+  if (s.scalar_type() != at::kFloat || s.dim() != x.dim())
+    refuse(std::string(name) + "'s scales must be float32 and have its codes' dimensions");
+  const int64_t rows = x.size(-2), cols = x.size(-1);
+  if (x.stride(-1) == 1 && (rows <= 1 || x.stride(-2) >= cols)) {
+    o.ld = rows > 1 ? x.stride(-2) : up(cols, 16);
+  } else if (x.stride(-2) == 1 && (cols <= 1 || x.stride(-1) >= rows)) {
+    o.transposed = 1;
+    o.ld = cols > 1 ? x.stride(-1) : up(rows, 16);
+  } else if (rows > 0 && cols > 0) {
+    refuse(std::string(name) + " must be row-major or a transposed row-major view");
+  }
+  o.data = x.const_data_ptr();
+  o.scales = s.const_data_ptr<float>();
+  const int64_t inner = inner_last ? cols : rows, outer = inner_last ? rows : cols;
+  const int64_t s_inner = s.size(inner_last ? -1 : -2), s_outer = s.size(inner_last ? -2 : -1);
+  if (s_inner != blocks_of(inner) || (s_outer != outer && s_outer != blocks_of(outer)))
+    refuse(std::string(name) +
+           "'s scales must have an entry for each 128 of the inner dimension, and for each or "
+           "each 128 of the other");
+  o.tiles = s_outer != outer;
+  o.s_inner = s.stride(inner_last ? -1 : -2);
+  o.s_outer = s.stride(inner_last ? -2 : -1);
+  if (x.dim() == 3) {
+    if (s.size(0) != x.size(0)) refuse(std::string(name) + "'s scales must be one set for each matrix");
+    o.batch = x.stride(0);
+    o.s_batch = s.stride(0);
+  }
+  return o;
+}
+
+py::object matmul_f8(int64_t plan, int device, const Tensor& a, const Tensor& sa, const Tensor& b,
+                     const Tensor& sb, const c10::optional<Tensor>& out_, at::ScalarType dtype,
+                     const c10::optional<Tensor>& starts, bool accumulate,
+                     const c10::optional<int64_t>& stream) {
+  if (a.dim() != 2 || (b.dim() != 2 && !(b.dim() == 3 && starts)))
+    refuse("A must be [M, K] and B [K, N], or [experts, K, N] with starts");
+  const int form = !starts ? GEMM_F8_DENSE : b.dim() == 3 ? GEMM_F8_BY_ROWS : GEMM_F8_BY_INNER;
+  const int64_t M = a.size(0), K = a.size(1), N = b.size(-1);
+  if (b.size(-2) != K) refuse("A and B must have the same inner dimension");
+  int64_t experts = 1;
+  if (starts) {
+    need(*starts, "starts", at::kInt, 1, device);
+    experts = starts->size(0) - 1;
+    if (experts < 1 || (form == GEMM_F8_BY_ROWS && b.size(0) != experts))
+      refuse("starts must have an entry more than there are experts");
+  }
+  const gemm_f8_operand A = operand(a, sa, "A", true, device);
+  const gemm_f8_operand B = operand(b, sb, "B", false, device);
+  OnStream on(stream, device);
+  Tensor c;
+  if (out_) {
+    c = *out_;
+    on_device(c, "C", device);
+    const bool shape = form == GEMM_F8_BY_INNER
+                           ? c.dim() == 3 && c.size(0) == experts && c.size(1) == M && c.size(2) == N
+                           : c.dim() == 2 && c.size(0) == M && c.size(1) == N;
+    if (!shape || (N > 1 && c.stride(-1) != 1)) refuse("C must be row-major and of the product's shape");
+  } else {
+    if (accumulate) refuse("accumulate needs C");
+    const auto o = a.options().dtype(dtype);
+    c = form == GEMM_F8_BY_INNER ? at::empty({experts, M, N}, o) : at::empty({M, N}, o);
+  }
+  const int type = type_of(c.scalar_type(), "C");
+  if (accumulate && type != GEMM_F8_F32) refuse("accumulate needs a float32 C");
+  if (c.numel() == 0) return py::cast(c);
+  const gemm_f16_plan_t p = plan_of(plan);
+  const int m = narrow(M, "M"), n = narrow(N, "N"), k = narrow(K, "K"), e = narrow(experts, "experts");
+  const size_t bytes = gemm_f8_workspace(p, form, m, n, k, e, A.transposed);
+  Tensor ws;
+  if (bytes > 0) ws = at::empty({(int64_t)bytes}, a.options().dtype(at::kByte));
+  const int rc = gemm_f8_run(p, form, m, n, k, e, starts ? ints(*starts) : nullptr, &A, &B,
+                             c.data_ptr(), M > 1 ? c.stride(-2) : N, c.dim() == 3 ? c.stride(0) : 0,
+                             type, accumulate, bytes > 0 ? ws.data_ptr() : nullptr, bytes, on.raw());
+  return done(rc, py::cast(c));
+}
+
+// ------------------------------------------------------------------ experts
+
+// -> (starts, rows, source), or an error code.
+py::object expert_maps(int64_t plan, int device, const Tensor& picks, int64_t num_experts,
+                       int64_t align, const c10::optional<int64_t>& stream) {
+  const bool wide = picks.scalar_type() == at::kLong;
+  need(picks, "experts", wide ? at::kLong : at::kInt, 2, device);
+  if (!picks.is_contiguous()) refuse("experts must be contiguous");
+  const int64_t entries = picks.numel();
+  const int64_t most = experts_max_rows(narrow(entries, "experts"), narrow(num_experts, "num_experts"),
+                                        narrow(align, "align"));
+  if (most < 0) return py::int_(most);
+  OnStream on(stream, device);
+  const auto o = picks.options().dtype(at::kInt);
+  const Tensor starts = at::empty({num_experts + 1}, o), rows = at::empty(picks.sizes(), o),
+               source = at::empty({most}, o);
+  const int rc = experts_maps(plan_of(plan), (int)entries, picks.const_data_ptr(), wide,
+                              (int)num_experts, (int)align, narrow(most, "rows"),
+                              starts.data_ptr<int32_t>(), rows.data_ptr<int32_t>(),
+                              source.data_ptr<int32_t>(), on.raw());
+  return done(rc, py::make_tuple(starts, rows, source));
+}
+
+int64_t row_stride(const Tensor& x) { return x.size(0) > 1 ? x.stride(0) : x.size(1); }
+
+void need_rows(const Tensor& x, const char* name, int device) {
+  type_of(x.scalar_type(), name);
+  need(x, name, x.scalar_type(), 2, device);
+}
+
+void need_maps(const Tensor& rows, const Tensor& source, int device) {
+  need(rows, "maps.rows", at::kInt, 2, device);
+  need(source, "maps.source", at::kInt, 1, device);
+  if (!rows.is_contiguous() || rows.size(1) < 1) refuse("maps.rows must be contiguous [tokens, choices]");
+}
+
+py::object expert_gather(int64_t plan, int device, const Tensor& x, const Tensor& rows,
+                         const Tensor& source, const c10::optional<int64_t>& stream) {
+  need_rows(x, "X", device);
+  need_maps(rows, source, device);
+  if (x.size(0) != rows.size(0)) refuse("X must have a row for each token of the maps");
+  OnStream on(stream, device);
+  const Tensor y = at::empty({source.size(0), x.size(1)}, x.options());
+  const int rc = experts_gather(plan_of(plan), type_of(x.scalar_type(), "X"),
+                                narrow(source.size(0), "rows"), narrow(x.size(1), "cols"),
+                                x.const_data_ptr(), row_stride(x), narrow(x.size(0), "rows"),
+                                narrow(rows.size(1), "choices"), ints(source), y.data_ptr(),
+                                x.size(1), on.raw());
+  return done(rc, py::cast(y));
+}
+
+int weights_type(const c10::optional<Tensor>& w, const Tensor& s, const Tensor& rows, int device) {
+  if (!w) return GEMM_F8_F32;
+  on_device(*w, "weights", device);
+  if (w->sizes() != rows.sizes() || !w->is_contiguous() ||
+      (w->scalar_type() != at::kFloat && w->scalar_type() != s.scalar_type()))
+    refuse("weights must be contiguous [tokens, choices], float32 or of the rows' type");
+  return type_of(w->scalar_type(), "weights");
+}
+
+py::object expert_combine(int64_t plan, int device, const Tensor& s, const Tensor& rows,
+                          const Tensor& source, const c10::optional<Tensor>& weights,
+                          const c10::optional<int64_t>& stream) {
+  need_rows(s, "S", device);
+  need_maps(rows, source, device);
+  if (s.size(0) != source.size(0)) refuse("S must have a row for each row of the maps");
+  const int wt = weights_type(weights, s, rows, device);
+  OnStream on(stream, device);
+  const Tensor y = at::empty({rows.size(0), s.size(1)}, s.options());
+  const int rc = experts_combine(plan_of(plan), type_of(s.scalar_type(), "S"),
+                                 narrow(rows.size(0), "tokens"), narrow(rows.size(1), "choices"),
+                                 narrow(s.size(1), "cols"), s.const_data_ptr(), row_stride(s),
+                                 narrow(s.size(0), "rows"), ints(rows),
+                                 weights ? weights->const_data_ptr() : nullptr, wt, y.data_ptr(),
+                                 s.size(1), on.raw());
+  return done(rc, py::cast(y));
+}
+
+// -> (dS or None, dweights or None), or an error code.
+py::object expert_combine_gradient(int64_t plan, int device, const Tensor& dy,
+                                   const c10::optional<Tensor>& s, const Tensor& rows,
+                                   const Tensor& source, const c10::optional<Tensor>& weights,
+                                   bool want_s, bool want_w, const c10::optional<int64_t>& stream) {
+  need_rows(dy, "dY", device);
+  need_maps(rows, source, device);
+  const int64_t n = source.size(0), cols = dy.size(1);
+  if (dy.size(0) != rows.size(0)) refuse("dY must have a row for each token of the maps");
+  want_w = want_w && weights;
+  if (want_w) {
+    if (!s) refuse("the weights' gradient needs S");
+    need_rows(*s, "S", device);
+    if (s->size(0) != n || s->size(1) != cols || s->scalar_type() != dy.scalar_type())
+      refuse("S must have a row for each row of the maps, and dY's columns and type");
+  }
+  const int wt = weights_type(weights, dy, rows, device);
+  OnStream on(stream, device);
+  Tensor ds, dw;
+  if (want_s) ds = at::empty({n, cols}, dy.options());
+  if (want_w) dw = at::empty(weights->sizes(), weights->options());
+  const int rc = experts_combine_gradient(
+      plan_of(plan), type_of(dy.scalar_type(), "dY"), narrow(rows.size(0), "tokens"),
+      narrow(rows.size(1), "choices"), narrow(cols, "cols"), dy.const_data_ptr(), row_stride(dy),
+      want_w ? s->const_data_ptr() : nullptr, want_w ? row_stride(*s) : 0, narrow(n, "rows"),
+      ints(rows), ints(source), weights ? weights->const_data_ptr() : nullptr, wt,
+      want_s ? ds.data_ptr() : nullptr, cols, want_w ? dw.data_ptr() : nullptr, on.raw());
+  return done(rc, py::make_tuple(want_s ? py::cast(ds) : py::none(),
+                                 want_w ? py::cast(dw) : py::none()));
+}
+
+void add_f8_calls(py::module_& m) {
+  m.def("quantize", [](int64_t plan, int device, const Tensor& x, int blocks, int format,
+                       const c10::optional<Tensor>& source, int64_t choices,
+                       const c10::optional<int64_t>& stream) {
+    return quantize(plan, device, x, blocks,
+                    format == GEMM_F8_E5M2 ? at::kFloat8_e5m2 : at::kFloat8_e4m3fn, source, choices,
+                    stream);
+  });
+  m.def("matmul_f8", [](int64_t plan, int device, const Tensor& a, const Tensor& sa, const Tensor& b,
+                        const Tensor& sb, const c10::optional<Tensor>& out, int type,
+                        const c10::optional<Tensor>& starts, bool accumulate,
+                        const c10::optional<int64_t>& stream) {
+    return matmul_f8(plan, device, a, sa, b, sb, out,
+                     type == GEMM_F8_F16 ? at::kHalf : type == GEMM_F8_BF16 ? at::kBFloat16 : at::kFloat,
+                     starts, accumulate, stream);
+  });
+  m.def("expert_maps", &expert_maps);
+  m.def("expert_gather", &expert_gather);
+  m.def("expert_combine", &expert_combine);
+  m.def("expert_combine_gradient", &expert_combine_gradient);
+}
+
+}  // namespace
