@@ -384,7 +384,7 @@ __device__ __forceinline__ void promote_role(const Params& p, const Segments& s,
         } else {
           ptx::tc_fence_before();
           __syncwarp();
-          if (lane == 0) ptx::mbar_arrive_cluster(leader_tempty + 8 * half);
+          if (lane == 0) ptx::mbar_arrive_cluster_relaxed(leader_tempty + 8 * half);
         }
         const uint32_t(&x)[16] = r[c & 1];
         if constexpr (COLS) {

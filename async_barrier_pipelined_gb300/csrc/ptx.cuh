@@ -446,6 +446,15 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t bar, uint16_t cta_mask)
       : "memory");
 }
 
+// The same without the release: for arrivals that publish no generic memory
+// (a tcgen05.ld that tcgen05.wait::ld has seen complete has its values in
+// registers).  With the release each one waits for the thread's loads and
+// stores in flight.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
+               : "memory");
+}
+
 // D (+)= A * B for 8-bit floating-point operands (kind::f8f6f4: 32 K elements a
 // step, FP32 accumulation), one CTA and a CTA pair.
 __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
