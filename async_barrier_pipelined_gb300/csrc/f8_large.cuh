@@ -362,56 +362,61 @@ __device__ __forceinline__ void promote_role(const Params& p, const Segments& s,
         pb += p.sb_inner;
         column_scales(nb);
       }
-      const bool got = wait_phase_inline(b.tfull + 8 * half, (done >> 1) & 1u, p, abort_flag);
-      if (!__all_sync(0xffffffffu, got)) return;
-      ptx::tc_fence_after();
-      const uint32_t t = t_row + half * PN;
-      const uint64_t sa2 = ptx::pack_f2(sa, sa);
-      uint32_t r[2][16];
-      ptx::tmem_ld_32x32b_x16(t, r[0]);
       // sa * sb is one number, unless it leaves FP32's normal range where the
       // product with the block's sum may not: then one after the other.
       const float sab = sa * sb;
       const bool split = !COLS && __any_sync(0xffffffffu, !(fabsf(sab) >= 1.17549435e-38f &&
                                                              fabsf(sab) <= 3.4e38f));
-      const uint64_t s1 = ptx::pack_f2(sab, sab), sb2 = ptx::pack_f2(sb, sb);
+      const uint64_t s1 = ptx::pack_f2(sab, sab), sb2 = ptx::pack_f2(sb, sb),
+                     sa2 = ptx::pack_f2(sa, sa);
+      const bool got = wait_phase_inline(b.tfull + 8 * half, (done >> 1) & 1u, p, abort_flag);
+      if (!__all_sync(0xffffffffu, got)) return;
+      ptx::tc_fence_after();
+      const uint32_t t = t_row + half * PN;
+      // Two loads of 32 columns on their way at a time: a load's latency is
+      // waited for twice a block.
+      uint32_t r[2][32];
+      ptx::tmem_ld_32x32b_x32(t, r[0]);
+      ptx::tmem_ld_32x32b_x32(t + 32u, r[1]);
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        ptx::tmem_ld_wait();
-        ptx::reg_fence(r[c & 1]);
-        if (c < 7) {
-          ptx::tmem_ld_32x32b_x16(t + 16u * (c + 1), r[(c + 1) & 1]);
-        } else {
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive_cluster_relaxed(leader_tempty + 8 * half);
+      for (int c = 0; c < 4; ++c) {
+        if ((c & 1) == 0) {
+          ptx::tmem_ld_wait();
+          ptx::reg_fence(r[0]);
+          ptx::reg_fence(r[1]);
+          if (c == 2) {
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive_cluster_relaxed(leader_tempty + 8 * half);
+          }
         }
-        const uint32_t(&x)[16] = r[c & 1];
+        const uint32_t(&x)[32] = r[c & 1];
         if constexpr (COLS) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint4 q = ld_shared_v4(sbuf + (16u * c + 4u * j) * 4u);
+          for (int j = 0; j < 8; ++j) {
+            const uint4 q = ld_shared_v4(sbuf + (32u * c + 4u * j) * 4u);
             const uint64_t q0 = ptx::pack_f2(__uint_as_float(q.x), __uint_as_float(q.y));
             const uint64_t q1 = ptx::pack_f2(__uint_as_float(q.z), __uint_as_float(q.w));
             const uint64_t x0 = ptx::pack_f2(__uint_as_float(x[4 * j]), __uint_as_float(x[4 * j + 1]));
             const uint64_t x1 = ptx::pack_f2(__uint_as_float(x[4 * j + 2]), __uint_as_float(x[4 * j + 3]));
-            acc[8 * c + 2 * j] = ptx::fma_f2(ptx::mul_f2(x0, q0), sa2, acc[8 * c + 2 * j]);
-            acc[8 * c + 2 * j + 1] = ptx::fma_f2(ptx::mul_f2(x1, q1), sa2, acc[8 * c + 2 * j + 1]);
-            asm volatile("" : "+l"(acc[8 * c + 2 * j]), "+l"(acc[8 * c + 2 * j + 1]));
+            acc[16 * c + 2 * j] = ptx::fma_f2(ptx::mul_f2(x0, q0), sa2, acc[16 * c + 2 * j]);
+            acc[16 * c + 2 * j + 1] = ptx::fma_f2(ptx::mul_f2(x1, q1), sa2, acc[16 * c + 2 * j + 1]);
+            asm volatile("" : "+l"(acc[16 * c + 2 * j]), "+l"(acc[16 * c + 2 * j + 1]));
           }
         } else if (!split) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            acc[8 * c + j] = ptx::fma_f2(
+          for (int j = 0; j < 16; ++j)
+            acc[16 * c + j] = ptx::fma_f2(
                 ptx::pack_f2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), s1,
-                acc[8 * c + j]);
+                acc[16 * c + j]);
         } else {
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            acc[8 * c + j] = ptx::fma_f2(
+          for (int j = 0; j < 16; ++j)
+            acc[16 * c + j] = ptx::fma_f2(
                 ptx::mul_f2(ptx::pack_f2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])),
-                            sb2), sa2, acc[8 * c + j]);
+                            sb2), sa2, acc[16 * c + j]);
         }
+        if (c < 2) ptx::tmem_ld_32x32b_x32(t + 64u + 32u * c, r[c]);
       }
     }
     if (row0 >= g.m_end && g.tail < 0) continue;
