@@ -57,7 +57,7 @@ struct Params {
   int tiles_m, tiles_n;      // DENSE: tiles of M; always: tiles of N
   int kblocks;               // DENSE
   int units;                 // DENSE, BY_INNER; BY_ROWS knows them on the device
-  int full_units, parts;     // large kernel, DENSE: see there
+  int full_units, cut_units, parts;   // large kernel, DENSE: see there
   float* ws;
   unsigned* counters;
   int* status;
@@ -222,6 +222,17 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
                : "r"(addr)
                : "memory");
   return v;
+}
+__device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_shared_b32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void st_shared_b64(uint32_t addr, uint64_t v) {
+  asm volatile("st.shared.b64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
 }
 __device__ __forceinline__ void st_shared_f32(uint32_t addr, float v) {
   asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");

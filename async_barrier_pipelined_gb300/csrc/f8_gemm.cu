@@ -334,6 +334,7 @@ int gemm_f8_run(gemm_f16_plan_t p, int form, int M, int N, int K, int experts,
   prm.full_units = (int)tiles - c.tail_tiles;
   prm.units = form == GEMM_F8_BY_INNER ? (int)tiles * experts
                                        : prm.full_units + c.tail_tiles * c.parts;
+  prm.cut_units = c.tail_tiles * c.parts;
   if (need > 0) {
     prm.counters = static_cast<unsigned*>(workspace);
     prm.ws = reinterpret_cast<float*>(static_cast<char*>(workspace) + counter_bytes(c));

@@ -6,27 +6,33 @@
 // 256 x 256 x 32 MMAs per K block, and each block's products go to one half of
 // tensor memory (256 of 512 columns) while eight promotion warps per CTA take
 // the block before out of the other half and add it, scaled, to FP32
-// registers: a thread holds one row and 128 columns.
+// registers: 128 sums a thread.
 //
 // What bounds it: an SM's tensor core takes 512 cycles for a K block (128 x
 // 256 x 128 products at 8192 a cycle), its four FP32 pipes 256 for one fused
 // multiply-add per product (scales per tile of B: sa * sb is one number for a
 // thread's 128 columns) or 512 for two operations (a scale per column of B).
-// So the accumulation hides behind the tensor core, just so in the second
-// case.
+// Measured at 4864 x 4096 x 8192: 405 ns a block with a scale per tile (2.8
+// PFLOP/s), 650 with one per column (1.8), 350 for the copies and the tensor
+// core alone.  MMAs of 128 columns, which would give tensor memory four slots
+// and the promotion warps more time for each, took 600.
 //
-// DENSE: pairs walk the tiles in bands of eight tile rows.  A last wave of
-// `rem` tiles with rem <= pairs / 2 is cut into `parts` ranges of K blocks, so
-// that no pair idles: each writes FP32 sums to the workspace, and whichever warp finds itself the last of
-// its rows and columns (a counter, one for each warp's piece of a tile) adds
-// the parts in their order and stores C.  BY_ROWS: tiles of 256 rows within
-// an expert's segment, those of one column of tiles side by side.  BY_INNER:
-// all tiles of each expert, with that expert's K blocks.
+// DENSE: pairs walk the tiles in bands of eight tile rows.  The `rem` tiles of
+// an incomplete wave, at most half as many as pairs, are cut into `parts`
+// ranges of K blocks, so that no pair idles.  These come first: the pairs that
+// had one are then out of step with the others, and the tiles' stores of some
+// run beside the products of the others.  Each writes FP32 sums to the workspace,
+// and whichever warp finds itself the last of its rows and columns (a counter,
+// one for each warp's piece of a tile) adds the parts in their order and stores
+// C.  BY_ROWS: tiles of 256 rows within an expert's segment, those of one column
+// of tiles side by side.  BY_INNER: all tiles of each expert, with that expert's
+// K blocks.
 //
 // Barriers (as in gemm_pair.cuh): full[s] leader only, 1 arrival and both
 // CTAs' bytes; empty[s] both CTAs, multicast commit; tfull[a] both CTAs,
 // multicast commit after a K block; tempty[a] leader only, 16 arrivals (8
-// promotion warps per CTA); mma_done leader only.  Waits are bounded; after an
+// promotion warps per CTA); sfull[s], sempty[s] each CTA (COLS), 64 copying
+// threads and 8 promotion warps; mma_done leader only.  Waits are bounded; after an
 // abort the leader completes the phases of copies that were issued.
 #pragma once
 
@@ -47,20 +53,26 @@ constexpr uint32_t B_STAGE = (PN / 2) * BLOCK;
 constexpr uint32_t CTA_STAGE_TX = A_STAGE + B_STAGE;
 constexpr uint32_t EPI_BUF = 32 * 128;        // 32 rows of 128 bytes
 constexpr uint32_t TMEM_COLS = 512;
+// Ring of scales (COLS): those of the CTA's 128 rows, then of the tile's 256
+// columns, four K blocks at a time; eight words between the blocks' banks, so
+// that the copies of a warp, eight rows by four blocks, do not collide.
+constexpr int CHUNK = 4, CHUNKS = 3;
+constexpr uint32_t SCALE_BLOCK = (CM + PN + 8) * 4, SCALE_CHUNK = CHUNK * SCALE_BLOCK;
+constexpr int SCALE_WARP0 = 2, SCALE_THREADS = 64;
 
 constexpr uint32_t OFF_A = 0;
 constexpr uint32_t OFF_B = OFF_A + STAGES * A_STAGE;
 constexpr uint32_t OFF_EPI = OFF_B + STAGES * B_STAGE;
-constexpr uint32_t OFF_SB = OFF_EPI + PROMOTE_WARPS * EPI_BUF;     // a warp's column scales, twice
-constexpr uint32_t OFF_SEG = OFF_SB + PROMOTE_WARPS * 2 * 128 * 4;
+constexpr uint32_t OFF_SCALE = OFF_EPI + PROMOTE_WARPS * EPI_BUF;
+constexpr uint32_t OFF_SEG = OFF_SCALE + CHUNKS * SCALE_CHUNK;
 constexpr uint32_t OFF_BAR = OFF_SEG + SEGMENT_BYTES;
-constexpr uint32_t NUM_BARS = 2 * STAGES + 2 + 2 + 1;
+constexpr uint32_t NUM_BARS = 2 * STAGES + 2 * CHUNKS + 2 + 2 + 1;
 constexpr uint32_t OFF_TMEM_SLOT = OFF_BAR + NUM_BARS * 8;
 constexpr uint32_t OFF_ABORT = OFF_TMEM_SLOT + 4;
 constexpr uint32_t OFF_PEER_ISSUED = OFF_ABORT + 4;
 constexpr uint32_t SMEM_BYTES = OFF_PEER_ISSUED + 4 + 1024;
 static_assert(SMEM_BYTES <= 232448, "over the 227 KB shared-memory limit per CTA");
-static_assert(OFF_BAR % 8 == 0 && OFF_EPI % 128 == 0 && OFF_SB % 16 == 0, "alignment");
+static_assert(OFF_BAR % 8 == 0 && OFF_EPI % 128 == 0 && OFF_SCALE % 16 == 0, "alignment");
 
 // Registers: 384 threads launch with 168 each (64,512); the four other warps
 // give up 112 each and the promotion warps take 56 more (128 * 56 + 256 * 224).
@@ -72,7 +84,7 @@ constexpr int PART_FLOATS = PM * PN;
 constexpr int TILE_COUNTERS = 2 * PROMOTE_WARPS;
 
 struct Bars {
-  uint32_t full, empty, tfull, tempty, mma_done;
+  uint32_t full, empty, tfull, tempty, sfull, sempty, mma_done;
 };
 
 struct Unit {
@@ -124,11 +136,10 @@ __device__ __forceinline__ Unit unit_at(const Params& p, const Segments& s, int 
     g.nkb = (s.len[g.expert] + BLOCK - 1) / BLOCK;
     band_tile(u - g.expert * per, p.tiles_m, p.tiles_n, &tm, &tn);
   } else {
-    int t = u;
-    if (u >= p.full_units) {
-      const int v = u - p.full_units;
-      g.tail = v / p.parts;
-      g.part = v - g.tail * p.parts;
+    int t = u - p.cut_units;
+    if (t < 0) {
+      g.tail = u / p.parts;
+      g.part = u - g.tail * p.parts;
       int end;
       split_range(p.kblocks, p.parts, g.part, &g.blk0, &end);
       g.nkb = end - g.blk0;
@@ -210,40 +221,61 @@ __device__ __forceinline__ void mma_role(const Params& p, const Segments& s, uin
   wait_drain(b.mma_done, 0, p.timeout_ns);
 }
 
-// A warp's 32 rows x 128 columns (acc: this lane's row) to C through a staging
+// A warp's 32 rows x 128 columns (acc: as in promote_role) to C through a staging
 // buffer of 32 rows x 128 bytes, so that a store instruction writes four whole
 // lines of 128 bytes and not 16 bytes of each of 32 rows.
-template <typename T>
+template <typename T, bool COLS>
 __device__ __forceinline__ void store_rows(const Params& p, T* C, const uint64_t (&acc)[64],
                                            uint32_t stage, int row0, int row_end, int col0,
                                            uint32_t lane) {
   constexpr int V = 16 / sizeof(T);        // numbers of a 16-byte unit
-  constexpr int COLS = 128 / sizeof(T);    // columns of a staging buffer
+  constexpr int WIDE = 128 / sizeof(T);    // columns of a staging buffer
+  constexpr int COLS_N = WIDE / 8;
 #pragma unroll
-  for (int c = 0; c < 128 / COLS; ++c) {
-    if (col0 + c * COLS >= p.N) break;
+  for (int c = 0; c < 128 / WIDE; ++c) {
+    if (col0 + c * WIDE >= p.N) break;
+    if constexpr (COLS) {
 #pragma unroll
-    for (uint32_t j = 0; j < 8; ++j) {
-      float v[V];
+      for (int n = 0; n < COLS_N; ++n) {
 #pragma unroll
-      for (int i = 0; i < V / 2; ++i)
-        ptx::unpack_f2(acc[(c * COLS + (int)j * V) / 2 + i], v[2 * i], v[2 * i + 1]);
-      uint32_t w[4];
-      if constexpr (sizeof(T) == 4) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(v[i]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = pack2<T>(v[2 * i], v[2 * i + 1]);
+        for (uint32_t q = 0; q < 4; ++q) {
+          const uint32_t row = (lane >> 2) + 8 * q, col = 8 * n + 2 * (lane & 3u);
+          const uint32_t byte = col * sizeof(T);
+          const uint32_t at = stage + row * 128u + (((byte >> 4) ^ (row & 7u)) << 4) + (byte & 15u);
+          const uint64_t v = acc[(c * COLS_N + n) * 4 + q];
+          if constexpr (sizeof(T) == 4) {
+            st_shared_b64(at, v);
+          } else {
+            float lo, hi;
+            ptx::unpack_f2(v, lo, hi);
+            st_shared_b32(at, pack2<T>(lo, hi));
+          }
+        }
       }
-      ptx::st_shared_v4(stage + lane * 128u + ((j ^ (lane & 7u)) << 4), w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+      for (uint32_t j = 0; j < 8; ++j) {
+        float v[V];
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i)
+          ptx::unpack_f2(acc[(c * WIDE + (int)j * V) / 2 + i], v[2 * i], v[2 * i + 1]);
+        uint32_t w[4];
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(v[i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = pack2<T>(v[2 * i], v[2 * i + 1]);
+        }
+        ptx::st_shared_v4(stage + lane * 128u + ((j ^ (lane & 7u)) << 4), w[0], w[1], w[2], w[3]);
+      }
     }
     __syncwarp();
 #pragma unroll
     for (uint32_t i = 0; i < 8; ++i) {
       const uint32_t r = i * 4 + (lane >> 3), j = lane & 7u;
       uint4 v = ld_shared_v4(stage + r * 128u + ((j ^ (r & 7u)) << 4));
-      const int row = row0 + (int)r, col = col0 + c * COLS + (int)j * V;
+      const int row = row0 + (int)r, col = col0 + c * WIDE + (int)j * V;
       if (row >= row_end || col >= p.N) continue;
       T* at = C + (int64_t)row * p.ldc + col;
       if (p.vec && col + V <= p.N) {
@@ -307,7 +339,93 @@ __device__ __forceinline__ bool join_parts(const Params& p, const Unit& g, uint3
   return true;
 }
 
+// Columns of B lie in the ring in the order in which the promotion warps' lanes
+// hold them (see promote_role).
+__device__ __forceinline__ uint32_t column_at(uint32_t j) {
+  return (j & ~15u) | ((j & 6u) << 1) | ((j & 8u) >> 2) | (j & 1u);
+}
+
+// `blocks` blocks' scales of OUTER rows (columns) of which `real` exist, by 64
+// threads: four blocks of a row side by side where the inner dimension is
+// contiguous, else rows side by side, so that a warp's copies share their
+// sectors.  Those past `real` belong to results that are not stored.
+template <int OUTER>
+__device__ __forceinline__ void copy_scales(uint32_t dst, const float* src, int64_t s_outer,
+                                            int64_t s_inner, int real, int blocks, uint32_t t) {
+  if (s_inner == 1) {
+    const uint32_t k = t % CHUNK, o = t / CHUNK;
+    constexpr int STEP = SCALE_THREADS / CHUNK;
+    if ((int)k >= blocks) return;
+    dst += k * SCALE_BLOCK + (OUTER == PN ? column_at(o) : o) * 4u;
+    src += k + o * s_outer;
+#pragma unroll 8
+    for (int i = 0; i < OUTER / STEP; ++i) {
+      if ((int)o + i * STEP < real) ptx::cp_async_4(dst + i * STEP * 4u, src);
+      src += STEP * s_outer;
+    }
+  } else {
+    dst += (OUTER == PN ? column_at(t) : t) * 4u;
+    src += t * s_outer;
+#pragma unroll
+    for (int i = 0; i < OUTER / SCALE_THREADS; ++i) {
+      if ((int)t + i * SCALE_THREADS >= real) return;
+      const float* at = src;
+#pragma unroll
+      for (int k = 0; k < CHUNK; ++k) {
+        if (k < blocks) ptx::cp_async_4(dst + k * SCALE_BLOCK + i * SCALE_THREADS * 4u, at);
+        at += s_inner;
+      }
+      src += SCALE_THREADS * s_outer;
+    }
+  }
+}
+
+// The scales of each K block into the ring, by asynchronous copies: the
+// promotion warps read them blocks later, when they have long arrived.  (Loaded
+// by those warps one block ahead, column scales were waited for: 890 ns a block
+// where they lie side by side, 1,530 where they do not, and 587 without them.)
+__device__ __forceinline__ void scale_role(const Params& p, const Segments& s, uint32_t base,
+                                           uint32_t rank, int pair, int npairs, const Bars& b,
+                                           uint32_t t, volatile int* abort_flag) {
+  RingPos pos{0, 0};
+  const int units = total_units(p, s);
+  bool ok = true;
+  for (int u = pair; u < units && ok; u += npairs) {
+    const Unit g = unit_at(p, s, u);
+    const int m0 = g.m0 + (int)rank * CM;
+    const float* pa = p.sa + (p.sa_shift ? 0 : m0 * p.sa_outer) + g.blk0 * p.sa_inner;
+    const float* pb = p.sb + g.n0 * p.sb_outer + g.blk0 * p.sb_inner +
+                      (p.form == GEMM_F8_BY_ROWS ? g.expert * p.sb_batch : 0);
+    for (int k = 0; k < g.nkb; k += CHUNK) {
+      const uint32_t dst = base + OFF_SCALE + pos.stage * SCALE_CHUNK;
+      if (!wait_phase(b.sempty + 8 * pos.stage, producer_wait_parity(pos), p, abort_flag)) {
+        ok = false;
+        break;
+      }
+      const int blocks = min(CHUNK, g.nkb - k);
+      copy_scales<PN>(dst + CM * 4u, pb, p.sb_outer, p.sb_inner, p.N - g.n0, blocks, t);
+      if (p.sa_shift == 0) {
+        copy_scales<CM>(dst, pa, p.sa_outer, p.sa_inner, g.m_end - m0, blocks, t);
+      } else {     // a scale for 128 rows of A
+        for (int i = (int)t; i < CM; i += SCALE_THREADS)
+          for (int j = 0; j < blocks && m0 + i < g.m_end; ++j)
+            ptx::cp_async_4(dst + j * SCALE_BLOCK + i * 4u,
+                            pa + ((m0 + i) >> p.sa_shift) * p.sa_outer + j * p.sa_inner);
+      }
+      ptx::cp_async_arrive(b.sfull + 8 * pos.stage);
+      ring_advance(pos, CHUNKS);
+      pa += CHUNK * p.sa_inner;
+      pb += CHUNK * p.sb_inner;
+    }
+  }
+  ptx::cp_async_wait_all();   // nothing in flight when the CTA exits
+}
+
 // COLS: B has a scale for each column (else one for a thread's 128 columns).
+// Without, a lane holds one row and 128 columns; with, four rows (lane / 4 and
+// every eighth after it) and 32 columns (2 (lane % 4) and the next, of every
+// eight), so that it reads 32 column scales a block from shared memory, not
+// 128, which the tensor core's operands and their copies need.
 template <bool COLS>
 __device__ __forceinline__ void promote_role(const Params& p, const Segments& s, uint32_t base,
                                              uint32_t tmem_base, uint32_t rank, int pair,
@@ -315,120 +433,170 @@ __device__ __forceinline__ void promote_role(const Params& p, const Segments& s,
                                              uint32_t lane, volatile int* abort_flag) {
   const uint32_t w = warp - PROMOTE_WARP0, quarter = warp & 3u, right = w >> 2;
   const uint32_t stage = base + OFF_EPI + w * EPI_BUF;
-  const uint32_t sb_buf = base + OFF_SB + w * 2 * 128 * 4;
+  const uint32_t row_scale = base + OFF_SCALE + (quarter * 32u + (lane >> 2)) * 4u;
+  const uint32_t col_scale = base + OFF_SCALE + (CM + right * 128u + (lane & 3u) * 4u) * 4u;
   const uint32_t t_row = tmem_base + ((quarter * 32u) << 16) + right * 128u;
   const uint32_t leader_tempty = ptx::map_to_cta(b.tempty, 0);
-  uint32_t done = 0;
+  uint32_t done = 0;    // K blocks so far: block i uses half i & 1
+  RingPos pos{0, 0};    // chunk of scales
   const int units = total_units(p, s);
-  for (int u = pair; u < units; u += npairs) {
+  // A unit's K blocks and, without COLS, its first scales.
+  int nkb = 0;
+  const float *pa = nullptr, *pb = nullptr;
+  float na = 0.f, nb = 0.f;
+  const auto begin = [&](int u) {
     const Unit g = unit_at(p, s, u);
-    const int row0 = g.m0 + (int)(rank * CM + quarter * 32);
-    const int col0 = g.n0 + (int)right * 128;
-    const int row = min(row0 + (int)lane, g.m_end - 1);
-    const float* pa = p.sa + (int64_t)(row >> p.sa_shift) * p.sa_outer + (int64_t)g.blk0 * p.sa_inner;
-    const float* pb = p.sb + (int64_t)g.blk0 * p.sb_inner +
-                      (p.form == GEMM_F8_BY_ROWS ? g.expert * p.sb_batch : 0);
-    if constexpr (!COLS) pb += (int64_t)(min(col0, p.N - 1) >> 7) * p.sb_outer;
-    // This lane's column scales of a K block (COLS), or the one of all columns.
-    const auto column_scales = [&](float(&v)[COLS ? 4 : 1]) {
-      if constexpr (COLS) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          v[i] = __ldg(pb + (int64_t)min(col0 + (int)lane + 32 * i, p.N - 1) * p.sb_outer);
-      } else {
-        v[0] = __ldg(pb);
-      }
-    };
+    nkb = g.nkb;
+    if (COLS || nkb == 0) return;
+    const int row = min(g.m0 + (int)(rank * CM + quarter * 32 + lane), g.m_end - 1);
+    const int col = min(g.n0 + (int)right * 128, p.N - 1);
+    pa = p.sa + (int64_t)(row >> p.sa_shift) * p.sa_outer + (int64_t)g.blk0 * p.sa_inner;
+    pb = p.sb + (int64_t)(col >> 7) * p.sb_outer + (int64_t)g.blk0 * p.sb_inner +
+         (p.form == GEMM_F8_BY_ROWS ? g.expert * p.sb_batch : 0);
+    na = __ldg(pa);
+    nb = __ldg(pb);
+  };
+  if (pair < units) begin(pair);
+  for (int u = pair; u < units; u += npairs) {
     uint64_t acc[64];
 #pragma unroll
     for (int i = 0; i < 64; ++i) acc[i] = 0;
-    float na = 0.f, nb[COLS ? 4 : 1];
-    if (g.nkb > 0) {
-      na = __ldg(pa);
-      column_scales(nb);
-    }
-    for (int i = 0; i < g.nkb; ++i, ++done) {
+    for (int i = 0; i < nkb; ++i, ++done) {
       const uint32_t half = done & 1u;
-      const float sa = na;
-      float sb = nb[0];
-      const uint32_t sbuf = sb_buf + half * 512u;
+      const float sa = na, sb = nb;
+      bool got = true;
       if constexpr (COLS) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) st_shared_f32(sbuf + (lane + 32u * c) * 4u, nb[c]);
-      }
-      if (i + 1 < g.nkb) {     // the next block's scales, on their way during this one
+        if (i % CHUNK == 0)
+          got = wait_phase_inline(b.sfull + 8 * pos.stage, consumer_wait_parity(pos), p, abort_flag);
+      } else if (i + 1 < nkb) {     // the next block's scales, on their way during this one
         pa += p.sa_inner;
         na = __ldg(pa);
         pb += p.sb_inner;
-        column_scales(nb);
+        nb = __ldg(pb);
       }
-      // sa * sb is one number, unless it leaves FP32's normal range where the
-      // product with the block's sum may not: then one after the other.
-      const float sab = sa * sb;
-      const bool split = !COLS && __any_sync(0xffffffffu, !(fabsf(sab) >= 1.17549435e-38f &&
-                                                             fabsf(sab) <= 3.4e38f));
-      const uint64_t s1 = ptx::pack_f2(sab, sab), sb2 = ptx::pack_f2(sb, sb),
-                     sa2 = ptx::pack_f2(sa, sa);
-      const bool got = wait_phase_inline(b.tfull + 8 * half, (done >> 1) & 1u, p, abort_flag);
+      got = wait_phase_inline(b.tfull + 8 * half, (done >> 1) & 1u, p, abort_flag) && got;
       if (!__all_sync(0xffffffffu, got)) return;
       ptx::tc_fence_after();
       const uint32_t t = t_row + half * PN;
-      // Two loads of 32 columns on their way at a time: a load's latency is
+      // Loads of 2 x 32 columns on their way at a time: a load's latency is
       // waited for twice a block.
-      uint32_t r[2][32];
-      ptx::tmem_ld_32x32b_x32(t, r[0]);
-      ptx::tmem_ld_32x32b_x32(t + 32u, r[1]);
+      const auto release = [&]() {
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive_cluster_relaxed(leader_tempty + 8 * half);
+      };
+      if constexpr (COLS) {
+        const uint32_t in_ring = pos.stage * SCALE_CHUNK + (i % CHUNK) * SCALE_BLOCK;
+        const uint32_t cols = col_scale + in_ring;
+        uint32_t lo[2][16], hi[2][16];     // rows 0-15 and 16-31
+        const auto load = [&](int c) {
+          ptx::tmem_ld_16x256b_x4(t + 32u * c, lo[c & 1]);
+          ptx::tmem_ld_16x256b_x4(t + 32u * c + (16u << 16), hi[c & 1]);
+        };
+        load(0);
+        load(1);
+        uint4 ahead = ld_shared_v4(cols);     // each group's scales one group ahead
+        uint64_t s4[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        if ((c & 1) == 0) {
-          ptx::tmem_ld_wait();
-          ptx::reg_fence(r[0]);
-          ptx::reg_fence(r[1]);
-          if (c == 2) {
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive_cluster_relaxed(leader_tempty + 8 * half);
-          }
+        for (uint32_t q = 0; q < 4; ++q) {
+          const float v = ld_shared_f32(row_scale + in_ring + 32u * q);
+          s4[q] = ptx::pack_f2(v, v);
         }
-        const uint32_t(&x)[32] = r[c & 1];
-        if constexpr (COLS) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const uint4 q = ld_shared_v4(sbuf + (32u * c + 4u * j) * 4u);
-            const uint64_t q0 = ptx::pack_f2(__uint_as_float(q.x), __uint_as_float(q.y));
-            const uint64_t q1 = ptx::pack_f2(__uint_as_float(q.z), __uint_as_float(q.w));
-            const uint64_t x0 = ptx::pack_f2(__uint_as_float(x[4 * j]), __uint_as_float(x[4 * j + 1]));
-            const uint64_t x1 = ptx::pack_f2(__uint_as_float(x[4 * j + 2]), __uint_as_float(x[4 * j + 3]));
-            acc[16 * c + 2 * j] = ptx::fma_f2(ptx::mul_f2(x0, q0), sa2, acc[16 * c + 2 * j]);
-            acc[16 * c + 2 * j + 1] = ptx::fma_f2(ptx::mul_f2(x1, q1), sa2, acc[16 * c + 2 * j + 1]);
-            asm volatile("" : "+l"(acc[16 * c + 2 * j]), "+l"(acc[16 * c + 2 * j + 1]));
+        for (int c = 0; c < 4; ++c) {
+          if ((c & 1) == 0) {
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              ptx::reg_fence(lo[k]);
+              ptx::reg_fence(hi[k]);
+            }
+            if (c == 2) release();
           }
-        } else if (!split) {
+          const uint32_t(&xl)[16] = lo[c & 1], (&xh)[16] = hi[c & 1];
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            acc[16 * c + j] = ptx::fma_f2(
-                ptx::pack_f2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), s1,
-                acc[16 * c + j]);
-        } else {
+          for (int m = 0; m < 2; ++m) {     // two groups of eight columns
+            const uint4 w4 = ahead;
+            if (2 * c + m < 7) ahead = ld_shared_v4(cols + (2 * c + m + 1) * 64u);
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            acc[16 * c + j] = ptx::fma_f2(
-                ptx::mul_f2(ptx::pack_f2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])),
-                            sb2), sa2, acc[16 * c + j]);
+            for (int n = 0; n < 2; ++n) {
+              const uint64_t q = n ? ptx::pack_f2(__uint_as_float(w4.z), __uint_as_float(w4.w))
+                                   : ptx::pack_f2(__uint_as_float(w4.x), __uint_as_float(w4.y));
+              uint64_t* a = acc + 16 * c + (2 * m + n) * 4;
+              const int j = (2 * m + n) * 4;
+              const auto add = [&](uint64_t& sum, uint32_t x0, uint32_t x1, uint64_t row) {
+                const uint64_t x = ptx::pack_f2(__uint_as_float(x0), __uint_as_float(x1));
+                sum = ptx::fma_f2(ptx::mul_f2(x, q), row, sum);
+              };
+              add(a[0], xl[j], xl[j + 1], s4[0]);
+              add(a[1], xl[j + 2], xl[j + 3], s4[1]);
+              add(a[2], xh[j], xh[j + 1], s4[2]);
+              add(a[3], xh[j + 2], xh[j + 3], s4[3]);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) asm volatile("" : "+l"(a[k]));
+            }
+          }
+          if (c < 2) load(c + 2);
         }
-        if (c < 2) ptx::tmem_ld_32x32b_x32(t + 64u + 32u * c, r[c]);
+        if (i % CHUNK == CHUNK - 1 || i == nkb - 1) {
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(b.sempty + 8 * pos.stage);
+          ring_advance(pos, CHUNKS);
+        }
+      } else {
+        // sa * sb is one number, unless it leaves FP32's normal range where the
+        // product with the block's sum may not: then one after the other.
+        const float sab = sa * sb;
+        const bool split = __any_sync(0xffffffffu, !(fabsf(sab) >= 1.17549435e-38f &&
+                                                      fabsf(sab) <= 3.4e38f));
+        const uint64_t s1 = ptx::pack_f2(sab, sab);
+        uint32_t r[2][32];
+        ptx::tmem_ld_32x32b_x32(t, r[0]);
+        ptx::tmem_ld_32x32b_x32(t + 32u, r[1]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if ((c & 1) == 0) {
+            ptx::tmem_ld_wait();
+            ptx::reg_fence(r[0]);
+            ptx::reg_fence(r[1]);
+            if (c == 2) release();
+          }
+          const uint32_t(&x)[32] = r[c & 1];
+          if (!split) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              acc[16 * c + j] = ptx::fma_f2(
+                  ptx::pack_f2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), s1,
+                  acc[16 * c + j]);
+          } else {
+            const uint64_t sa2 = ptx::pack_f2(sa, sa), sb2 = ptx::pack_f2(sb, sb);
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              acc[16 * c + j] = ptx::fma_f2(
+                  ptx::mul_f2(
+                      ptx::pack_f2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), sb2),
+                  sa2, acc[16 * c + j]);
+          }
+          if (c < 2) ptx::tmem_ld_32x32b_x32(t + 64u + 32u * c, r[c]);
+        }
       }
     }
+    // The unit again, so that the loop's registers are the sums' alone.
+    int same = u;
+    asm volatile("" : "+r"(same));
+    const Unit g = unit_at(p, s, same);
+    if (u + npairs < units) begin(u + npairs);   // on their way during the stores
+    const int row0 = g.m0 + (int)(rank * CM + quarter * 32), col0 = g.n0 + (int)right * 128;
     if (row0 >= g.m_end && g.tail < 0) continue;
     if (g.tail >= 0 && !join_parts(p, g, rank, w, lane, acc)) continue;
     const int64_t off = p.form == GEMM_F8_BY_INNER ? g.expert * p.c_batch : 0;
     if (p.type == GEMM_F8_F16)
-      store_rows<__half>(p, static_cast<__half*>(p.C) + off, acc, stage, row0, g.m_end, col0, lane);
+      store_rows<__half, COLS>(p, static_cast<__half*>(p.C) + off, acc, stage, row0, g.m_end, col0, lane);
     else if (p.type == GEMM_F8_BF16)
-      store_rows<__nv_bfloat16>(p, static_cast<__nv_bfloat16*>(p.C) + off, acc, stage, row0,
+      store_rows<__nv_bfloat16, COLS>(p, static_cast<__nv_bfloat16*>(p.C) + off, acc, stage, row0,
                                 g.m_end, col0, lane);
     else
-      store_rows<float>(p, static_cast<float*>(p.C) + off, acc, stage, row0, g.m_end, col0, lane);
+      store_rows<float, COLS>(p, static_cast<float*>(p.C) + off, acc, stage, row0, g.m_end, col0, lane);
   }
 }
 
@@ -465,7 +633,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
   b.empty = b.full + 8 * STAGES;
   b.tfull = b.empty + 8 * STAGES;
   b.tempty = b.tfull + 16;
-  b.mma_done = b.tempty + 16;
+  b.sfull = b.tempty + 16;
+  b.sempty = b.sfull + 8 * CHUNKS;
+  b.mma_done = b.sempty + 8 * CHUNKS;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_ABORT);
 
   if (warp == 0 && lane == 0) {
@@ -478,6 +648,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     for (int a = 0; a < 2; ++a) {
       ptx::mbar_init(b.tfull + 8 * a, 1);
       ptx::mbar_init(b.tempty + 8 * a, 2 * PROMOTE_WARPS);
+    }
+    for (int s = 0; s < CHUNKS; ++s) {
+      ptx::mbar_init(b.sfull + 8 * s, SCALE_THREADS);
+      ptx::mbar_init(b.sempty + 8 * s, PROMOTE_WARPS);
     }
     ptx::mbar_init(b.mma_done, 1);
     *abort_flag = 0;
@@ -510,6 +684,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       issued = producer_role(&tmA, &tmB, p, seg, base, rank, pair, npairs, b, abort_flag);
     if (warp == 1 && lane == 0 && rank == 0)
       mma_role(p, seg, base, tmem_base, pair, npairs, b, abort_flag);
+    if (COLS && warp >= SCALE_WARP0)
+      scale_role(p, seg, base, rank, pair, npairs, b, (warp - SCALE_WARP0) * 32 + lane,
+                 abort_flag);
     __syncwarp();
   }
 
