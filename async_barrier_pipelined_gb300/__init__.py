@@ -1034,100 +1034,18 @@ def matmul_f8(plan: Plan, A, B, C=None, dtype=None, starts=None, accumulate: boo
         accumulate, stream if stream is None else _stream_handle(stream)), "gemm_f8_run")
 
 
+_no_change = contextlib.nullcontext()
+
+
 def _on_stream(plan: Plan, stream):
     """A context in which ``stream`` (None: no change) is the current one: an
     autograd function's backward pass runs on its forward pass's stream."""
     if stream is None:
-        return contextlib.nullcontext()
+        return _no_change
     import torch
     handle = _stream_handle(stream)
     return torch.cuda.stream(torch.cuda.ExternalStream(handle, device=plan.device) if handle
                              else torch.cuda.default_stream(plan.device))
-
-
-_f8_functions = None
-
-
-def _autograd_f8():
-    """The autograd functions (made on first use: torch is not loaded with this
-    module)."""
-    global _f8_functions
-    if _f8_functions is not None:
-        return _f8_functions
-    import torch
-    from torch.autograd.function import once_differentiable
-
-    class Linear(torch.autograd.Function):
-        @staticmethod
-        def forward(ctx, X, W, codes, scales, starts, plan, formats, training):
-            want_x, want_w = (training and n for n in ctx.needs_input_grad[:2])
-            ctx.call = plan, formats, X.dtype, W.dtype if codes is None else None
-            Q = quantize(plan, W, "tiles", formats[0]) if codes is None else Blocks(codes, scales)
-            if want_w:
-                R, C = quantize(plan, X, "both", formats[0])
-            else:
-                R, C = quantize(plan, X, "rows", formats[0]), (None, None)
-            ctx.save_for_backward(*(C if want_w else (None, None)),
-                                  *(Q if want_x else (None, None)), starts)
-            return matmul_f8(plan, R, Q.t(), dtype=X.dtype, starts=starts)
-
-        @staticmethod
-        @once_differentiable
-        def backward(ctx, dY):
-            xc, xs, wc, ws, starts = ctx.saved_tensors
-            plan, formats, x_type, w_type = ctx.call
-            dY = dY.contiguous()
-            dX = dW = R = C = None
-            if wc is not None and xc is not None:
-                R, C = quantize(plan, dY, "both", formats[1])
-            elif wc is not None:
-                R = quantize(plan, dY, "rows", formats[1])
-            elif xc is not None:
-                C = quantize(plan, dY, "columns", formats[1])
-            if R is not None:
-                dX = matmul_f8(plan, R, Blocks(wc, ws), dtype=x_type, starts=starts)
-            if C is not None:
-                dW = matmul_f8(plan, C.t(), Blocks(xc, xs), dtype=w_type, starts=starts)
-            return dX, dW, None, None, None, None, None, None
-
-    class Gather(torch.autograd.Function):
-        @staticmethod
-        def forward(ctx, X, starts, rows, source, plan):
-            ctx.save_for_backward(starts, rows, source)
-            ctx.plan = plan
-            return _result((_calls or _torch_calls()).expert_gather(
-                plan.handle, plan.device, X, rows, source, None), "experts_gather")
-
-        @staticmethod
-        def backward(ctx, dY):
-            maps = ExpertMaps._make(ctx.saved_tensors)
-            return expert_combine(ctx.plan, dY.contiguous(), maps), None, None, None, None
-
-    class Combine(torch.autograd.Function):
-        @staticmethod
-        def forward(ctx, S, weights, starts, rows, source, plan):
-            ctx.save_for_backward(S if weights is not None and ctx.needs_input_grad[1] else None,
-                                  weights, starts, rows, source)
-            ctx.plan = plan
-            return _result((_calls or _torch_calls()).expert_combine(
-                plan.handle, plan.device, S, rows, source, weights, None), "experts_combine")
-
-        @staticmethod
-        @once_differentiable
-        def backward(ctx, dY):
-            S, weights, starts, rows, source = ctx.saved_tensors
-            plan, dY = ctx.plan, dY.contiguous()
-            if weights is None:
-                return (expert_gather(plan, dY, ExpertMaps(starts, rows, source)), None, None, None,
-                        None, None)
-            want_s, want_w = ctx.needs_input_grad[:2]
-            dS, dw = _result((_calls or _torch_calls()).expert_combine_gradient(
-                plan.handle, plan.device, dY, S, rows, source, weights, want_s, want_w, None),
-                "experts_combine_gradient")
-            return dS, dw, None, None, None, None
-
-    _f8_functions = Linear, Gather, Combine
-    return _f8_functions
 
 
 def linear_f8(plan: Plan, X, W, starts=None, dtype=None, grad_dtype=None, stream=None):
@@ -1144,21 +1062,11 @@ def linear_f8(plan: Plan, X, W, starts=None, dtype=None, grad_dtype=None, stream
     and rows that no expert has are 0, as expert_gather leaves them.  ``plan``
     must last until the backward pass, which runs on the stream of the call.
     """
-    frozen = isinstance(W, Blocks)
-    shape = X.shape
-    if starts is None:
-        X = X.reshape(-1, shape[-1])
-    elif X.dim() != 2:
-        raise ValueError("X must be [rows, K] where starts are given")
-    if (W.data if frozen else W).dim() != (2 if starts is None else 3):
-        raise ValueError("W must be [N, K], or [experts, N, K] with starts")
-    import torch
-    formats = dtype or torch.float8_e4m3fn, grad_dtype or torch.float8_e4m3fn
+    W, codes, scales = (None, *W) if isinstance(W, Blocks) else (W, None, None)
     with _on_stream(plan, stream):
-        Y = _autograd_f8()[0].apply(X, None if frozen else W, W.data if frozen else None,
-                                    W.scales if frozen else None, starts, plan, formats,
-                                    torch.is_grad_enabled())
-        return Y if starts is not None else Y.view(*shape[:-1], Y.shape[-1])
+        return _result((_calls or _torch_calls()).linear_f8(
+            plan, plan.device, X, W, codes, scales, starts, _f8_format(dtype),
+            _f8_format(grad_dtype)), "linear_f8")
 
 
 # ---------------------------------------------------------------- experts
@@ -1187,7 +1095,8 @@ def expert_gather(plan: Plan, X, maps: ExpertMaps, stream=None):
     experts' order: row r is that of the token of maps.source[r], 0 where there
     is none.  Differentiable (the gradient is expert_combine's sum)."""
     with _on_stream(plan, stream):
-        return _autograd_f8()[1].apply(X, *maps, plan)
+        return _result((_calls or _torch_calls()).expert_gather(
+            plan, plan.device, X, maps.rows, maps.source), "experts_gather")
 
 
 def expert_combine(plan: Plan, S, maps: ExpertMaps, weights=None, stream=None):
@@ -1197,4 +1106,5 @@ def expert_combine(plan: Plan, S, maps: ExpertMaps, weights=None, stream=None):
     S's type (None: all 1); choices without a row are left out.  Differentiable
     in S and weights."""
     with _on_stream(plan, stream):
-        return _autograd_f8()[2].apply(S, weights, *maps, plan)
+        return _result((_calls or _torch_calls()).expert_combine(
+            plan, plan.device, S, maps.rows, maps.source, weights), "experts_combine")

@@ -2,14 +2,40 @@
 // C ABI call, in C++ for the same reason as torch_calls.cpp (a generation
 // step makes several of them per layer).  Nothing is computed here.  A bad
 // tensor raises ValueError; a code of the C ABI is returned as a number for
-// the caller to raise.
+// the caller to raise.  The differentiable calls are autograd functions in C++
+// too: in Python a dense layer's step, forward and backward, took 330 us for
+// kernels of 109.
 //
 // Part of torch_calls.cpp (and of its module), after the helpers there.
 #pragma once
 
+#include <torch/csrc/autograd/custom_function.h>
+#include <torch/csrc/autograd/functions/basic_ops.h>
+
 #include "gemm_f8.h"
 
 namespace {
+
+// A code of the C ABI on its way to a binding (raised there) or, from a backward
+// pass, to Python as a RuntimeError.
+struct CallError : std::runtime_error {
+  int code;
+  CallError(int rc, const char* where)
+      : std::runtime_error(std::string(where) + ": " + gemm_f16_strerror(rc)), code(rc) {}
+};
+void check(int rc, const char* where) {
+  if (rc < 0) throw CallError(rc, where);
+}
+
+// A call's result for Python: what `f` returns, or the code of the C ABI.
+template <typename F>
+py::object answer(const F& f) {
+  try {
+    return f();
+  } catch (const CallError& e) {
+    return py::int_(e.code);
+  }
+}
 
 void on_device(const Tensor& x, const char* name, int device) {
   if (!x.is_cuda() || x.get_device() != device)
@@ -35,10 +61,13 @@ int64_t blocks_of(int64_t n) { return (n + 127) / 128; }
 
 // ------------------------------------------------------------------ quantize
 
-// -> (codes, scales) or, for BOTH, (codes, scales, codes, scales).
-py::object quantize(int64_t plan, int device, const Tensor& x_, int blocks, at::ScalarType dtype,
-                    const c10::optional<Tensor>& source, int64_t choices,
-                    const c10::optional<int64_t>& stream) {
+struct Quantized {
+  Tensor q, s, q2, s2;     // q2, s2: the columns' of BOTH
+};
+
+Quantized quantize(int64_t plan, int device, const Tensor& x_, int blocks, at::ScalarType dtype,
+                   const c10::optional<Tensor>& source = {}, int64_t choices = 1,
+                   const c10::optional<int64_t>& stream = {}) {
   const int type = type_of(x_.scalar_type(), "X"), format = format_of(dtype, "dtype");
   on_device(x_, "X", device);
   if (x_.dim() != 2 && x_.dim() != 3) refuse("X must be [rows, cols] or [matrices, rows, cols]");
@@ -73,23 +102,20 @@ py::object quantize(int64_t plan, int device, const Tensor& x_, int blocks, at::
     q2 = codes();
     s2 = scales(GEMM_F8_COLUMNS);
   }
-  const int rc = gemm_f8_quantize(
-      plan_of(plan), blocks, format, type, narrow(batch, "matrices"), narrow(rows, "rows"),
-      narrow(cols, "cols"), x.const_data_ptr(), x.size(-2) > 1 ? x.stride(-2) : pitch,
-      batch > 1 ? x.stride(0) : 0, source ? ints(*source) : nullptr, narrow(choices, "choices"),
-      narrow(x.size(-2), "rows"), q.data_ptr(), pitch, rows * pitch, s.data_ptr<float>(),
-      both ? q2.data_ptr() : nullptr, both ? s2.data_ptr<float>() : nullptr, on.raw());
-  if (rc < 0) return py::int_(rc);
+  check(gemm_f8_quantize(
+            plan_of(plan), blocks, format, type, narrow(batch, "matrices"), narrow(rows, "rows"),
+            narrow(cols, "cols"), x.const_data_ptr(), x.size(-2) > 1 ? x.stride(-2) : pitch,
+            batch > 1 ? x.stride(0) : 0, source ? ints(*source) : nullptr,
+            narrow(choices, "choices"), narrow(x.size(-2), "rows"), q.data_ptr(), pitch,
+            rows * pitch, s.data_ptr<float>(), both ? q2.data_ptr() : nullptr,
+            both ? s2.data_ptr<float>() : nullptr, on.raw()),
+        "gemm_f8_quantize");
   if (turned) {
     q = q.transpose(-1, -2);
     s = s.transpose(-1, -2);
-    if (both) {
-      q2 = q2.transpose(-1, -2);
-      s2 = s2.transpose(-1, -2);
-      return py::make_tuple(q2, s2, q, s);
-    }
+    if (both) return {q2.transpose(-1, -2), s2.transpose(-1, -2), q, s};
   }
-  return both ? py::make_tuple(q, s, q2, s2) : py::make_tuple(q, s);
+  return {q, s, q2, s2};
 }
 
 // ------------------------------------------------------------------ product
@@ -132,10 +158,10 @@ gemm_f8_operand operand(const Tensor& x, const Tensor& s, const char* name, bool
   return o;
 }
 
-py::object matmul_f8(int64_t plan, int device, const Tensor& a, const Tensor& sa, const Tensor& b,
-                     const Tensor& sb, const c10::optional<Tensor>& out_, at::ScalarType dtype,
-                     const c10::optional<Tensor>& starts, bool accumulate,
-                     const c10::optional<int64_t>& stream) {
+Tensor matmul_f8(int64_t plan, int device, const Tensor& a, const Tensor& sa, const Tensor& b,
+                 const Tensor& sb, const c10::optional<Tensor>& out_, at::ScalarType dtype,
+                 const c10::optional<Tensor>& starts, bool accumulate = false,
+                 const c10::optional<int64_t>& stream = {}) {
   if (a.dim() != 2 || (b.dim() != 2 && !(b.dim() == 3 && starts)))
     refuse("A must be [M, K] and B [K, N], or [experts, K, N] with starts");
   const int form = !starts ? GEMM_F8_DENSE : b.dim() == 3 ? GEMM_F8_BY_ROWS : GEMM_F8_BY_INNER;
@@ -166,16 +192,17 @@ py::object matmul_f8(int64_t plan, int device, const Tensor& a, const Tensor& sa
   }
   const int type = type_of(c.scalar_type(), "C");
   if (accumulate && type != GEMM_F8_F32) refuse("accumulate needs a float32 C");
-  if (c.numel() == 0) return py::cast(c);
+  if (c.numel() == 0) return c;
   const gemm_f16_plan_t p = plan_of(plan);
   const int m = narrow(M, "M"), n = narrow(N, "N"), k = narrow(K, "K"), e = narrow(experts, "experts");
   const size_t bytes = gemm_f8_workspace(p, form, m, n, k, e, A.transposed);
   Tensor ws;
   if (bytes > 0) ws = at::empty({(int64_t)bytes}, a.options().dtype(at::kByte));
-  const int rc = gemm_f8_run(p, form, m, n, k, e, starts ? ints(*starts) : nullptr, &A, &B,
-                             c.data_ptr(), M > 1 ? c.stride(-2) : N, c.dim() == 3 ? c.stride(0) : 0,
-                             type, accumulate, bytes > 0 ? ws.data_ptr() : nullptr, bytes, on.raw());
-  return done(rc, py::cast(c));
+  check(gemm_f8_run(p, form, m, n, k, e, starts ? ints(*starts) : nullptr, &A, &B, c.data_ptr(),
+                    M > 1 ? c.stride(-2) : N, c.dim() == 3 ? c.stride(0) : 0, type, accumulate,
+                    bytes > 0 ? ws.data_ptr() : nullptr, bytes, on.raw()),
+        "gemm_f8_run");
+  return c;
 }
 
 // ------------------------------------------------------------------ experts
@@ -214,99 +241,327 @@ void need_maps(const Tensor& rows, const Tensor& source, int device) {
   if (!rows.is_contiguous() || rows.size(1) < 1) refuse("maps.rows must be contiguous [tokens, choices]");
 }
 
-py::object expert_gather(int64_t plan, int device, const Tensor& x, const Tensor& rows,
-                         const Tensor& source, const c10::optional<int64_t>& stream) {
+Tensor expert_gather(int64_t plan, int device, const Tensor& x, const Tensor& rows,
+                     const Tensor& source) {
   need_rows(x, "X", device);
   need_maps(rows, source, device);
   if (x.size(0) != rows.size(0)) refuse("X must have a row for each token of the maps");
-  OnStream on(stream, device);
+  OnStream on({}, device);
   const Tensor y = at::empty({source.size(0), x.size(1)}, x.options());
-  const int rc = experts_gather(plan_of(plan), type_of(x.scalar_type(), "X"),
-                                narrow(source.size(0), "rows"), narrow(x.size(1), "cols"),
-                                x.const_data_ptr(), row_stride(x), narrow(x.size(0), "rows"),
-                                narrow(rows.size(1), "choices"), ints(source), y.data_ptr(),
-                                x.size(1), on.raw());
-  return done(rc, py::cast(y));
+  check(experts_gather(plan_of(plan), type_of(x.scalar_type(), "X"), narrow(source.size(0), "rows"),
+                       narrow(x.size(1), "cols"), x.const_data_ptr(), row_stride(x),
+                       narrow(x.size(0), "rows"), narrow(rows.size(1), "choices"), ints(source),
+                       y.data_ptr(), x.size(1), on.raw()),
+        "experts_gather");
+  return y;
 }
 
-int weights_type(const c10::optional<Tensor>& w, const Tensor& s, const Tensor& rows, int device) {
-  if (!w) return GEMM_F8_F32;
-  on_device(*w, "weights", device);
-  if (w->sizes() != rows.sizes() || !w->is_contiguous() ||
-      (w->scalar_type() != at::kFloat && w->scalar_type() != s.scalar_type()))
+// w: undefined where all weights are 1.
+int weights_type(const Tensor& w, const Tensor& s, const Tensor& rows, int device) {
+  if (!w.defined()) return GEMM_F8_F32;
+  on_device(w, "weights", device);
+  if (w.sizes() != rows.sizes() || !w.is_contiguous() ||
+      (w.scalar_type() != at::kFloat && w.scalar_type() != s.scalar_type()))
     refuse("weights must be contiguous [tokens, choices], float32 or of the rows' type");
-  return type_of(w->scalar_type(), "weights");
+  return type_of(w.scalar_type(), "weights");
 }
 
-py::object expert_combine(int64_t plan, int device, const Tensor& s, const Tensor& rows,
-                          const Tensor& source, const c10::optional<Tensor>& weights,
-                          const c10::optional<int64_t>& stream) {
+Tensor expert_combine(int64_t plan, int device, const Tensor& s, const Tensor& rows,
+                      const Tensor& source, const Tensor& weights) {
   need_rows(s, "S", device);
   need_maps(rows, source, device);
   if (s.size(0) != source.size(0)) refuse("S must have a row for each row of the maps");
   const int wt = weights_type(weights, s, rows, device);
-  OnStream on(stream, device);
+  OnStream on({}, device);
   const Tensor y = at::empty({rows.size(0), s.size(1)}, s.options());
-  const int rc = experts_combine(plan_of(plan), type_of(s.scalar_type(), "S"),
-                                 narrow(rows.size(0), "tokens"), narrow(rows.size(1), "choices"),
-                                 narrow(s.size(1), "cols"), s.const_data_ptr(), row_stride(s),
-                                 narrow(s.size(0), "rows"), ints(rows),
-                                 weights ? weights->const_data_ptr() : nullptr, wt, y.data_ptr(),
-                                 s.size(1), on.raw());
-  return done(rc, py::cast(y));
+  check(experts_combine(plan_of(plan), type_of(s.scalar_type(), "S"), narrow(rows.size(0), "tokens"),
+                        narrow(rows.size(1), "choices"), narrow(s.size(1), "cols"),
+                        s.const_data_ptr(), row_stride(s), narrow(s.size(0), "rows"), ints(rows),
+                        weights.defined() ? weights.const_data_ptr() : nullptr, wt, y.data_ptr(),
+                        s.size(1), on.raw()),
+        "experts_combine");
+  return y;
 }
 
-// -> (dS or None, dweights or None), or an error code.
-py::object expert_combine_gradient(int64_t plan, int device, const Tensor& dy,
-                                   const c10::optional<Tensor>& s, const Tensor& rows,
-                                   const Tensor& source, const c10::optional<Tensor>& weights,
-                                   bool want_s, bool want_w, const c10::optional<int64_t>& stream) {
-  need_rows(dy, "dY", device);
-  need_maps(rows, source, device);
+// -> the gradients of S and of the weights, undefined where not wanted.
+std::pair<Tensor, Tensor> expert_combine_gradient(int64_t plan, int device, const Tensor& dy,
+                                                  const Tensor& s, const Tensor& rows,
+                                                  const Tensor& source, const Tensor& weights,
+                                                  bool want_s, bool want_w) {
   const int64_t n = source.size(0), cols = dy.size(1);
-  if (dy.size(0) != rows.size(0)) refuse("dY must have a row for each token of the maps");
-  want_w = want_w && weights;
-  if (want_w) {
-    if (!s) refuse("the weights' gradient needs S");
-    need_rows(*s, "S", device);
-    if (s->size(0) != n || s->size(1) != cols || s->scalar_type() != dy.scalar_type())
-      refuse("S must have a row for each row of the maps, and dY's columns and type");
-  }
   const int wt = weights_type(weights, dy, rows, device);
-  OnStream on(stream, device);
+  OnStream on({}, device);
   Tensor ds, dw;
   if (want_s) ds = at::empty({n, cols}, dy.options());
-  if (want_w) dw = at::empty(weights->sizes(), weights->options());
-  const int rc = experts_combine_gradient(
-      plan_of(plan), type_of(dy.scalar_type(), "dY"), narrow(rows.size(0), "tokens"),
-      narrow(rows.size(1), "choices"), narrow(cols, "cols"), dy.const_data_ptr(), row_stride(dy),
-      want_w ? s->const_data_ptr() : nullptr, want_w ? row_stride(*s) : 0, narrow(n, "rows"),
-      ints(rows), ints(source), weights ? weights->const_data_ptr() : nullptr, wt,
-      want_s ? ds.data_ptr() : nullptr, cols, want_w ? dw.data_ptr() : nullptr, on.raw());
-  return done(rc, py::make_tuple(want_s ? py::cast(ds) : py::none(),
-                                 want_w ? py::cast(dw) : py::none()));
+  if (want_w) dw = at::empty(weights.sizes(), weights.options());
+  check(experts_combine_gradient(
+            plan_of(plan), type_of(dy.scalar_type(), "dY"), narrow(rows.size(0), "tokens"),
+            narrow(rows.size(1), "choices"), narrow(cols, "cols"), dy.const_data_ptr(),
+            row_stride(dy), want_w ? s.const_data_ptr() : nullptr, want_w ? row_stride(s) : 0,
+            narrow(n, "rows"), ints(rows), ints(source), weights.const_data_ptr(), wt,
+            want_s ? ds.data_ptr() : nullptr, cols, want_w ? dw.data_ptr() : nullptr, on.raw()),
+        "experts_combine_gradient");
+  return {ds, dw};
 }
 
+// ------------------------------------------------------------------ gradients
+
+using torch::autograd::AutogradContext;
+using torch::autograd::variable_list;
+
+// A graph of gradients keeps its plan: the Python object, whose handle is None
+// once it has been closed.
+struct PlanRef : torch::CustomClassHolder {
+  py::object plan;
+  int device;
+  PlanRef(py::object p, int d) : plan(std::move(p)), device(d) {}
+  ~PlanRef() override {
+    if (!Py_IsInitialized()) {
+      plan.release();
+      return;
+    }
+    py::gil_scoped_acquire gil;
+    plan = py::object();
+  }
+  int64_t handle() const {
+    py::gil_scoped_acquire gil;
+    const py::object h = plan.attr("handle");
+    if (h.is_none()) throw std::runtime_error("the plan was closed before the backward pass");
+    return h.cast<int64_t>();
+  }
+};
+using Keep = c10::intrusive_ptr<PlanRef>;
+
+void keep(AutogradContext* ctx, const Keep& plan) {
+  ctx->saved_data["plan"] = c10::IValue::make_capsule(plan);
+}
+Keep kept(AutogradContext* ctx) {
+  return c10::static_intrusive_pointer_cast<PlanRef>(ctx->saved_data["plan"].toCapsule());
+}
+
+// A gradient as the calls take it (it may be one number for all of a tensor).
+Tensor dense(const Tensor& x) { return x.contiguous(); }
+
+// Gradients that have none of their own: an error where one is asked for.
+variable_list once(variable_list grads) {
+  if (!at::GradMode::is_enabled()) return grads;
+  variable_list some;
+  for (const Tensor& g : grads)
+    if (g.defined()) some.push_back(g.detach().set_requires_grad(true));
+  auto fn = std::make_shared<torch::autograd::DelayedError>(
+      "8-bit products and weighted sums of experts' rows have first gradients only",
+      (int)some.size());
+  some = (*fn)(std::move(some));
+  size_t at = 0;
+  for (Tensor& g : grads)
+    if (g.defined()) g = some[at++];
+  return grads;
+}
+
+// Y = X W^T; formats[0] that of X and W, [1] that of dY.  Without w, W comes as
+// codes and scales of tiles.
+struct LinearCall {
+  Keep plan;
+  Tensor codes, scales;
+  c10::optional<Tensor> starts;
+  at::ScalarType formats[2];
+  bool want_x, want_w;     // gradients that a backward pass may ask for
+};
+
+struct Linear : torch::autograd::Function<Linear> {
+  static Tensor run(AutogradContext* ctx, const Tensor& x, const c10::optional<Tensor>& w,
+                    const LinearCall& call) {
+    const int64_t plan = call.plan->handle();
+    const int device = call.plan->device;
+    const Quantized qw = w ? quantize(plan, device, *w, GEMM_F8_TILES, call.formats[0])
+                           : Quantized{call.codes, call.scales, {}, {}};
+    const Quantized qx =
+        quantize(plan, device, x, call.want_w ? GEMM_F8_BOTH : GEMM_F8_ROWS, call.formats[0]);
+    if (ctx) {
+      keep(ctx, call.plan);
+      ctx->saved_data["x"] = x.scalar_type();
+      ctx->saved_data["w"] = w ? w->scalar_type() : x.scalar_type();
+      ctx->saved_data["format"] = call.formats[1];
+      ctx->save_for_backward({qx.q2, qx.s2, call.want_x ? qw.q : Tensor(),
+                              call.want_x ? qw.s : Tensor(), call.starts ? *call.starts : Tensor()});
+    }
+    return matmul_f8(plan, device, qx.q, qx.s, qw.q.transpose(-1, -2), qw.s.transpose(-1, -2), {},
+                     x.scalar_type(), call.starts);
+  }
+  static Tensor forward(AutogradContext* ctx, const Tensor& x, const c10::optional<Tensor>& w,
+                        const LinearCall& call) {
+    return run(ctx, x, w, call);
+  }
+  static variable_list backward(AutogradContext* ctx, variable_list grads) {
+    const variable_list saved = ctx->get_saved_variables();
+    const Tensor &xq = saved[0], &xs = saved[1], &wq = saved[2], &ws = saved[3];
+    const auto starts = saved[4].defined() ? c10::optional<Tensor>(saved[4]) : c10::nullopt;
+    const auto type = [&](const char* key) {
+      return static_cast<at::ScalarType>(ctx->saved_data[key].toInt());
+    };
+    const bool want_x = wq.defined() && ctx->needs_input_grad(0);
+    const bool want_w = xq.defined() && ctx->needs_input_grad(1);
+    variable_list out(3);
+    if (!want_x && !want_w) return out;
+    const Keep plan = kept(ctx);
+    const int64_t h = plan->handle();
+    {
+      at::AutoGradMode off(false);
+      const Tensor dy = dense(grads[0]);
+      const Quantized g =
+          quantize(h, plan->device, dy,
+                   want_x && want_w ? GEMM_F8_BOTH : want_x ? GEMM_F8_ROWS : GEMM_F8_COLUMNS,
+                   type("format"));
+      if (want_x) out[0] = matmul_f8(h, plan->device, g.q, g.s, wq, ws, {}, type("x"), starts);
+      if (want_w) {
+        const Tensor &q = want_x ? g.q2 : g.q, &s = want_x ? g.s2 : g.s;
+        out[1] = matmul_f8(h, plan->device, q.transpose(-1, -2), s.transpose(-1, -2), xq, xs, {},
+                           type("w"), starts);
+      }
+    }
+    return once(std::move(out));
+  }
+};
+
+Tensor gather_call(const Keep& plan, const Tensor& x, const Tensor& rows, const Tensor& source);
+Tensor combine_call(const Keep& plan, const Tensor& s, const Tensor& weights, const Tensor& rows,
+                    const Tensor& source);
+
+struct MapsCall {
+  Keep plan;
+  Tensor rows, source;
+};
+
+// The gradients of these two are one another, and so have gradients themselves.
+struct Gather : torch::autograd::Function<Gather> {
+  static Tensor forward(AutogradContext* ctx, const Tensor& x, const MapsCall& call) {
+    keep(ctx, call.plan);
+    ctx->save_for_backward({call.rows, call.source});
+    return expert_gather(call.plan->handle(), call.plan->device, x, call.rows, call.source);
+  }
+  static variable_list backward(AutogradContext* ctx, variable_list grads) {
+    const variable_list saved = ctx->get_saved_variables();
+    return {combine_call(kept(ctx), dense(grads[0]), {}, saved[0], saved[1]), {}};
+  }
+};
+
+struct Combine : torch::autograd::Function<Combine> {
+  static Tensor forward(AutogradContext* ctx, const Tensor& s, const c10::optional<Tensor>& weights,
+                        const MapsCall& call) {
+    keep(ctx, call.plan);
+    const Tensor w = weights ? *weights : Tensor();
+    ctx->save_for_backward({w.defined() && w.requires_grad() ? s : Tensor(), w, call.rows, call.source});
+    return expert_combine(call.plan->handle(), call.plan->device, s, call.rows, call.source, w);
+  }
+  static variable_list backward(AutogradContext* ctx, variable_list grads) {
+    const variable_list saved = ctx->get_saved_variables();
+    const Tensor &s = saved[0], &weights = saved[1], &rows = saved[2], &source = saved[3];
+    const Keep plan = kept(ctx);
+    variable_list out(3);
+    if (!weights.defined()) {
+      out[0] = gather_call(plan, dense(grads[0]), rows, source);
+      return out;
+    }
+    const bool want_s = ctx->needs_input_grad(0), want_w = s.defined() && ctx->needs_input_grad(1);
+    if (!want_s && !want_w) return out;
+    {
+      at::AutoGradMode off(false);
+      std::tie(out[0], out[1]) =
+          expert_combine_gradient(plan->handle(), plan->device, dense(grads[0]), s, rows, source,
+                                  weights, want_s, want_w);
+    }
+    return once(std::move(out));
+  }
+};
+
+bool wants(const Tensor& x) {
+  return at::GradMode::is_enabled() && x.defined() && x.requires_grad();
+}
+
+Tensor gather_call(const Keep& plan, const Tensor& x, const Tensor& rows, const Tensor& source) {
+  if (wants(x)) return Gather::apply(x, MapsCall{plan, rows, source});
+  return expert_gather(plan->handle(), plan->device, x, rows, source);
+}
+Tensor combine_call(const Keep& plan, const Tensor& s, const Tensor& weights, const Tensor& rows,
+                    const Tensor& source) {
+  if (wants(s) || wants(weights))
+    return Combine::apply(s, weights.defined() ? c10::optional<Tensor>(weights) : c10::nullopt,
+                          MapsCall{plan, rows, source});
+  return expert_combine(plan->handle(), plan->device, s, rows, source, weights);
+}
+
+Tensor linear_f8(const py::object& plan, int device, const Tensor& x_, const Tensor& w,
+                 const Tensor& codes, const Tensor& scales, const c10::optional<Tensor>& starts,
+                 at::ScalarType format, at::ScalarType grad_format) {
+  if (x_.dim() < 1) refuse("X must be [.., K]");
+  if (starts && x_.dim() != 2) refuse("X must be [rows, K] where starts are given");
+  const Tensor& W = w.defined() ? w : codes;
+  if (W.dim() != (starts ? 3 : 2)) refuse("W must be [N, K], or [experts, N, K] with starts");
+  const Tensor x = x_.dim() == 2 ? x_ : x_.reshape({x_.numel() / std::max<int64_t>(x_.size(-1), 1), x_.size(-1)});
+  const LinearCall call = {c10::make_intrusive<PlanRef>(plan, device), codes, scales, starts,
+                           {format, grad_format}, wants(x), wants(w)};
+  const c10::optional<Tensor> given = w.defined() ? c10::optional<Tensor>(w) : c10::nullopt;
+  const Tensor y = call.want_x || call.want_w ? Linear::apply(x, given, call)
+                                              : Linear::run(nullptr, x, given, call);
+  if (x_.dim() == 2) return y;
+  std::vector<int64_t> shape(x_.sizes().begin(), x_.sizes().end());
+  shape.back() = y.size(1);
+  return y.view(shape);
+}
+
+at::ScalarType codes_type(int format) {
+  return format == GEMM_F8_E5M2 ? at::kFloat8_e5m2 : at::kFloat8_e4m3fn;
+}
+Tensor or_none(const c10::optional<Tensor>& x) { return x ? *x : Tensor(); }
+
 void add_f8_calls(py::module_& m) {
+  // -> (codes, scales) or, for BOTH, (codes, scales, codes, scales)
   m.def("quantize", [](int64_t plan, int device, const Tensor& x, int blocks, int format,
                        const c10::optional<Tensor>& source, int64_t choices,
                        const c10::optional<int64_t>& stream) {
-    return quantize(plan, device, x, blocks,
-                    format == GEMM_F8_E5M2 ? at::kFloat8_e5m2 : at::kFloat8_e4m3fn, source, choices,
-                    stream);
+    return answer([&]() -> py::object {
+      const Quantized r =
+          quantize(plan, device, x, blocks, codes_type(format), source, choices, stream);
+      return blocks == GEMM_F8_BOTH ? py::make_tuple(r.q, r.s, r.q2, r.s2)
+                                    : py::make_tuple(r.q, r.s);
+    });
   });
   m.def("matmul_f8", [](int64_t plan, int device, const Tensor& a, const Tensor& sa, const Tensor& b,
                         const Tensor& sb, const c10::optional<Tensor>& out, int type,
                         const c10::optional<Tensor>& starts, bool accumulate,
                         const c10::optional<int64_t>& stream) {
-    return matmul_f8(plan, device, a, sa, b, sb, out,
-                     type == GEMM_F8_F16 ? at::kHalf : type == GEMM_F8_BF16 ? at::kBFloat16 : at::kFloat,
-                     starts, accumulate, stream);
+    return answer([&]() -> py::object {
+      return py::cast(matmul_f8(plan, device, a, sa, b, sb, out,
+                                type == GEMM_F8_F16    ? at::kHalf
+                                : type == GEMM_F8_BF16 ? at::kBFloat16
+                                                       : at::kFloat,
+                                starts, accumulate, stream));
+    });
+  });
+  m.def("linear_f8", [](const py::object& plan, int device, const Tensor& x,
+                        const c10::optional<Tensor>& w, const c10::optional<Tensor>& codes,
+                        const c10::optional<Tensor>& scales, const c10::optional<Tensor>& starts,
+                        int format, int grad_format) {
+    return answer([&]() -> py::object {
+      return py::cast(linear_f8(plan, device, x, or_none(w), or_none(codes), or_none(scales), starts,
+                                codes_type(format), codes_type(grad_format)));
+    });
   });
   m.def("expert_maps", &expert_maps);
-  m.def("expert_gather", &expert_gather);
-  m.def("expert_combine", &expert_combine);
-  m.def("expert_combine_gradient", &expert_combine_gradient);
+  m.def("expert_gather", [](const py::object& plan, int device, const Tensor& x, const Tensor& rows,
+                            const Tensor& source) {
+    return answer([&]() -> py::object {
+      return py::cast(
+          gather_call(c10::make_intrusive<PlanRef>(plan, device), x, rows, source));
+    });
+  });
+  m.def("expert_combine", [](const py::object& plan, int device, const Tensor& s, const Tensor& rows,
+                             const Tensor& source, const c10::optional<Tensor>& weights) {
+    return answer([&]() -> py::object {
+      return py::cast(combine_call(c10::make_intrusive<PlanRef>(plan, device), s, or_none(weights),
+                                   rows, source));
+    });
+  });
 }
 
 }  // namespace
