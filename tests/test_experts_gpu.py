@@ -158,8 +158,10 @@ def test_gradients_of_gradients(g, plan):
     w = torch.rand(30, 2, device="cuda", requires_grad=True)
     y = g.expert_combine(plan, g.expert_gather(plan, x, m), m, w)
     dw, = torch.autograd.grad(y.sum(), w, create_graph=True)
+    with pytest.raises(RuntimeError):                  # torch's: no way from dw to x
+        torch.autograd.grad(dw.sum(), x, retain_graph=True)
     with pytest.raises(RuntimeError, match="first gradients only"):
-        torch.autograd.grad(dw.sum(), x)
+        dw.sum().backward()
 
 
 # ------------------------------------------------------------------ linear layers
