@@ -8,12 +8,17 @@
 // conversion rounds to nearest even and clamps the one number whose product
 // may pass L by FP32's rounding.
 //
-// Bound by the memory: each number is read once and written once (or twice,
-// for both directions).  ROWS: eight lanes a block, 16 numbers each, so that
-// a lane stores 16 bytes; nothing but shuffles.  The others: a CTA takes a tile
-// of 128 x 128 into registers (64 numbers a thread), reduces it along the rows
-// by shuffles and along the columns through 4 KB of shared memory, and writes
-// the codes of one or both directions from the same registers.
+// ROWS is bound by the memory: eight lanes a block, 16 numbers each, so that a
+// lane stores 16 bytes; nothing but shuffles (16001 x 4104 bf16: 34 us, 5.8 TB/s).
+// The others: a CTA takes a tile of 128 x 128 into registers (32 numbers a
+// thread), reduces it along the rows by shuffles and along the columns through
+// 8 KB of shared memory, and writes the codes of one or both directions from the
+// same registers, so that X is read once.  Maxima are taken of pairs in the
+// numbers' own type, divisions spread over the lanes.  Tiles take 43 us (4.6
+// TB/s), columns 54 and both directions 73 (3.6 TB/s), bound by their 16 to 22
+// instructions a number and the two barriers.  Tried: four columns of eight rows
+// a lane (stores of four bytes; tiles 55, both 73), CTAs that stay and fetch the
+// next tile early (82), two FP32 products at once (the pairs' moves cost more).
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -54,17 +59,46 @@ template <>
 struct alignas(16) Pack<float> {
   float v[16];
   __device__ float get(int i) const { return v[i]; }
+  using Pair = float2;      // two magnitudes
+  __device__ Pair size(int i) const { return make_float2(fabsf(v[2 * i]), fabsf(v[2 * i + 1])); }
 };
 template <>
 struct alignas(16) Pack<__half> {
   __half2 v[8];
   __device__ float get(int i) const { return i & 1 ? __high2float(v[i / 2]) : __low2float(v[i / 2]); }
+  using Pair = __half2;
+  __device__ Pair size(int i) const { return __habs2(v[i]); }
 };
 template <>
 struct alignas(16) Pack<__nv_bfloat16> {
-  __nv_bfloat162 v[8];
-  __device__ float get(int i) const { return i & 1 ? __high2float(v[i / 2]) : __low2float(v[i / 2]); }
+  uint32_t v[8];            // by their bits: FP32's upper half, and a sign
+  __device__ float get(int i) const {
+    return __uint_as_float(i & 1 ? v[i / 2] & 0xffff0000u : v[i / 2] << 16);
+  }
+  using Pair = __nv_bfloat162;
+  __device__ Pair size(int i) const {
+    const uint32_t m = v[i] & 0x7fff7fffu;
+    return *reinterpret_cast<const __nv_bfloat162*>(&m);
+  }
 };
+// Larger of two magnitudes; a NaN is left out beside a number.
+__device__ __forceinline__ float2 larger(float2 a, float2 b) {
+  return make_float2(fmaxf(a.x, b.x), fmaxf(a.y, b.y));
+}
+__device__ __forceinline__ __half2 larger(__half2 a, __half2 b) { return __hmax2(a, b); }
+__device__ __forceinline__ __nv_bfloat162 larger(__nv_bfloat162 a, __nv_bfloat162 b) {
+  return __hmax2(a, b);
+}
+__device__ __forceinline__ float2 floats(float2 a) { return a; }
+__device__ __forceinline__ float2 floats(__half2 a) { return __half22float2(a); }
+__device__ __forceinline__ float2 floats(__nv_bfloat162 a) { return __bfloat1622float2(a); }
+__device__ __forceinline__ float2 other_lane(float2 a, int d) {
+  return make_float2(__shfl_xor_sync(0xffffffffu, a.x, d), __shfl_xor_sync(0xffffffffu, a.y, d));
+}
+template <typename P>
+__device__ __forceinline__ P other_lane(P a, int d) {
+  return __shfl_xor_sync(0xffffffffu, a, d);
+}
 
 // Numbers col .. col + 15 of a row (0 past `cols`, and everywhere for a null
 // row).  VEC: rows start on 16-byte boundaries.
@@ -85,18 +119,11 @@ __device__ __forceinline__ void load16(Pack<T>& x, const T* row, int col, int co
 // Largest magnitude, NaN left out (infinity if there is one).
 template <typename T>
 __device__ __forceinline__ float largest(const Pack<T>& x) {
-  if constexpr (sizeof(T) == 4) {
-    float a = 0.f;
+  auto a = x.size(0);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) a = fmaxf(a, fabsf(x.v[i]));
-    return a;
-  } else {
-    auto a = __habs2(x.v[0]);
-#pragma unroll
-    for (int i = 1; i < 8; ++i) a = __hmax2(a, __habs2(x.v[i]));
-    const float lo = __low2float(a), hi = __high2float(a);
-    return fmaxf(fmaxf(lo, hi), 0.f);     // fmaxf leaves a NaN out
-  }
+  for (int i = 1; i < 8; ++i) a = larger(a, x.size(i));
+  const float2 f = floats(a);
+  return fmaxf(fmaxf(f.x, f.y), 0.f);     // fmaxf leaves a NaN out
 }
 // The same of the finite ones, for blocks that hold an infinity.
 template <typename T>
@@ -123,10 +150,21 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
   }
   return (uint32_t)lo | ((uint32_t)hi << 16);
 }
-// An infinity times the block's factor would be clamped: it becomes NaN.
-__device__ __forceinline__ float scaled(float x, float f) {
-  const float y = __fmul_rn(x, f);
-  return fabsf(y) < INFINITY ? y : NAN;
+// Sixteen codes; f(i): the factor of number i.  `inf`, the same in
+// the whole warp: there are infinities, which the conversion would clamp and
+// which become NaN.
+template <int FORMAT, typename T, typename F>
+__device__ __forceinline__ void codes16(uint32_t (&w)[4], const Pack<T>& x, bool inf, const F& f) {
+  float y[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) y[i] = __fmul_rn(x.get(i), f(i));
+  if (inf) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) y[i] = fabsf(y[i]) < INFINITY ? y[i] : NAN;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = codes4<FORMAT>(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
 }
 
 template <int FORMAT>
@@ -179,122 +217,150 @@ __global__ void __launch_bounds__(ROW_THREADS) quantize_rows_kernel(const Params
     float a = largest(x);
 #pragma unroll
     for (int d = 1; d < 8; d *= 2) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
-    const bool inf = !(a < INFINITY);
-    if (__any_sync(0xffffffffu, inf)) {
-      float f = largest_finite(x);
+    const bool inf = __any_sync(0xffffffffu, !(a < INFINITY));
+    if (inf) {
+      a = largest_finite(x);
 #pragma unroll
-      for (int d = 1; d < 8; d *= 2) f = fmaxf(f, __shfl_xor_sync(0xffffffffu, f, d));
-      a = f;
+      for (int d = 1; d < 8; d *= 2) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
     }
     a = fmaxf(a, FLOOR);
-    const float f = __fdiv_rn(LARGEST<FORMAT>, a);
+    // One division a lane: the factor by a block's even lanes, the scale by the odd.
+    const bool odd = part & 1;
+    const float q = __fdiv_rn(odd ? a : LARGEST<FORMAT>, odd ? LARGEST<FORMAT> : a);
+    const float f = __shfl_sync(0xffffffffu, q, lane & ~1);
     if (!real) continue;
     uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      w[i] = codes4<FORMAT>(scaled(x.get(4 * i), f), scaled(x.get(4 * i + 1), f),
-                            scaled(x.get(4 * i + 2), f), scaled(x.get(4 * i + 3), f));
+    codes16<FORMAT>(w, x, inf, [&](int) { return f; });
     if (col < p.cols)
       store_codes(p.Q + (int64_t)b * p.q_batch + (int64_t)r * p.ldq, col, p.cols, w);
-    if (part == 0) p.S[blk] = __fdiv_rn(a, LARGEST<FORMAT>);
+    if (part == 1) p.S[blk] = q;
   }
 }
 
-constexpr int TILE_THREADS = 256;
+constexpr int TILE_THREADS = 512, TILE_WARPS = TILE_THREADS / 32;
+constexpr int LINES = 1024 / TILE_THREADS;      // rows of a thread
 
 // BLOCKS: GEMM_F8_COLUMNS, _TILES or _BOTH.  Thread (warp w, lane l): rows
-// 16 w + 4 i + l / 8 for i < 4, columns 16 (l % 8) .. + 15.
+// 4 LINES w + 4 i + l / 8 for i < LINES, columns 16 (l % 8) .. + 15.
 template <typename T, int FORMAT, int BLOCKS, bool VEC>
-__global__ void __launch_bounds__(TILE_THREADS) quantize_tile_kernel(const Params p) {
-  __shared__ float top[8][128];
+__global__ void __launch_bounds__(TILE_THREADS, 2) quantize_tile_kernel(const Params p) {
+  __shared__ __align__(16) float top[TILE_WARPS][128];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = lane & 7;
   const int tile = (int)blockIdx.x;
   const int rb = tile / p.blk_cols, cb = tile - rb * p.blk_cols, b = (int)blockIdx.y;
-  const int row0 = rb * 128 + warp * 16 + (lane >> 3), col = cb * 128 + part * 16;
-  Pack<T> x[4];
+  const int row0 = rb * 128 + warp * 4 * LINES + (lane >> 3), col = cb * 128 + part * 16;
+  Pack<T> x[LINES];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < LINES; ++i) {
     const int r = row0 + 4 * i;
     load16<T, VEC>(x[i], r < p.rows ? row_of<T>(p, b, r) : nullptr, col, p.cols);
   }
   uint8_t* Q = p.Q + (int64_t)b * p.q_batch;
   if constexpr (BLOCKS == GEMM_F8_BOTH) {
+    float a[LINES];
+    bool inf = false;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float a = largest(x[i]);
+    for (int i = 0; i < LINES; ++i) {
+      a[i] = largest(x[i]);
 #pragma unroll
-      for (int d = 1; d < 8; d *= 2) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
-      if (__any_sync(0xffffffffu, !(a < INFINITY))) {
-        a = largest_finite(x[i]);
+      for (int d = 1; d < 8; d *= 2) a[i] = fmaxf(a[i], __shfl_xor_sync(0xffffffffu, a[i], d));
+      inf = inf || !(a[i] < INFINITY);
+    }
+    inf = __any_sync(0xffffffffu, inf);
+    if (inf) {
 #pragma unroll
-        for (int d = 1; d < 8; d *= 2) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
+      for (int i = 0; i < LINES; ++i) {
+        a[i] = largest_finite(x[i]);
+#pragma unroll
+        for (int d = 1; d < 8; d *= 2) a[i] = fmaxf(a[i], __shfl_xor_sync(0xffffffffu, a[i], d));
       }
-      a = fmaxf(a, FLOOR);
-      const float f = __fdiv_rn(LARGEST<FORMAT>, a);
+    }
+    // One division a lane: the first of a row's eight lanes have its lines'
+    // factors, the next ones their scales.
+    const bool upper = part >= LINES && part < 2 * LINES;
+    const int mine = part % LINES;
+    float m = a[0];
+#pragma unroll
+    for (int i = 1; i < LINES; ++i) m = mine == i ? a[i] : m;
+    m = fmaxf(m, FLOOR);
+    const float q = __fdiv_rn(upper ? m : LARGEST<FORMAT>, upper ? LARGEST<FORMAT> : m);
+    if (upper && row0 + 4 * mine < p.rows) p.S[(int64_t)(row0 + 4 * mine) * p.blk_cols + cb] = q;
+#pragma unroll
+    for (int i = 0; i < LINES; ++i) {
+      const float f = __shfl_sync(0xffffffffu, q, (lane & 24) + i);
       const int r = row0 + 4 * i;
-      if (r < p.rows) {
-        uint32_t w[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          w[k] = codes4<FORMAT>(scaled(x[i].get(4 * k), f), scaled(x[i].get(4 * k + 1), f),
-                                scaled(x[i].get(4 * k + 2), f), scaled(x[i].get(4 * k + 3), f));
-        if (col < p.cols) store_codes(Q + (int64_t)r * p.ldq, col, p.cols, w);
-        if (part == 0) p.S[(int64_t)r * p.blk_cols + cb] = __fdiv_rn(a, LARGEST<FORMAT>);
-      }
+      uint32_t w[4];
+      codes16<FORMAT>(w, x[i], inf, [&](int) { return f; });
+      if (r < p.rows && col < p.cols) store_codes(Q + (int64_t)r * p.ldq, col, p.cols, w);
     }
   }
   if constexpr (BLOCKS == GEMM_F8_TILES) {
-    float a = fmaxf(fmaxf(largest(x[0]), largest(x[1])), fmaxf(largest(x[2]), largest(x[3])));
-    if (__syncthreads_or(!(a < INFINITY)))
-      a = fmaxf(fmaxf(largest_finite(x[0]), largest_finite(x[1])),
-                fmaxf(largest_finite(x[2]), largest_finite(x[3])));
+    float a = 0.f;
+#pragma unroll
+    for (int i = 0; i < LINES; ++i) a = fmaxf(a, largest(x[i]));
+    const bool inf = __syncthreads_or(!(a < INFINITY));
+    if (inf) {
+      a = 0.f;
+#pragma unroll
+      for (int i = 0; i < LINES; ++i) a = fmaxf(a, largest_finite(x[i]));
+    }
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
     if (lane == 0) top[0][warp] = a;
     __syncthreads();
     a = FLOOR;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a = fmaxf(a, top[0][i]);
+    for (int i = 0; i < TILE_WARPS; ++i) a = fmaxf(a, top[0][i]);
     const float f = __fdiv_rn(LARGEST<FORMAT>, a);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < LINES; ++i) {
       const int r = row0 + 4 * i;
       uint32_t w[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        w[k] = codes4<FORMAT>(scaled(x[i].get(4 * k), f), scaled(x[i].get(4 * k + 1), f),
-                              scaled(x[i].get(4 * k + 2), f), scaled(x[i].get(4 * k + 3), f));
+      codes16<FORMAT>(w, x[i], inf, [&](int) { return f; });
       if (r < p.rows && col < p.cols) store_codes(Q + (int64_t)r * p.ldq, col, p.cols, w);
     }
     if (threadIdx.x == 0)
       p.S[((int64_t)b * p.blk_rows + rb) * p.blk_cols + cb] = __fdiv_rn(a, LARGEST<FORMAT>);
   } else {
-    // Columns: each thread's four rows, the warp's sixteen, the CTA's 128.
-    float a[16];
-    bool inf = false;
+    // Columns: each thread's lines, the warp's, the CTA's 128 rows.
+    // A NaN that no number of its column replaces falls out at the end, where the
+    // floor does.
+    typename Pack<T>::Pair top2[8];
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      a[k] = fmaxf(fmaxf(fabsf(x[0].get(k)), fabsf(x[1].get(k))),
-                   fmaxf(fabsf(x[2].get(k)), fabsf(x[3].get(k))));
-      inf = inf || !(a[k] < INFINITY);   // a NaN in all four, or an infinity
+    for (int k = 0; k < 8; ++k) {
+      top2[k] = x[0].size(k);
+#pragma unroll
+      for (int i = 1; i < LINES; ++i) top2[k] = larger(top2[k], x[i].size(k));
     }
-    if (__any_sync(0xffffffffu, inf)) {
+    typename Pack<T>::Pair all = top2[0];
+#pragma unroll
+    for (int k = 1; k < 8; ++k) all = larger(all, top2[k]);
+    const float2 of_all = floats(all);
+    const bool inf = __any_sync(0xffffffffu, of_all.x == INFINITY || of_all.y == INFINITY);
+    float a[16];
+    if (inf) {
 #pragma unroll
       for (int k = 0; k < 16; ++k) {
         a[k] = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < LINES; ++i) {
           const float v = fabsf(x[i].get(k));
           a[k] = fmaxf(a[k], v < INFINITY ? v : 0.f);
         }
+        a[k] = fmaxf(a[k], __shfl_xor_sync(0xffffffffu, a[k], 8));
+        a[k] = fmaxf(a[k], __shfl_xor_sync(0xffffffffu, a[k], 16));
       }
-    }
+    } else {
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      a[k] = fmaxf(a[k], __shfl_xor_sync(0xffffffffu, a[k], 8));
-      a[k] = fmaxf(a[k], __shfl_xor_sync(0xffffffffu, a[k], 16));
+      for (int k = 0; k < 8; ++k) {
+        top2[k] = larger(top2[k], other_lane(top2[k], 8));
+        top2[k] = larger(top2[k], other_lane(top2[k], 16));
+        const float2 f = floats(top2[k]);
+        a[2 * k] = f.x;
+        a[2 * k + 1] = f.y;
+      }
     }
     if (lane < 8) {
 #pragma unroll
@@ -306,7 +372,7 @@ __global__ void __launch_bounds__(TILE_THREADS) quantize_tile_kernel(const Param
     if (threadIdx.x < 128) {
       float m = FLOOR;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = fmaxf(m, top[i][threadIdx.x]);
+      for (int i = 0; i < TILE_WARPS; ++i) m = fmaxf(m, top[i][threadIdx.x]);
       top[0][threadIdx.x] = __fdiv_rn(LARGEST<FORMAT>, m);
       float* S = BLOCKS == GEMM_F8_BOTH ? p.S2 : p.S;
       const int c = cb * 128 + (int)threadIdx.x;
@@ -320,14 +386,10 @@ __global__ void __launch_bounds__(TILE_THREADS) quantize_tile_kernel(const Param
       *reinterpret_cast<float4*>(&f[k]) = *reinterpret_cast<const float4*>(&top[0][part * 16 + k]);
     if (BLOCKS == GEMM_F8_BOTH) Q = p.Q2;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < LINES; ++i) {
       const int r = row0 + 4 * i;
       uint32_t w[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        w[k] = codes4<FORMAT>(scaled(x[i].get(4 * k), f[4 * k]), scaled(x[i].get(4 * k + 1), f[4 * k + 1]),
-                              scaled(x[i].get(4 * k + 2), f[4 * k + 2]),
-                              scaled(x[i].get(4 * k + 3), f[4 * k + 3]));
+      codes16<FORMAT>(w, x[i], inf, [&](int k) { return f[k]; });
       if (r < p.rows && col < p.cols) store_codes(Q + (int64_t)r * p.ldq, col, p.cols, w);
     }
   }
