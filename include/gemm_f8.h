@@ -11,7 +11,10 @@
  *     C[m,n] = sum_b  sa[m,b] sb[b,n]  sum_{k in block b} A[m,k] B[k,n]
  *
  * with the inner sums on the tensor cores and the outer ones in FP32, and one
- * rounding to C's type.  The last block of a dimension may be shorter.
+ * rounding to C's type.  A block's inner sum is multiplied with one scale and
+ * then the other (or, where that is a normal FP32 number, with their product):
+ * where the first of these is below 2^-126, digits are lost that a large second
+ * scale would have shown.  The last block of a dimension may be shorter.
  *
  * Conventions are those of gemm_f16.h: device pointers on the plan's device,
  * leading dimensions in elements, GEMM_F16_* codes (on an error nothing has
