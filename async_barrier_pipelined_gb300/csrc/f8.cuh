@@ -59,7 +59,6 @@ struct Params {
   int units;                 // DENSE, BY_INNER; BY_ROWS knows them on the device
   int full_units, cut_units, parts;   // large kernel, DENSE: see there
   float* ws;
-  unsigned* counters;
   int* status;
   unsigned long long timeout_ns;
   int fault_unit;

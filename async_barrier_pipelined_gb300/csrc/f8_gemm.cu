@@ -30,8 +30,7 @@ SmallKernel small_kernel() {
   return {f8::small::f8_small_kernel<NT>, C::SMEM, C::SMEM_EXPERTS, C::CTAS};
 }
 SmallKernel small_kernel(int nt) {
-  return nt == 16 ? small_kernel<16>()
-                  : nt == 32 ? small_kernel<32>() : nt == 64 ? small_kernel<64>() : small_kernel<128>();
+  return nt == 16 ? small_kernel<16>() : nt == 32 ? small_kernel<32>() : small_kernel<64>();
 }
 
 constexpr int MAX_SIZE = 0x7fffffff - 1023;   // coordinates of a last tile stay in 31 bits
@@ -56,11 +55,14 @@ Choice choose(const gemm_f16_plan_s* p, int form, int M, int N, int K, int exper
   c.parts = 1;
   const int kblocks = (int)ceil_div(K, f8::BLOCK);
   // Rows of a tile of the small kernel: those of the call, or of an expert on
-  // the average.
+  // the average.  Up to 64 of them: 64 x 4096 x 4096 takes 13.2 us there and 14.1
+  // in the large kernel, 64 experts of 64 rows (1024 x 2048) 40.6 and 44.1; with a
+  // tile of 128 rows 128 x 4096 x 4096 took 18.8 and 16 experts of 96 rows (4096 x
+  // 2048) 102, in the large kernel 16.4 and 43.
   const int64_t rows = form == GEMM_F8_BY_ROWS ? ceil_div(M, experts) : M;
-  if (form != GEMM_F8_BY_INNER && !a_transposed && rows <= 128) {
+  if (form != GEMM_F8_BY_INNER && !a_transposed && rows <= 64) {
     c.small = true;
-    c.nt = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+    c.nt = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
     // As many CTAs for a tile as keep all resident (CTAs per SM) and leave each
     // two K blocks or more.
     const int64_t tiles_n = ceil_div(N, f8::small::CN);
@@ -77,11 +79,13 @@ Choice choose(const gemm_f16_plan_s* p, int form, int M, int N, int K, int exper
     const int64_t tiles = ceil_div(M, f8::large::PM) * ceil_div(N, f8::large::PN);
     const int pairs = pairs_of(p);
     const int rem = (int)(tiles % pairs);
-    // Parts for a last wave of at most half the pairs, each of four K blocks
-    // or more (a part costs its tile's 256 KB, written and read).
+    // Parts for a last wave of at most half the pairs, each of four K blocks or
+    // more, where they save sixteen blocks (0.4 to 0.65 us each): the parts' 256 KB,
+    // written and read, and a launch cost 7 us.  129 x 4096 x 4096: 16.5 us with
+    // four parts, 19.1 without; 1000 x 1024 x 2048 (12 blocks saved) 14.2 and 12.5.
     if (rem > 0) {
-      const int parts = std::min({pairs / rem, kblocks / 4, 8});
-      if (parts > 1) {
+      const int parts = std::min({pairs / rem, kblocks / 4, f8::large::MAX_PARTS});
+      if (parts > 1 && kblocks - ceil_div(kblocks, parts) >= 16) {
         c.tail_tiles = rem;
         c.parts = parts;
       }
@@ -90,12 +94,9 @@ Choice choose(const gemm_f16_plan_s* p, int form, int M, int N, int K, int exper
   return c;
 }
 
-size_t counter_bytes(const Choice& c) {
-  return (size_t)ceil_div((int64_t)c.tail_tiles * f8::large::TILE_COUNTERS * 4, 256) * 256;
-}
 size_t workspace_bytes(const Choice& c) {
   if (c.small || c.parts == 1) return 0;
-  return counter_bytes(c) + (size_t)c.tail_tiles * c.parts * f8::large::PART_FLOATS * 4;
+  return (size_t)c.tail_tiles * c.parts * f8::large::PART_FLOATS * 4;
 }
 
 bool off(const void* p, uintptr_t mask) { return ((uintptr_t)p & mask) != 0; }
@@ -182,7 +183,7 @@ int f8_plan_init(gemm_f16_plan_s* p, const cudaDeviceProp& prop) {
     GF16_CUDA(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                    (int)f8::large::SMEM_BYTES),
               "cudaFuncSetAttribute(8-bit product smem)");
-  for (int nt = 16; nt <= 128; nt *= 2) {
+  for (int nt = 16; nt <= 64; nt *= 2) {
     const SmallKernel k = small_kernel(nt);
     GF16_CUDA(cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                    (int)k.smem_experts),
@@ -335,17 +336,26 @@ int gemm_f8_run(gemm_f16_plan_t p, int form, int M, int N, int K, int experts,
   prm.units = form == GEMM_F8_BY_INNER ? (int)tiles * experts
                                        : prm.full_units + c.tail_tiles * c.parts;
   prm.cut_units = c.tail_tiles * c.parts;
-  if (need > 0) {
-    prm.counters = static_cast<unsigned*>(workspace);
-    prm.ws = reinterpret_cast<float*>(static_cast<char*>(workspace) + counter_bytes(c));
-    GF16_CUDA(cudaMemsetAsync(workspace, 0, counter_bytes(c), st), "cudaMemsetAsync(counters)");
-  }
+  prm.ws = static_cast<float*>(workspace);
   const int64_t most = form == GEMM_F8_BY_ROWS
                            ? (ceil_div(M, PM) + std::min(M, experts)) * (int64_t)prm.tiles_n
                            : prm.units;
   const int pairs = (int)std::min<int64_t>(most, pairs_of(p));
-  return launch(p, prm.sb_shift ? f8_large_kernel<false> : f8_large_kernel<true>,
-                "launch f8_large_kernel", 2 * pairs, 0, NUM_THREADS, SMEM_BYTES, st, tmA, tmB, prm);
+  rc = launch(p, prm.sb_shift ? f8_large_kernel<false> : f8_large_kernel<true>,
+              "launch f8_large_kernel", 2 * pairs, 0, NUM_THREADS, SMEM_BYTES, st, tmA, tmB, prm);
+  if (rc || c.tail_tiles == 0) return rc;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)c.tail_tiles * 2 * PROMOTE_WARPS, 1, 1);
+  cfg.blockDim = dim3(JOIN_THREADS, 1, 1);
+  cfg.stream = st;
+  cudaLaunchAttribute pdl;
+  pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &pdl;
+  cfg.numAttrs = 1;
+  GF16_CUDA(cudaLaunchKernelEx(&cfg, prm.sb_shift ? f8_join_kernel<false> : f8_join_kernel<true>, prm),
+            "launch f8_join_kernel");
+  return GEMM_F16_OK;
 }
 
 }  // extern "C"

@@ -22,11 +22,10 @@
 // ranges of K blocks, so that no pair idles.  These come first: the pairs that
 // had one are then out of step with the others, and the tiles' stores of some
 // run beside the products of the others.  Each writes FP32 sums to the workspace,
-// and whichever warp finds itself the last of its rows and columns (a counter,
-// one for each warp's piece of a tile) adds the parts in their order and stores
-// C.  BY_ROWS: tiles of 256 rows within an expert's segment, those of one column
-// of tiles side by side.  BY_INNER: all tiles of each expert, with that expert's
-// K blocks.
+// and a second kernel adds a tile's parts in their order and stores C (129 x 4096
+// x 4096: 16.5 us; with the last warp to arrive adding them, 40).  BY_ROWS: tiles
+// of 256 rows within an expert's segment, those of one column of tiles side by
+// side.  BY_INNER: all tiles of each expert, with that expert's K blocks.
 //
 // Barriers (as in gemm_pair.cuh): full[s] leader only, 1 arrival and both
 // CTAs' bytes; empty[s] both CTAs, multicast commit; tfull[a] both CTAs,
@@ -79,9 +78,9 @@ static_assert(OFF_BAR % 8 == 0 && OFF_EPI % 128 == 0 && OFF_SCALE % 16 == 0, "al
 constexpr int IO_REGS = 56, PROMOTE_REGS = 224;
 static_assert(128 * IO_REGS + 256 * PROMOTE_REGS <= 384 * 168, "register split");
 
-// FP32 numbers of a cut tile's part, and the counters of a cut tile.
+// FP32 numbers of a cut tile's part.
 constexpr int PART_FLOATS = PM * PN;
-constexpr int TILE_COUNTERS = 2 * PROMOTE_WARPS;
+constexpr int MAX_PARTS = 8;
 
 struct Bars {
   uint32_t full, empty, tfull, tempty, sfull, sempty, mma_done;
@@ -304,39 +303,15 @@ __device__ __forceinline__ void store_rows(const Params& p, T* C, const uint64_t
   }
 }
 
-// This warp's piece of a cut tile: its part to the workspace; true for the
-// warp that finds all others' there, with their sum (in the parts' order) in
-// acc.
-__device__ __forceinline__ bool join_parts(const Params& p, const Unit& g, uint32_t rank,
-                                           uint32_t w, uint32_t lane, uint64_t (&acc)[64]) {
-  // part -> [rank][warp][pair of float2][lane], 16 bytes a lane
-  const int64_t stride = PART_FLOATS / 4;
-  ulonglong2* base = reinterpret_cast<ulonglong2*>(p.ws) + (int64_t)g.tail * p.parts * stride +
+// This warp's piece of a cut tile's part to the workspace, as its lanes hold it:
+// [part][rank][warp][32][lane], 16 bytes a lane.
+__device__ __forceinline__ void store_part(const Params& p, const Unit& g, uint32_t rank, uint32_t w,
+                                           uint32_t lane, const uint64_t (&acc)[64]) {
+  ulonglong2* mine = reinterpret_cast<ulonglong2*>(p.ws) +
+                     ((int64_t)g.tail * p.parts + g.part) * (PART_FLOATS / 4) +
                      (rank * PROMOTE_WARPS + w) * 32 * 32 + lane;
-  ulonglong2* mine = base + g.part * stride;
 #pragma unroll
   for (int j = 0; j < 32; ++j) __stcg(mine + j * 32, make_ulonglong2(acc[2 * j], acc[2 * j + 1]));
-  __threadfence();
-  __syncwarp();
-  unsigned before = 0;
-  if (lane == 0)
-    before = atomicAdd(p.counters + g.tail * TILE_COUNTERS + rank * PROMOTE_WARPS + w, 1u);
-  before = __shfl_sync(0xffffffffu, before, 0);
-  if (before != (unsigned)p.parts - 1) return false;
-  __threadfence();
-  const uint64_t one = ptx::pack_f2(1.f, 1.f);
-#pragma unroll
-  for (int j = 0; j < 32; ++j) {
-    ulonglong2 sum = __ldcg(base + j * 32);
-    for (int i = 1; i < p.parts; ++i) {
-      const ulonglong2 x = __ldcg(base + i * stride + j * 32);
-      sum.x = ptx::fma_f2(x.x, one, sum.x);
-      sum.y = ptx::fma_f2(x.y, one, sum.y);
-    }
-    acc[2 * j] = sum.x;
-    acc[2 * j + 1] = sum.y;
-  }
-  return true;
 }
 
 // Columns of B lie in the ring in the order in which the promotion warps' lanes
@@ -587,8 +562,11 @@ __device__ __forceinline__ void promote_role(const Params& p, const Segments& s,
     const Unit g = unit_at(p, s, same);
     if (u + npairs < units) begin(u + npairs);   // on their way during the stores
     const int row0 = g.m0 + (int)(rank * CM + quarter * 32), col0 = g.n0 + (int)right * 128;
-    if (row0 >= g.m_end && g.tail < 0) continue;
-    if (g.tail >= 0 && !join_parts(p, g, rank, w, lane, acc)) continue;
+    if (row0 >= g.m_end) continue;
+    if (g.tail >= 0) {
+      store_part(p, g, rank, w, lane, acc);
+      continue;
+    }
     const int64_t off = p.form == GEMM_F8_BY_INNER ? g.expert * p.c_batch : 0;
     if (p.type == GEMM_F8_F16)
       store_rows<__half, COLS>(p, static_cast<__half*>(p.C) + off, acc, stage, row0, g.m_end, col0, lane);
@@ -704,6 +682,82 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     ptx::tc_fence_after();
     ptx::tmem_dealloc_pair(tmem_base, TMEM_COLS);
   }
+}
+
+// The sums of cut tiles' parts, in their order, to C.  A CTA takes a warp's piece
+// (32 rows x 128 columns) of a tile.  Bound by latency and the cache: all parts'
+// loads are on their way together.
+constexpr int JOIN_THREADS = 256;
+
+template <typename T>
+__device__ __forceinline__ void store_joined(const Params& p, const float (&x)[32][132], int row0,
+                                             int col0) {
+  constexpr int V = 16 / sizeof(T), UNITS = 128 / V;
+  T* C = static_cast<T*>(p.C);
+#pragma unroll
+  for (int i = 0; i < 32 * UNITS / JOIN_THREADS; ++i) {
+    const int at = (int)threadIdx.x + i * JOIN_THREADS, r = at / UNITS, c = at % UNITS * V;
+    const int row = row0 + r, col = col0 + c;
+    if (row >= p.M || col >= p.N) continue;
+    T* to = C + (int64_t)row * p.ldc + col;
+    alignas(16) T y[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      if constexpr (sizeof(T) == 4) y[k] = p.accumulate && col + k < p.N ? to[k] + x[r][c + k] : x[r][c + k];
+      else y[k] = to_type<T>(x[r][c + k]);
+    }
+    if (p.vec && col + V <= p.N) {
+      *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(y);
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+        if (col + k < p.N) to[k] = y[k];
+    }
+  }
+}
+
+template <bool COLS>
+__global__ void __launch_bounds__(JOIN_THREADS) f8_join_kernel(const __grid_constant__ Params p) {
+  __shared__ __align__(16) float x[32][132];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int tail = (int)blockIdx.x / (2 * PROMOTE_WARPS), piece = (int)blockIdx.x % (2 * PROMOTE_WARPS);
+  const int rank = piece / PROMOTE_WARPS, w = piece % PROMOTE_WARPS;
+  int tm, tn;
+  band_tile(p.full_units + tail, p.tiles_m, p.tiles_n, &tm, &tn);
+  const int row0 = tm * PM + rank * CM + (w & 3) * 32, col0 = tn * PN + (w >> 2) * 128;
+  if (row0 >= p.M || col0 >= p.N) return;
+  const float4* base = reinterpret_cast<const float4*>(p.ws) +
+                       (int64_t)tail * p.parts * (PART_FLOATS / 4) + piece * 32 * 32;
+#pragma unroll
+  for (int u = 0; u < 1024 / JOIN_THREADS; ++u) {
+    const int at = (int)threadIdx.x + u * JOIN_THREADS, j = at >> 5, lane = at & 31;
+    float4 v[MAX_PARTS];
+#pragma unroll
+    for (int i = 0; i < MAX_PARTS; ++i)
+      if (i < p.parts) v[i] = __ldcg(base + i * (PART_FLOATS / 4) + at);
+    float4 sum = v[0];
+#pragma unroll
+    for (int i = 1; i < MAX_PARTS; ++i) {
+      if (i < p.parts) {
+        sum.x += v[i].x;
+        sum.y += v[i].y;
+        sum.z += v[i].z;
+        sum.w += v[i].w;
+      }
+    }
+    if constexpr (COLS) {      // two columns of two rows (see promote_role)
+      const int r = (lane >> 2) + 16 * (j & 1), c = 8 * (j >> 1) + 2 * (lane & 3);
+      *reinterpret_cast<float2*>(&x[r][c]) = make_float2(sum.x, sum.y);
+      *reinterpret_cast<float2*>(&x[r + 8][c]) = make_float2(sum.z, sum.w);
+    } else {
+      *reinterpret_cast<float4*>(&x[lane][4 * j]) = sum;
+    }
+  }
+  __syncthreads();
+  if (p.type == GEMM_F8_F16) store_joined<__half>(p, x, row0, col0);
+  else if (p.type == GEMM_F8_BF16) store_joined<__nv_bfloat16>(p, x, row0, col0);
+  else store_joined<float>(p, x, row0, col0);
 }
 
 }  // namespace large
