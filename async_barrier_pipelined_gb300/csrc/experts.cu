@@ -213,6 +213,7 @@ constexpr int ROW_THREADS = 256, ROW_WARPS = 8;
 // the tokens' rows for the other choices: 8192 tokens of 4096 16-bit numbers to
 // four experts each, there 75 -> 70 us (169 -> 138 MB read of the memory).
 constexpr int64_t CACHE_BYTES = 48 << 20;
+constexpr int COMBINE_LOADS = 8;
 
 struct RowParams {
   int64_t rows;             // of the output
@@ -271,13 +272,14 @@ __global__ void __launch_bounds__(ROW_THREADS) experts_gather_kernel(const RowPa
 }
 
 // A warp takes a piece of a token, UNITS units a lane, and adds its choices in
-// their order, four of them on their way at a time: 89 -> 71 us for 8192 tokens
-// of 4096 numbers from four rows each, against a unit a thread.
-template <typename T, typename W, int V, int UNITS>
+// their order, AT_ONCE of them on their way at a time, eight loads a lane in all:
+// 89 -> 71 us for 8192 tokens of 4096 numbers from four rows each, against a unit
+// a thread.
+template <typename T, typename W, int V, int AT_ONCE>
 __global__ void __launch_bounds__(ROW_THREADS) experts_combine_kernel(const RowParams p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  constexpr int AT_ONCE = 4;
+  constexpr int UNITS = COMBINE_LOADS / AT_ONCE;
   const int lane = threadIdx.x & 31;
   const int units = p.cols / V, pieces = (units + 32 * UNITS - 1) / (32 * UNITS);
   const int64_t work = p.rows * pieces, step = (int64_t)gridDim.x * ROW_WARPS;
@@ -398,15 +400,13 @@ __global__ void __launch_bounds__(ROW_THREADS) experts_combine_gradient_kernel(c
 
 using RowKernel = void (*)(const RowParams);
 
-// Units of a token that a lane of the combination takes.
-constexpr int COMBINE_UNITS = 2;
-
-enum Which { COMBINE, GRADIENT };
+enum Which { COMBINE, COMBINE_FEW, GRADIENT };   // FEW: up to two choices
 
 template <typename T, typename W, int V>
 RowKernel pick_row(Which which) {
-  return which == COMBINE ? experts_combine_kernel<T, W, V, COMBINE_UNITS>
-                          : experts_combine_gradient_kernel<T, W, V>;
+  return which == COMBINE       ? experts_combine_kernel<T, W, V, 4>
+         : which == COMBINE_FEW ? experts_combine_kernel<T, W, V, 2>
+                                : experts_combine_gradient_kernel<T, W, V>;
 }
 template <typename T>
 RowKernel pick_row(Which which, bool f32_weights, bool vec) {
@@ -603,8 +603,9 @@ int experts_combine(gemm_f16_plan_t p, int type, int tokens, int choices, int co
   prm.Y = Y;
   prm.ldy = ldy;
   prm.status = p->status_dev;
-  const int64_t pieces = ceil_div(cols / (vec ? v : 1), 32 * COMBINE_UNITS);
-  return launch_rows(p, pick_row(COMBINE, type, weights_type == GEMM_F8_F32, vec),
+  const bool few = choices <= 2;
+  const int64_t pieces = ceil_div(cols / (vec ? v : 1), 32 * COMBINE_LOADS / (few ? 2 : 4));
+  return launch_rows(p, pick_row(few ? COMBINE_FEW : COMBINE, type, weights_type == GEMM_F8_F32, vec),
                      ceil_div(tokens * pieces, ROW_WARPS), (cudaStream_t)stream, prm,
                      "launch experts_combine_kernel");
 }

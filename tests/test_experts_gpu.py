@@ -367,3 +367,59 @@ def test_on_a_stream_of_its_own(g, plan):
     torch.cuda.synchronize()
     b = torch.autograd.grad(layer(g, plan, *leaves, 128)[0].float().square().sum(), leaves[0])[0]
     assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("m", [40, 300])
+def test_linear_of_transposed_views(g, plan, m):
+    """X and W as views of their transposes: the same bits, gradients too."""
+    x = torch.randn(m, 200, generator=gen(21), device="cuda").to(BF16)
+    w = torch.randn(130, 200, generator=gen(22), device="cuda").to(BF16)
+    dy = torch.randn(m, 130, generator=gen(23), device="cuda").to(BF16)
+
+    def run(x, w):
+        x, w = x.detach().requires_grad_(), w.detach().requires_grad_()
+        y = g.linear_f8(plan, x, w)
+        return (y, *torch.autograd.grad(y, (x, w), dy))
+
+    want = run(x, w)
+    turned = lambda t: t.t().contiguous().t()
+    for a, b in ((turned(x), w), (x, turned(w)), (turned(x), turned(w))):
+        got = run(a, b)
+        # another kernel may add a block's parts in another order
+        for c, d in zip(got, want):
+            assert c.shape == d.shape
+        for c, (p, q) in zip(got, linear_grads(x, w, dy)):
+            ref.check_product(c.detach(), p, q)
+
+
+def test_no_tokens(g, plan):
+    """Nothing to do forward; the gradients of weights are 0."""
+    x = torch.zeros(0, 136, dtype=BF16, device="cuda", requires_grad=True)
+    w = torch.randn(200, 136, device="cuda").to(BF16).requires_grad_()
+    y = g.linear_f8(plan, x, w)
+    dx, dw = torch.autograd.grad(y, (x, w), torch.zeros_like(y))
+    assert y.shape == (0, 200) and dx.shape == (0, 136) and (dw == 0).all()
+    _, _, _, up, down = layer_inputs(1)
+    up.requires_grad_(), down.requires_grad_()
+    picks = torch.zeros(0, 2, dtype=torch.int32, device="cuda")
+    wt = torch.zeros(0, 2, device="cuda", requires_grad=True)
+    y = layer(g, plan, x, picks, wt, up, down, 128)[0]
+    got = torch.autograd.grad(y, (x, wt, up, down), torch.zeros_like(y))
+    assert y.shape == (0, 136) and all((t == 0).all() for t in got)
+    assert plan.status() == g.OK
+
+
+@pytest.mark.parametrize("m,n,k", [(129, 300, 4100), (1000, 1024, 8192), (300, 2049, 2600)])
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+def test_products_of_cut_tiles(g, plan, m, n, k, dtype):
+    """Few tiles and many blocks: every kind of result, from parts joined after."""
+    a = torch.randn(m, k, generator=gen(31), device="cuda") * k ** -0.5
+    b = torch.randn(n, k, generator=gen(32), device="cuda")
+    A = g.quantize(plan, a)
+    for B in (g.quantize(plan, b, "tiles").t(), g.quantize(plan, b, "rows").t()):
+        room = torch.full((m + 2, n + 24), 7.0, dtype=dtype, device="cuda")
+        c = room[1:-1, 8:n + 8]
+        g.matmul_f8(plan, A, B, c)
+        ref.check_product(c, ref.values(A), ref.values(B))
+        c.fill_(7.0)
+        assert (room == 7.0).all()
