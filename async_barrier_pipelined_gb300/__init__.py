@@ -1061,6 +1061,9 @@ def linear_f8(plan: Plan, X, W, starts=None, dtype=None, grad_dtype=None, stream
     W's gradient the starts are multiples of 128 (expert_maps with align=128)
     and rows that no expert has are 0, as expert_gather leaves them.  ``plan``
     must last until the backward pass, which runs on the stream of the call.
+    To capture a backward pass into a CUDA graph, take it with torch.autograd.grad:
+    a leaf whose ``grad`` is accumulated stays tied, by torch, to the stream of an
+    earlier graph of it that is still alive.
     """
     W, codes, scales = (None, *W) if isinstance(W, Blocks) else (W, None, None)
     with _on_stream(plan, stream):

@@ -214,6 +214,7 @@ __device__ __forceinline__ void promote_role(const Params& p, const Segments& s,
       }
       const bool got = wait_phase(b.tfull + 8 * half, (done >> 1) & 1u, p, abort_flag);
       if (!__all_sync(0xffffffffu, got)) return;
+      __syncwarp();     // the warp's scales are in shared memory
       ptx::tc_fence_after();
       const uint64_t sb2 = ptx::pack_f2(sb, sb);
 #pragma unroll

@@ -497,6 +497,9 @@ Tensor linear_f8(const py::object& plan, int device, const Tensor& x_, const Ten
   if (starts && x_.dim() != 2) refuse("X must be [rows, K] where starts are given");
   const Tensor& W = w.defined() ? w : codes;
   if (W.dim() != (starts ? 3 : 2)) refuse("W must be [N, K], or [experts, N, K] with starts");
+  if (!w.defined() && (scales.dim() != W.dim() || scales.size(-2) != blocks_of(W.size(-2)) ||
+                       scales.size(-1) != blocks_of(W.size(-1))))
+    refuse("W's blocks must be tiles");
   const Tensor x = x_.dim() == 2 ? x_ : x_.reshape({x_.numel() / std::max<int64_t>(x_.size(-1), 1), x_.size(-1)});
   const LinearCall call = {c10::make_intrusive<PlanRef>(plan, device), codes, scales, starts,
                            {format, grad_format}, wants(x), wants(w)};

@@ -195,6 +195,8 @@ def test_tensors_elsewhere_and_of_other_types_are_refused(torch):
         g.linear_f8(PLAN, x, x[None])
     with pytest.raises(ValueError):
         g.linear_f8(PLAN, x[None], x[None], starts=torch.zeros(2, dtype=torch.int32))
+    with pytest.raises(ValueError, match="tiles"):
+        g.linear_f8(PLAN, x, b._replace(scales=torch.ones(4, 1)))
     picks = torch.zeros(4, 2, dtype=torch.int32)
     with pytest.raises(ValueError):
         g.expert_maps(PLAN, picks, 4)
