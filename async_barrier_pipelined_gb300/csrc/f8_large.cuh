@@ -641,13 +641,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     ptx::tmem_relinquish_pair();
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (p.form != GEMM_F8_DENSE) load_segments(p, seg, PM, NUM_THREADS);
   ptx::tc_fence_before();
   __syncthreads();
   ptx::cluster_sync();  // the peer's barriers exist before anyone signals them
   ptx::tc_fence_after();
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEM_SLOT);
+  // All of this beside the end of the kernel before; its results from here on.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (p.form != GEMM_F8_DENSE) {
+    load_segments(p, seg, PM, NUM_THREADS);
+    __syncthreads();
+  }
 
   uint32_t issued = 0;
   if (warp >= PROMOTE_WARP0) {

@@ -350,13 +350,17 @@ __global__ void __launch_bounds__(NUM_THREADS, Cfg<NT>::CTAS)
     ptx::tmem_relinquish();
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (p.form != GEMM_F8_DENSE) load_segments(p, seg, NT, NUM_THREADS);
   ptx::tc_fence_before();
   __syncthreads();
   if (split > 1) ptx::cluster_sync();   // the others' barriers exist
   ptx::tc_fence_after();
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(smem + C::OFF_TMEM_SLOT);
+  // All of this beside the end of the kernel before; its results from here on.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (p.form != GEMM_F8_DENSE) {
+    load_segments(p, seg, NT, NUM_THREADS);
+    __syncthreads();
+  }
 
   uint32_t issued = 0;
   if (warp == 0) {
