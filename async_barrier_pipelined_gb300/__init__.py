@@ -1025,8 +1025,9 @@ def matmul_f8(plan: Plan, A, B, C=None, dtype=None, starts=None, accumulate: boo
     With ``starts`` (int32 [experts + 1], from expert_maps) the product is by
     expert.  B [experts, K, N]: rows starts[e] to starts[e + 1] - 1 of A times
     B[e], and rows past the last expert's are 0.  B [K, N]: C [experts, M, N],
-    each of A's columns and B's rows starts[e] to starts[e + 1] - 1 (starts are
-    multiples of 128), 0 where there are none: the gradient of weights.
+    each of A's columns and B's rows starts[e] to starts[e + 1] - 1, 0 where
+    there are none: the gradient of weights.  Here starts are multiples of 128;
+    C is NaN for an expert whose starts are not, and plan.status() tells.
     Forward only: C carries no gradient (linear_f8 does).
     """
     return _result((_calls or _torch_calls()).matmul_f8(

@@ -110,10 +110,11 @@ __device__ __forceinline__ void report_bad_index(const Params& p) {
   *(volatile int*)p.status = (int)GEMM_F16_ERR_BAD_INDEX;
 }
 
-// The experts' segments in shared memory: lo[e], first row of expert e (0 rows
-// where its starts are bad); tiles[e], the tiles of `rows` rows of the experts
-// before it (BY_ROWS), tiles[experts] of all.  Called by the whole CTA, which
-// synchronises afterwards; the scan is warp 0's.
+// The experts' segments in shared memory: lo[e], first row of expert e; len[e],
+// its rows, or -1 where its starts are bad (no tiles and no K blocks then);
+// tiles[e], the tiles of `rows` rows of the experts before it (BY_ROWS),
+// tiles[experts] of all.  Called by the whole CTA, which synchronises
+// afterwards; the scan is warp 0's.
 struct Segments {
   int* lo;       // [MAX_EXPERTS]
   int* len;      // [MAX_EXPERTS]
@@ -136,7 +137,7 @@ __device__ __forceinline__ void load_segments(const Params& p, const Segments& s
       bad = bad || (lo & (BLOCK - 1)) || ((hi & (BLOCK - 1)) && hi != room);
     if (bad) report_bad_index(p);
     s.lo[e] = bad ? 0 : lo;
-    s.len[e] = bad ? 0 : hi - lo;
+    s.len[e] = bad ? -1 : hi - lo;
   }
   __syncthreads();
   if (threadIdx.x < 32) {
@@ -170,23 +171,44 @@ __device__ __forceinline__ int expert_of_tile(const Segments& s, int experts, in
   return lo;
 }
 
-// Rows of C past the last expert's are 0 (BY_ROWS): warp `w` of `warps`.
-__device__ __forceinline__ void zero_rest(const Params& p, int w, int warps, uint32_t lane) {
-  if (p.form != GEMM_F8_BY_ROWS || p.accumulate) return;
-  const int size = p.type == GEMM_F8_F32 ? 4 : 2;
-  const int end = max(0, p.starts[p.experts]);
-  for (int64_t r = (int64_t)end + w; r < p.M; r += warps) {
-    uint8_t* row = static_cast<uint8_t*>(p.C) + r * p.ldc * size;
-    const int64_t bytes = (int64_t)p.N * size;
-    int64_t at = 0;
-    if (p.vec) {
-      for (int64_t i = (int64_t)lane * 16; i + 16 <= bytes; i += 512)
-        *reinterpret_cast<uint4*>(row + i) = make_uint4(0, 0, 0, 0);
-      at = bytes & ~(int64_t)15;
-    }
-    for (int64_t i = at + (int64_t)lane * 2; i < bytes; i += 64)
-      *reinterpret_cast<uint16_t*>(row + i) = 0;
+// A row of C, by a warp: every 16 bits those of `bits`.
+__device__ __forceinline__ void fill_row(uint8_t* row, int64_t bytes, uint32_t bits, bool vec,
+                                         uint32_t lane) {
+  int64_t at = 0;
+  if (vec) {
+    for (int64_t i = (int64_t)lane * 16; i + 16 <= bytes; i += 512)
+      *reinterpret_cast<uint4*>(row + i) = make_uint4(bits, bits, bits, bits);
+    at = bytes & ~(int64_t)15;
   }
+  for (int64_t i = at + (int64_t)lane * 2; i < bytes; i += 64)
+    *reinterpret_cast<uint16_t*>(row + i) = (uint16_t)bits;
+}
+
+// What no tile stores, by warp `w` of `warps`.  BY_ROWS: rows of C past the last
+// expert's are 0.  BY_INNER: the matrix of an expert whose starts are bad is NaN,
+// for zeros would pass for a gradient.
+__device__ __forceinline__ void fill_rest(const Params& p, const Segments& s, int w, int warps,
+                                          uint32_t lane) {
+  if (p.form == GEMM_F8_DENSE) return;
+  const int size = p.type == GEMM_F8_F32 ? 4 : 2;
+  const int64_t bytes = (int64_t)p.N * size;
+  uint8_t* C = static_cast<uint8_t*>(p.C);
+  if (p.form == GEMM_F8_BY_INNER) {
+    for (int e0 = 0; e0 < p.experts; e0 += 32) {
+      const int mine = e0 + (int)lane;
+      for (uint32_t bad = __ballot_sync(0xffffffffu, mine < p.experts && s.len[mine] < 0); bad != 0;
+           bad &= bad - 1) {
+        const int64_t e = e0 + __ffs(bad) - 1;
+        for (int64_t r = w; r < p.M; r += warps)
+          fill_row(C + (e * p.c_batch + r * p.ldc) * size, bytes, 0xffffffffu, p.vec, lane);
+      }
+    }
+    return;
+  }
+  if (p.accumulate) return;
+  const int end = max(0, p.starts[p.experts]);
+  for (int64_t r = (int64_t)end + w; r < p.M; r += warps)
+    fill_row(C + r * p.ldc * size, bytes, 0, p.vec, lane);
 }
 
 template <typename T>

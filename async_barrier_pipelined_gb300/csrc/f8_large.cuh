@@ -132,7 +132,9 @@ __device__ __forceinline__ Unit unit_at(const Params& p, const Segments& s, int 
     g.expert = u / per;
     g.k0 = s.lo[g.expert];
     g.blk0 = g.k0 / BLOCK;
-    g.nkb = (s.len[g.expert] + BLOCK - 1) / BLOCK;
+    const int len = s.len[g.expert];
+    g.nkb = (len + BLOCK - 1) / BLOCK;
+    if (len < 0) g.m_end = 0;     // no rows to store: fill_rest's
     band_tile(u - g.expert * per, p.tiles_m, p.tiles_n, &tm, &tn);
   } else {
     int t = u - p.cut_units;
@@ -658,7 +660,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(PROMOTE_REGS));
     promote_role<COLS>(p, seg, base, tmem_base, rank, pair, npairs, b, warp, lane, abort_flag);
     __syncwarp();
-    zero_rest(p, (int)blockIdx.x * PROMOTE_WARPS + (int)warp - PROMOTE_WARP0,
+    fill_rest(p, seg, (int)blockIdx.x * PROMOTE_WARPS + (int)warp - PROMOTE_WARP0,
               (int)gridDim.x * PROMOTE_WARPS, lane);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(IO_REGS));

@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(NUM_THREADS, Cfg<NT>::CTAS)
     promote_role<NT>(p, seg, base, tmem_base, rank, split, kb0, kb1, cluster, clusters, b, warp,
                      lane, abort_flag);
     __syncwarp();
-    zero_rest(p, (int)blockIdx.x * PROMOTE_WARPS + (int)warp - PROMOTE_WARP0,
+    fill_rest(p, seg, (int)blockIdx.x * PROMOTE_WARPS + (int)warp - PROMOTE_WARP0,
               (int)gridDim.x * PROMOTE_WARPS, lane);
   }
   ptx::tc_fence_before();

@@ -119,8 +119,9 @@ enum {
  *               starts[0] are not written.  BY_INNER: K is the room.
  *   experts     1 .. 1024 for the forms by expert, with starts[experts + 1]
  *               on the device; starts that decrease, pass the room or, BY_INNER,
- *               are no multiples of 128 are reported (GEMM_F16_ERR_BAD_INDEX)
- *               and leave that expert's rows (its matrix) unspecified.
+ *               are no multiples of 128 (the end of the room may be none) are
+ *               reported (GEMM_F16_ERR_BAD_INDEX).  They leave that expert's
+ *               rows unspecified (BY_ROWS) or make its matrix NaN (BY_INNER).
  *   C           row-major, of `type`, rows ldc apart, matrices c_batch apart;
  *               its type's alignment (faster on 16-byte rows).  Must not
  *               overlap the operands.

@@ -1,0 +1,60 @@
+"""8-bit products, linear layers and experts' rows on the GPU where a call is at
+the edge of what it takes: bad starts, mistakes that must not pass for results."""
+from __future__ import annotations
+
+import pytest
+
+torch = pytest.importorskip("torch")
+from tests import f8_ref as ref  # noqa: E402
+from tests.test_f8_gpu import E4, BF16, F16, F32, g, gen, operands, plan, rand  # noqa: E402, F401
+
+pytestmark = pytest.mark.gpu
+
+
+def i32(*v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+# ------------------------------------------------------------------ bad starts
+
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("starts,bad", [
+    ([0, 128, 200, 512, 640, 700], [1, 2]), ([0, 100, 100, 256, 384, 700], [0, 1, 2]),
+    ([0, 128, 0, 256, 512, 700], [1]), ([0, 128, 256, 384, 512, 640], []),
+    ([-128, 128, 256, 384, 512, 768], [0, 4])])
+def test_the_matrix_of_an_expert_with_bad_inner_starts_is_nan(g, plan, starts, bad, dtype):
+    """And the others' are right: an end inside a block spoils both its experts."""
+    m, n, room = 300, 140, 700
+    for turned in (False, True):
+        x, y = rand(1, room, m) * 1e-3, rand(2, room, n) * 1e-3
+        A = g.quantize(plan, x, "columns").t()
+        B = g.quantize(plan, y, "tiles" if turned else "columns")
+        a, b = ref.values(A, "rows"), ref.values(B, "tiles" if turned else "columns")
+        A = A._replace(scales=(A.scales / (a.abs() @ b.abs()).max() * 1e3).float())
+        a = ref.values(A, "rows")
+        c = g.matmul_f8(plan, A, B, dtype=dtype, starts=i32(*starts))
+        torch.cuda.synchronize()
+        assert plan.status() == (g.ERR_BAD_INDEX if bad else g.OK) and plan.status() == g.OK
+        for e, (lo, hi) in enumerate(zip(starts, starts[1:])):
+            if e in bad:
+                assert c[e].isnan().all()
+            else:
+                ref.check_product(c[e], a[:, lo:hi], b[lo:hi])
+    old = torch.ones(len(starts) - 1, m, n, device="cuda")
+    g.matmul_f8(plan, A, B, old, starts=i32(*starts), accumulate=True)
+    torch.cuda.synchronize()
+    assert plan.status() == (g.ERR_BAD_INDEX if bad else g.OK) and plan.status() == g.OK
+    assert old.isnan().flatten(1).all(1).nonzero().flatten().tolist() == bad
+    assert old.isnan().flatten(1).any(1).nonzero().flatten().tolist() == bad
+
+
+def test_weights_of_experts_with_rows_out_of_step_have_no_gradient_of_zeros(g, plan):
+    """Starts as they come from expert_maps without align=128."""
+    x = torch.randn(50, 136, generator=gen(3), device="cuda")
+    w = torch.randn(4, 64, 136, generator=gen(4), device="cuda", requires_grad=True)
+    m = g.expert_maps(plan, torch.arange(100, device="cuda").view(50, 2) % 4, 4)
+    y = g.linear_f8(plan, g.expert_gather(plan, x, m), w, starts=m.starts)
+    dw, = torch.autograd.grad(y.sum(), w)
+    torch.cuda.synchronize()
+    assert dw.isnan().all()
+    assert plan.status() == g.ERR_BAD_INDEX and plan.status() == g.OK
