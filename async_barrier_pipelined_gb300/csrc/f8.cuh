@@ -127,6 +127,32 @@ __device__ __forceinline__ Segments segments_at(void* smem) {
   return Segments{i, i + MAX_EXPERTS, i + 2 * MAX_EXPERTS};
 }
 
+// Where starts decrease, segments may hold the same rows, which two experts
+// would then store in a race: those that begin before the end of an earlier
+// one are bad too.  Warp 0's; experts e0 .. e1 - 1 are this lane's.  Returns
+// their tiles.
+__device__ __noinline__ int drop_overlaps(const Segments s, int e0, int e1, int rows) {
+  int before = 0;
+  for (int e = e0; e < e1; ++e)
+    if (s.len[e] >= 0) before = max(before, s.lo[e] + s.len[e]);
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const int up = __shfl_up_sync(0xffffffffu, before, d);
+    if ((int)threadIdx.x >= d) before = max(before, up);
+  }
+  before = __shfl_up_sync(0xffffffffu, before, 1);
+  if (threadIdx.x == 0) before = 0;
+  int tiles = 0;
+  for (int e = e0; e < e1; ++e) {
+    if (s.len[e] < 0) continue;
+    const int lo = s.lo[e], end = lo + s.len[e];
+    if (lo < before) s.len[e] = -1;
+    else tiles += (s.len[e] + rows - 1) / rows;
+    before = max(before, end);
+  }
+  return tiles;
+}
+
 __device__ __forceinline__ void load_segments(const Params& p, const Segments& s, int rows,
                                               int threads) {
   const int room = p.form == GEMM_F8_BY_INNER ? p.K : p.M;
@@ -143,7 +169,14 @@ __device__ __forceinline__ void load_segments(const Params& p, const Segments& s
   if (threadIdx.x < 32) {
     const int per = (p.experts + 31) / 32, e0 = (int)threadIdx.x * per;
     int sum = 0;
-    for (int e = e0; e < min(e0 + per, p.experts); ++e) sum += (s.len[e] + rows - 1) / rows;
+    bool bad = false;
+    for (int e = e0; e < min(e0 + per, p.experts); ++e) {
+      sum += (s.len[e] + rows - 1) / rows;      // 0 for -1
+      bad = bad || s.len[e] < 0;
+    }
+    // Starts that never decrease make segments without common rows.
+    if (__any_sync(0xffffffffu, bad) && p.form == GEMM_F8_BY_ROWS)
+      sum = drop_overlaps(s, e0, min(e0 + per, p.experts), rows);
     int before = sum;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
@@ -185,8 +218,9 @@ __device__ __forceinline__ void fill_row(uint8_t* row, int64_t bytes, uint32_t b
 }
 
 // What no tile stores, by warp `w` of `warps`.  BY_ROWS: rows of C past the last
-// expert's are 0.  BY_INNER: the matrix of an expert whose starts are bad is NaN,
-// for zeros would pass for a gradient.
+// expert's are 0 (by the segments that were found good: starts[experts] may be a
+// bad one, below rows that others store).  BY_INNER: the matrix of an expert
+// whose starts are bad is NaN, for zeros would pass for a gradient.
 __device__ __forceinline__ void fill_rest(const Params& p, const Segments& s, int w, int warps,
                                           uint32_t lane) {
   if (p.form == GEMM_F8_DENSE) return;
@@ -206,7 +240,10 @@ __device__ __forceinline__ void fill_rest(const Params& p, const Segments& s, in
     return;
   }
   if (p.accumulate) return;
-  const int end = max(0, p.starts[p.experts]);
+  int last = p.experts - 1;
+  while (last >= 0 && s.len[last] < 0) --last;
+  if (last < 0) return;
+  const int end = s.lo[last] + s.len[last];
   for (int64_t r = (int64_t)end + w; r < p.M; r += warps)
     fill_row(C + r * p.ldc * size, bytes, 0, p.vec, lane);
 }

@@ -120,8 +120,12 @@ enum {
  *   experts     1 .. 1024 for the forms by expert, with starts[experts + 1]
  *               on the device; starts that decrease, pass the room or, BY_INNER,
  *               are no multiples of 128 (the end of the room may be none) are
- *               reported (GEMM_F16_ERR_BAD_INDEX).  They leave that expert's
- *               rows unspecified (BY_ROWS) or make its matrix NaN (BY_INNER).
+ *               reported (GEMM_F16_ERR_BAD_INDEX).  They make that expert's
+ *               matrix NaN (BY_INNER) or leave its rows unspecified (BY_ROWS;
+ *               also those of an expert that begins before the end of an earlier
+ *               one).  The other experts' rows and matrices are right, and rows
+ *               past the last of them 0 (BY_ROWS; nothing is written where every
+ *               expert's starts are bad).
  *   C           row-major, of `type`, rows ldc apart, matrices c_batch apart;
  *               its type's alignment (faster on 16-byte rows).  Must not
  *               overlap the operands.

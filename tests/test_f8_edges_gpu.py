@@ -58,3 +58,43 @@ def test_weights_of_experts_with_rows_out_of_step_have_no_gradient_of_zeros(g, p
     torch.cuda.synchronize()
     assert dw.isnan().all()
     assert plan.status() == g.ERR_BAD_INDEX and plan.status() == g.OK
+
+
+@pytest.mark.parametrize("times", [1, 20])         # the kernels for few and for many rows
+@pytest.mark.parametrize("starts,good", [
+    ([0, 40, 20], [0]), ([0, 40, -1], [0]), ([0, 40, 20, 60], [0]), ([0, 20, 40, 61], [0, 1]),
+    ([-1, 20, 40, 60], [1, 2]), ([0, 30, 10, 30, 50], [0, 3]), ([0, 61, 5, 25, 60], [2, 3]),
+    ([10, 30, 20, 25, 20, 40], [0]), ([70, 65, 3], []), ([5, 5, 3, 5, 60], [0, 3])])
+def test_bad_starts_leave_the_other_experts_rows(g, plan, starts, good, times):
+    """Rows of each expert whose starts are good, also where the last start is a
+    bad one, or another expert's range would hold the same rows; 0 behind them."""
+    room, experts = 60 * times, len(starts) - 1
+    starts = [times * s for s in starts]
+    A = g.quantize(plan, rand(1, room, 300))
+    B = g.quantize(plan, rand(2, experts, 300, 200), "tiles")
+    a, b = ref.values(A), ref.values(B)
+    for _ in range(3):
+        c = torch.full((room, 200), 7.0, device="cuda")
+        g.matmul_f8(plan, A, B, c, starts=i32(*starts))
+        torch.cuda.synchronize()
+        assert plan.status() == g.ERR_BAD_INDEX and plan.status() == g.OK
+        for e in good:
+            lo, hi = starts[e:e + 2]
+            ref.check_product(c[lo:hi], a[lo:hi], b[e])
+        if good:
+            assert (c[max(starts[e + 1] for e in good):] == 0).all()
+        else:
+            assert (c == 7.0).all()
+
+
+def test_many_experts_whose_ranges_overlap(g, plan):
+    """Every other range is all rows: the first of them is stored, once."""
+    starts = [0, 500] * 200
+    A = g.quantize(plan, rand(1, 500, 128))
+    w = rand(2, len(starts) - 1, 128, 16)
+    B = g.quantize(plan, w, "tiles")
+    c = torch.full((500, 16), 7.0, device="cuda")
+    g.matmul_f8(plan, A, B, c, starts=i32(*starts))
+    torch.cuda.synchronize()
+    assert plan.status() == g.ERR_BAD_INDEX and plan.status() == g.OK
+    ref.check_product(c, ref.values(A), ref.values(B)[0])
