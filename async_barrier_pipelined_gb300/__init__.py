@@ -964,6 +964,12 @@ class Blocks(collections.namedtuple("Blocks", "data scales")):
         return Blocks(self.data.transpose(-1, -2), self.scales.transpose(-1, -2))
 
 
+class ExpertMaps(collections.namedtuple("ExpertMaps", "starts rows source")):
+    """The order of tokens' choices by expert (see expert_maps).  ``align``: what
+    each expert's rows are filled up to a multiple of (None: not known)."""
+    align = None
+
+
 _F8_BLOCKS = {"rows": F8_ROWS, "columns": F8_COLUMNS, "tiles": F8_TILES, "both": F8_BOTH}
 
 
@@ -1058,15 +1064,23 @@ def linear_f8(plan: Plan, X, W, starts=None, dtype=None, grad_dtype=None, stream
     ``dtype`` and ``grad_dtype`` are the formats of X and W and of that
     gradient (float8_e4m3fn if None).  X's gradient has X's type, W's W's.
 
-    With ``starts`` X is [rows, K], sorted by expert, and W [experts, N, K]; for
-    W's gradient the starts are multiples of 128 (expert_maps with align=128)
-    and rows that no expert has are 0, as expert_gather leaves them.  ``plan``
-    must last until the backward pass, which runs on the stream of the call.
+    With ``starts`` (an ExpertMaps, or its starts) X is [rows, K], sorted by
+    expert, and W [experts, N, K]; for W's gradient the starts are multiples of
+    128 (expert_maps with align=128) and rows that no expert has are 0, as
+    expert_gather leaves them.  An ExpertMaps of another align is refused where W
+    requires a gradient; with starts alone that gradient is NaN for each expert
+    whose starts are none (plan.status() tells too).  ``plan`` must last until the backward pass, which runs on the stream of the call.
     To capture a backward pass into a CUDA graph, take it with torch.autograd.grad:
     a leaf whose ``grad`` is accumulated stays tied, by torch, to the stream of an
     earlier graph of it that is still alive.
     """
     W, codes, scales = (None, *W) if isinstance(W, Blocks) else (W, None, None)
+    if isinstance(starts, ExpertMaps):
+        align, starts = starts.align, starts.starts
+        if align is not None and align % 128 and W is not None and W.requires_grad:
+            import torch
+            if torch.is_grad_enabled():
+                raise ValueError(f"W's gradient needs maps with align=128 (these have {align})")
     with _on_stream(plan, stream):
         return _result((_calls or _torch_calls()).linear_f8(
             plan, plan.device, X, W, codes, scales, starts, _f8_format(dtype),
@@ -1074,8 +1088,6 @@ def linear_f8(plan: Plan, X, W, starts=None, dtype=None, grad_dtype=None, stream
 
 
 # ---------------------------------------------------------------- experts
-ExpertMaps = collections.namedtuple("ExpertMaps", "starts rows source")
-ExpertMaps.__doc__ = """The order of tokens' choices by expert (see expert_maps)."""
 
 
 def expert_maps(plan: Plan, experts, num_experts: int, align: int = 1, stream=None) -> ExpertMaps:
@@ -1089,9 +1101,11 @@ def expert_maps(plan: Plan, experts, num_experts: int, align: int = 1, stream=No
     past the last expert.  There are as many rows as any router can need
     (experts_max_rows), so that a step's shapes do not depend on its tokens.
     """
-    return ExpertMaps._make(_result((_calls or _torch_calls()).expert_maps(
+    maps = ExpertMaps._make(_result((_calls or _torch_calls()).expert_maps(
         plan.handle, plan.device, experts, num_experts, align,
         stream if stream is None else _stream_handle(stream)), "experts_maps"))
+    maps.align = align
+    return maps
 
 
 def expert_gather(plan: Plan, X, maps: ExpertMaps, stream=None):

@@ -98,3 +98,23 @@ def test_many_experts_whose_ranges_overlap(g, plan):
     torch.cuda.synchronize()
     assert plan.status() == g.ERR_BAD_INDEX and plan.status() == g.OK
     ref.check_product(c, ref.values(A), ref.values(B)[0])
+
+
+def test_linear_of_maps_is_that_of_their_starts(g, plan):
+    x = torch.randn(50, 136, generator=gen(3), device="cuda").to(BF16)
+    w = torch.randn(4, 64, 136, generator=gen(4), device="cuda").to(BF16).requires_grad_()
+    picks = torch.arange(100, device="cuda").view(50, 2) % 4
+    m = g.expert_maps(plan, picks, 4, align=128)
+    assert m.align == 128
+    s = g.expert_gather(plan, x, m)
+    got, want = (g.linear_f8(plan, s, w, starts=t) for t in (m, m.starts))
+    assert torch.equal(got, want)
+    assert all(torch.equal(torch.autograd.grad(y.float().sum(), w)[0],
+                           torch.autograd.grad(want.float().sum(), w, retain_graph=True)[0])
+               for y in (got,))
+    m = g.expert_maps(plan, picks, 4)
+    assert m.align == 1
+    with pytest.raises(ValueError, match="align=128"):
+        g.linear_f8(plan, g.expert_gather(plan, x, m), w, starts=m)
+    assert g.linear_f8(plan, g.expert_gather(plan, x, m), w.detach(), starts=m).shape == (100, 64)
+    assert plan.status() == g.OK
