@@ -1063,6 +1063,8 @@ def linear_f8(plan: Plan, X, W, starts=None, dtype=None, grad_dtype=None, stream
     by rows for X's gradient and along the rows' dimension, like X, for W's;
     ``dtype`` and ``grad_dtype`` are the formats of X and W and of that
     gradient (float8_e4m3fn if None).  X's gradient has X's type, W's W's.
+    Forward-mode derivatives are refused (here, and in expert_gather and
+    expert_combine).
 
     With ``starts`` (an ExpertMaps, or its starts) X is [rows, K], sorted by
     expert, and W [experts, N, K]; for W's gradient the starts are multiples of

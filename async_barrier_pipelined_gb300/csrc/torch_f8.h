@@ -339,8 +339,20 @@ Keep kept(AutogradContext* ctx) {
   return c10::static_intrusive_pointer_cast<PlanRef>(ctx->saved_data["plan"].toCapsule());
 }
 
+// Forward-mode derivatives have no kernels.  torch refuses them where one of its
+// functions in C++ is applied, which is only where a gradient is wanted: without
+// this a tangent would be lost in silence everywhere else.
+void no_tangent(const Tensor& x) {
+  TORCH_CHECK_NOT_IMPLEMENTED(
+      !x.defined() || !x._fw_grad(0).defined(),
+      "8-bit products and experts' rows have no forward-mode derivatives");
+}
+
 // A gradient as the calls take it (it may be one number for all of a tensor).
-Tensor dense(const Tensor& x) { return x.contiguous(); }
+Tensor dense(const Tensor& x) {
+  no_tangent(x);
+  return x.contiguous();
+}
 
 // Gradients that have none of their own: an error where one is asked for.
 variable_list once(variable_list grads) {
@@ -479,11 +491,14 @@ bool wants(const Tensor& x) {
 }
 
 Tensor gather_call(const Keep& plan, const Tensor& x, const Tensor& rows, const Tensor& source) {
+  no_tangent(x);
   if (wants(x)) return Gather::apply(x, MapsCall{plan, rows, source});
   return expert_gather(plan->handle(), plan->device, x, rows, source);
 }
 Tensor combine_call(const Keep& plan, const Tensor& s, const Tensor& weights, const Tensor& rows,
                     const Tensor& source) {
+  no_tangent(s);
+  no_tangent(weights);
   if (wants(s) || wants(weights))
     return Combine::apply(s, weights.defined() ? c10::optional<Tensor>(weights) : c10::nullopt,
                           MapsCall{plan, rows, source});
@@ -500,6 +515,8 @@ Tensor linear_f8(const py::object& plan, int device, const Tensor& x_, const Ten
   if (!w.defined() && (scales.dim() != W.dim() || scales.size(-2) != blocks_of(W.size(-2)) ||
                        scales.size(-1) != blocks_of(W.size(-1))))
     refuse("W's blocks must be tiles");
+  no_tangent(x_);
+  no_tangent(w);
   const Tensor x = x_.dim() == 2 ? x_ : x_.reshape({x_.numel() / std::max<int64_t>(x_.size(-1), 1), x_.size(-1)});
   const LinearCall call = {c10::make_intrusive<PlanRef>(plan, device), codes, scales, starts,
                            {format, grad_format}, wants(x), wants(w)};

@@ -118,3 +118,20 @@ def test_linear_of_maps_is_that_of_their_starts(g, plan):
         g.linear_f8(plan, g.expert_gather(plan, x, m), w, starts=m)
     assert g.linear_f8(plan, g.expert_gather(plan, x, m), w.detach(), starts=m).shape == (100, 64)
     assert plan.status() == g.OK
+
+
+# ------------------------------------------------------------------ derivatives
+
+def test_a_tangent_of_a_gradient_is_refused(g, plan):
+    """Forward over reverse: the gradient that arrives carries a tangent."""
+    import torch.autograd.forward_ad as fwd
+    x = torch.randn(20, 64, device="cuda", requires_grad=True)
+    w = torch.randn(32, 64, device="cuda", requires_grad=True)
+    m = g.expert_maps(plan, torch.zeros(20, 2, dtype=torch.int32, device="cuda"), 2)
+    weights = torch.ones(20, 2, device="cuda", requires_grad=True)
+    s = g.expert_gather(plan, x, m)
+    for y, leaf in ((g.linear_f8(plan, x, w), x), (s, x), (g.expert_combine(plan, s, m), x),
+                    (g.expert_combine(plan, s.detach(), m, weights), weights)):
+        with fwd.dual_level(), pytest.raises(RuntimeError, match="forward-mode"):
+            dy = fwd.make_dual(torch.ones_like(y), torch.ones_like(y))
+            torch.autograd.grad(y, leaf, dy, retain_graph=True)

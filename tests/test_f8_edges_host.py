@@ -59,3 +59,26 @@ def test_maps_are_still_three_tensors(torch):
     starts, rows, source = m
     assert len(m) == 3 and m._fields == ("starts", "rows", "source") and m[0] is starts
     assert m._replace(rows=rows).align is None      # others' maps: not known
+
+
+# ------------------------------------------------------------------ forward mode
+
+@pytest.mark.parametrize("which", ["X", "W", "gather", "S", "weights"])
+@pytest.mark.parametrize("grad", [False, True])
+def test_forward_mode_derivatives_are_refused(torch, which, grad):
+    """Not dropped, whether or not a gradient is wanted as well."""
+    import torch.autograd.forward_ad as fwd
+    m = maps_of(torch, 128)
+    with fwd.dual_level():
+        def t(*shape, dual=False):
+            x = torch.ones(shape, requires_grad=grad)
+            return fwd.make_dual(x, torch.ones(shape)) if dual else x
+        calls = {"X": lambda: g.linear_f8(PLAN, t(3, 4, 32, dual=True), t(16, 32)),
+                 "W": lambda: g.linear_f8(PLAN, t(4, 32), t(16, 32, dual=True)),
+                 "gather": lambda: g.expert_gather(PLAN, t(4, 32, dual=True), m),
+                 "S": lambda: g.expert_combine(PLAN, t(8, 32, dual=True), m),
+                 "weights": lambda: g.expert_combine(PLAN, t(8, 32), m, t(4, 2, dual=True))}
+        with pytest.raises(NotImplementedError, match="forward-mode"):
+            calls[which]()
+        with fwd._set_fwd_grad_enabled(False), pytest.raises(ValueError, match="plan's device"):
+            calls[which]()       # switched off: the next refusal
