@@ -44,7 +44,7 @@ __all__ = [
     "rope_frequencies", "rope_turns", "rotary", "rotary_to_cache", "paged_attention",
     "EXPORTED_SYMBOLS_F8", "GemmF8Operand", "F8_E4M3", "F8_E5M2", "F8_DENSE", "F8_BY_ROWS",
     "F8_BY_INNER", "gemm_f8_quantize", "gemm_f8_quantize_validate", "gemm_f8_run",
-    "gemm_f8_workspace", "gemm_f8_validate", "experts_maps", "experts_maps_validate",
+    "gemm_f8_workspace", "gemm_f8_run_choice", "gemm_f8_validate", "experts_maps", "experts_maps_validate",
     "experts_max_rows", "experts_gather", "experts_gather_validate", "experts_combine",
     "experts_combine_validate", "experts_combine_gradient",
     "experts_combine_gradient_validate", "Blocks", "quantize", "matmul_f8", "linear_f8",
@@ -182,6 +182,7 @@ _SIGNATURES_F8 = {
     "gemm_f8_quantize_validate": (_c_int, _F8_QUANTIZE),
     "gemm_f8_run": (_c_int, [_vp, *_F8_RUN, _vp, ctypes.c_size_t, _vp]),
     "gemm_f8_workspace": (ctypes.c_size_t, [_vp] + [_c_int] * 6),
+    "gemm_f8_run_choice": (_c_int, [_c_int] * 9 + [ctypes.POINTER(_c_int)]),
     "gemm_f8_validate": (_c_int, _F8_RUN),
     "experts_maps": (_c_int, [_vp, *_EXPERTS_MAPS, _vp]),
     "experts_maps_validate": (_c_int, _EXPERTS_MAPS),
@@ -893,6 +894,16 @@ def gemm_f8_workspace(plan: int, form: int, M: int, N: int, K: int, experts: int
                       a_transposed: int = 0) -> int:
     """Bytes of workspace that gemm_f8_run needs for these sizes."""
     return load().gemm_f8_workspace(plan, form, M, N, K, experts, a_transposed)
+
+
+def gemm_f8_run_choice(form: int, M: int, N: int, K: int, experts: int = 1, a_transposed: int = 0,
+                       num_sms: int = 152, max_pairs: int = 76, sm_limit: int = 0) -> dict:
+    """What a gemm_f8_run of these sizes launches on a device with these facts
+    (host only; the defaults are a GB300's; see gemm_f8.h)."""
+    info = (_c_int * 4)()
+    _check(load().gemm_f8_run_choice(form, M, N, K, experts, a_transposed, num_sms, max_pairs,
+                                     sm_limit, info), "gemm_f8_run_choice")
+    return {"kernel": info[0], "parts": info[1], "ctas": info[2], "join_ctas": info[3]}
 
 
 def gemm_f8_validate(form, M, N, K, experts, starts, A, B, C, ldc, c_batch, type,

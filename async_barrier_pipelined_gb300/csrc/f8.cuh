@@ -58,6 +58,7 @@ struct Params {
   int kblocks;               // DENSE
   int units;                 // DENSE, BY_INNER; BY_ROWS knows them on the device
   int full_units, cut_units, parts;   // large kernel, DENSE: see there
+  int join_pieces;           // pieces of 32 rows x 128 columns of all cut tiles
   float* ws;
   int* status;
   unsigned long long timeout_ns;

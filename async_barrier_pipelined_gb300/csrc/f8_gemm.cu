@@ -45,8 +45,10 @@ struct Choice {
 int pairs_of(const gemm_f16_plan_s* p) {
   return p->sm_limit > 0 ? std::max(1, std::min(p->f8_pairs, p->sm_limit / 2)) : p->f8_pairs;
 }
-int sms_of(const gemm_f16_plan_s* p) {
-  return p->sm_limit > 0 ? std::min(p->sm_limit, p->num_sms) : p->num_sms;
+// CTAs of the small kernel at once.  Nothing places two of them on one SM, so
+// that with a limit there is one for each SM that may be used.
+int64_t small_room(const gemm_f16_plan_s* p, int ctas_per_sm) {
+  return p->sm_limit > 0 ? std::min(p->sm_limit, p->num_sms) : (int64_t)p->num_sms * ctas_per_sm;
 }
 
 Choice choose(const gemm_f16_plan_s* p, int form, int M, int N, int K, int experts,
@@ -69,7 +71,7 @@ Choice choose(const gemm_f16_plan_s* p, int form, int M, int N, int K, int exper
     const int64_t units = form == GEMM_F8_BY_ROWS
                               ? std::min<int64_t>(M, experts) * tiles_n
                               : ceil_div(M, c.nt) * tiles_n;
-    const int64_t room = (int64_t)sms_of(p) * small_kernel(c.nt).ctas;
+    const int64_t room = small_room(p, small_kernel(c.nt).ctas);
     c.split = 1;
     while (c.split < f8::small::MAX_SPLIT && 2 * c.split * units <= room && 4 * c.split <= kblocks)
       c.split *= 2;
@@ -92,6 +94,31 @@ Choice choose(const gemm_f16_plan_s* p, int form, int M, int N, int K, int exper
     }
   }
   return c;
+}
+
+// CTAs of a call's kernel and of the one that joins cut tiles (0: none).
+struct Grids {
+  int product, join;
+};
+Grids grids(const gemm_f16_plan_s* p, const Choice& c, int form, int M, int N, int experts) {
+  Grids g = {};
+  if (c.small) {
+    const int64_t tiles_n = ceil_div(N, f8::small::CN);
+    const int64_t most = form == GEMM_F8_BY_ROWS ? (ceil_div(M, c.nt) + std::min(M, experts)) * tiles_n
+                                                 : ceil_div(M, c.nt) * tiles_n;
+    const int64_t room = std::max<int64_t>(1, small_room(p, small_kernel(c.nt).ctas) / c.split);
+    g.product = (int)std::min(most, room) * c.split;
+    return g;
+  }
+  const int64_t tiles_n = ceil_div(N, f8::large::PN), tiles = ceil_div(M, f8::large::PM) * tiles_n;
+  const int64_t most = form == GEMM_F8_BY_ROWS
+                           ? (ceil_div(M, f8::large::PM) + std::min(M, experts)) * tiles_n
+                       : form == GEMM_F8_BY_INNER ? tiles * experts
+                                                  : tiles + (int64_t)c.tail_tiles * (c.parts - 1);
+  g.product = 2 * (int)std::min<int64_t>(most, pairs_of(p));
+  g.join = c.tail_tiles * 2 * f8::large::PROMOTE_WARPS;
+  if (p->sm_limit > 0) g.join = std::min(g.join, p->sm_limit);
+  return g;
 }
 
 size_t workspace_bytes(const Choice& c) {
@@ -247,6 +274,25 @@ size_t gemm_f8_workspace(gemm_f16_plan_t p, int form, int M, int N, int K, int e
   return workspace_bytes(choose(p, form, M, N, K, experts, a_transposed != 0));
 }
 
+int gemm_f8_run_choice(int form, int M, int N, int K, int experts, int a_transposed, int num_sms,
+                       int max_pairs, int sm_limit, int info[4]) {
+  if (!info || form < GEMM_F8_DENSE || form > GEMM_F8_BY_INNER || M < 1 || N < 1 || K < 1 ||
+      M > MAX_SIZE || N > MAX_SIZE || K > MAX_SIZE || num_sms < 1 || max_pairs < 1 || sm_limit < 0 ||
+      (form != GEMM_F8_DENSE && (experts < 1 || experts > f8::MAX_EXPERTS)))
+    return GEMM_F16_ERR_INVALID_ARG;
+  gemm_f16_plan_s p;
+  p.num_sms = num_sms;
+  p.f8_pairs = max_pairs;
+  p.sm_limit = sm_limit;
+  const Choice c = choose(&p, form, M, N, K, experts, a_transposed != 0);
+  const Grids g = grids(&p, c, form, M, N, experts);
+  info[0] = c.small ? 1 : 2;
+  info[1] = c.small ? c.split : c.parts;
+  info[2] = g.product;
+  info[3] = g.join;
+  return GEMM_F16_OK;
+}
+
 int gemm_f8_run(gemm_f16_plan_t p, int form, int M, int N, int K, int experts,
                 const int32_t* starts, const gemm_f8_operand* A, const gemm_f8_operand* B, void* C,
                 int64_t ldc, int64_t c_batch, int type, int accumulate, void* workspace,
@@ -304,6 +350,7 @@ int gemm_f8_run(gemm_f16_plan_t p, int form, int M, int N, int K, int experts,
   prm.timeout_ns = p->timeout_ns;
   prm.fault_unit = p->fault_unit;
   const int b_matrices = form == GEMM_F8_BY_ROWS ? experts : 1;
+  const Grids grid = grids(p, c, form, M, N, experts);
   CUtensorMap tmA, tmB;
   if (c.small) {
     using namespace f8::small;
@@ -316,12 +363,7 @@ int gemm_f8_run(gemm_f16_plan_t p, int form, int M, int N, int K, int experts,
     prm.units = prm.tiles_m * prm.tiles_n;
     // The MMA's rows are B's: formats and majors change places.
     prm.idesc = f8::idesc_f8(B->format, A->format, prm.b_mn, false, CN, c.nt);
-    const int64_t most = form == GEMM_F8_BY_ROWS
-                             ? (ceil_div(M, c.nt) + std::min(M, experts)) * (int64_t)prm.tiles_n
-                             : prm.units;
-    const int64_t room = std::max<int64_t>(1, (int64_t)sms_of(p) * k.ctas / c.split);
-    const int clusters = (int)std::min(most, room);
-    return launch(p, k.fn, "launch f8_small_kernel", clusters * c.split, c.split, NUM_THREADS,
+    return launch(p, k.fn, "launch f8_small_kernel", grid.product, c.split, NUM_THREADS,
                   by ? k.smem_experts : k.smem, st, tmA, tmB, prm);
   }
   using namespace f8::large;
@@ -337,15 +379,12 @@ int gemm_f8_run(gemm_f16_plan_t p, int form, int M, int N, int K, int experts,
                                        : prm.full_units + c.tail_tiles * c.parts;
   prm.cut_units = c.tail_tiles * c.parts;
   prm.ws = static_cast<float*>(workspace);
-  const int64_t most = form == GEMM_F8_BY_ROWS
-                           ? (ceil_div(M, PM) + std::min(M, experts)) * (int64_t)prm.tiles_n
-                           : prm.units;
-  const int pairs = (int)std::min<int64_t>(most, pairs_of(p));
   rc = launch(p, prm.sb_shift ? f8_large_kernel<false> : f8_large_kernel<true>,
-              "launch f8_large_kernel", 2 * pairs, 0, NUM_THREADS, SMEM_BYTES, st, tmA, tmB, prm);
+              "launch f8_large_kernel", grid.product, 0, NUM_THREADS, SMEM_BYTES, st, tmA, tmB, prm);
   if (rc || c.tail_tiles == 0) return rc;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)c.tail_tiles * 2 * PROMOTE_WARPS, 1, 1);
+  cfg.gridDim = dim3((unsigned)grid.join, 1, 1);
+  prm.join_pieces = c.tail_tiles * 2 * PROMOTE_WARPS;
   cfg.blockDim = dim3(JOIN_THREADS, 1, 1);
   cfg.stream = st;
   cudaLaunchAttribute pdl;

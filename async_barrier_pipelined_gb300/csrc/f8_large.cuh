@@ -691,8 +691,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
 }
 
 // The sums of cut tiles' parts, in their order, to C.  A CTA takes a warp's piece
-// (32 rows x 128 columns) of a tile.  Bound by latency and the cache: all parts'
-// loads are on their way together.
+// (32 rows x 128 columns) of a tile at a time; there are as many CTAs as pieces
+// unless fewer SMs may be used.  Bound by latency and the cache: all parts' loads
+// are on their way together.
 constexpr int JOIN_THREADS = 256;
 
 template <typename T>
@@ -727,43 +728,46 @@ __global__ void __launch_bounds__(JOIN_THREADS) f8_join_kernel(const __grid_cons
   __shared__ __align__(16) float x[32][132];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int tail = (int)blockIdx.x / (2 * PROMOTE_WARPS), piece = (int)blockIdx.x % (2 * PROMOTE_WARPS);
-  const int rank = piece / PROMOTE_WARPS, w = piece % PROMOTE_WARPS;
-  int tm, tn;
-  band_tile(p.full_units + tail, p.tiles_m, p.tiles_n, &tm, &tn);
-  const int row0 = tm * PM + rank * CM + (w & 3) * 32, col0 = tn * PN + (w >> 2) * 128;
-  if (row0 >= p.M || col0 >= p.N) return;
-  const float4* base = reinterpret_cast<const float4*>(p.ws) +
-                       (int64_t)tail * p.parts * (PART_FLOATS / 4) + piece * 32 * 32;
+  for (int at_piece = (int)blockIdx.x; at_piece < p.join_pieces; at_piece += (int)gridDim.x) {
+    const int tail = at_piece / (2 * PROMOTE_WARPS), piece = at_piece % (2 * PROMOTE_WARPS);
+    const int rank = piece / PROMOTE_WARPS, w = piece % PROMOTE_WARPS;
+    int tm, tn;
+    band_tile(p.full_units + tail, p.tiles_m, p.tiles_n, &tm, &tn);
+    const int row0 = tm * PM + rank * CM + (w & 3) * 32, col0 = tn * PN + (w >> 2) * 128;
+    if (row0 >= p.M || col0 >= p.N) continue;      // the same in the whole CTA
+    const float4* base = reinterpret_cast<const float4*>(p.ws) +
+                         (int64_t)tail * p.parts * (PART_FLOATS / 4) + piece * 32 * 32;
 #pragma unroll
-  for (int u = 0; u < 1024 / JOIN_THREADS; ++u) {
-    const int at = (int)threadIdx.x + u * JOIN_THREADS, j = at >> 5, lane = at & 31;
-    float4 v[MAX_PARTS];
+    for (int u = 0; u < 1024 / JOIN_THREADS; ++u) {
+      const int at = (int)threadIdx.x + u * JOIN_THREADS, j = at >> 5, lane = at & 31;
+      float4 v[MAX_PARTS];
 #pragma unroll
-    for (int i = 0; i < MAX_PARTS; ++i)
-      if (i < p.parts) v[i] = __ldcg(base + i * (PART_FLOATS / 4) + at);
-    float4 sum = v[0];
+      for (int i = 0; i < MAX_PARTS; ++i)
+        if (i < p.parts) v[i] = __ldcg(base + i * (PART_FLOATS / 4) + at);
+      float4 sum = v[0];
 #pragma unroll
-    for (int i = 1; i < MAX_PARTS; ++i) {
-      if (i < p.parts) {
-        sum.x += v[i].x;
-        sum.y += v[i].y;
-        sum.z += v[i].z;
-        sum.w += v[i].w;
+      for (int i = 1; i < MAX_PARTS; ++i) {
+        if (i < p.parts) {
+          sum.x += v[i].x;
+          sum.y += v[i].y;
+          sum.z += v[i].z;
+          sum.w += v[i].w;
+        }
+      }
+      if constexpr (COLS) {      // two columns of two rows (see promote_role)
+        const int r = (lane >> 2) + 16 * (j & 1), c = 8 * (j >> 1) + 2 * (lane & 3);
+        *reinterpret_cast<float2*>(&x[r][c]) = make_float2(sum.x, sum.y);
+        *reinterpret_cast<float2*>(&x[r + 8][c]) = make_float2(sum.z, sum.w);
+      } else {
+        *reinterpret_cast<float4*>(&x[lane][4 * j]) = sum;
       }
     }
-    if constexpr (COLS) {      // two columns of two rows (see promote_role)
-      const int r = (lane >> 2) + 16 * (j & 1), c = 8 * (j >> 1) + 2 * (lane & 3);
-      *reinterpret_cast<float2*>(&x[r][c]) = make_float2(sum.x, sum.y);
-      *reinterpret_cast<float2*>(&x[r + 8][c]) = make_float2(sum.z, sum.w);
-    } else {
-      *reinterpret_cast<float4*>(&x[lane][4 * j]) = sum;
-    }
+    __syncthreads();
+    if (p.type == GEMM_F8_F16) store_joined<__half>(p, x, row0, col0);
+    else if (p.type == GEMM_F8_BF16) store_joined<__nv_bfloat16>(p, x, row0, col0);
+    else store_joined<float>(p, x, row0, col0);
+    __syncthreads();      // x is free again
   }
-  __syncthreads();
-  if (p.type == GEMM_F8_F16) store_joined<__half>(p, x, row0, col0);
-  else if (p.type == GEMM_F8_BF16) store_joined<__nv_bfloat16>(p, x, row0, col0);
-  else store_joined<float>(p, x, row0, col0);
 }
 
 }  // namespace large

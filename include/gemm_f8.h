@@ -135,7 +135,8 @@ enum {
  *               order, so that a call's result is the same bits every time.
  * Returns GEMM_F16_OK, GEMM_F16_ERR_INVALID_ARG, GEMM_F16_ERR_MISALIGNED,
  * GEMM_F16_ERR_SCRATCH_TOO_SMALL (the workspace) or GEMM_F16_ERR_CUDA.
- * GEMM_F16_OPT_TIMEOUT_NS, _SM_LIMIT and _KERNEL_TIMING apply;
+ * GEMM_F16_OPT_TIMEOUT_NS, _SM_LIMIT (both launches of a product with cut tiles;
+ * no other call of this header) and _KERNEL_TIMING apply;
  * GEMM_F16_OPT_FAULT_UNIT names the unit whose first copy is left out.
  */
 int gemm_f8_run(gemm_f16_plan_t plan, int form, int M, int N, int K, int experts,
@@ -146,6 +147,14 @@ int gemm_f8_run(gemm_f16_plan_t plan, int form, int M, int N, int K, int experts
  * too); a call with other sizes needs its own. */
 size_t gemm_f8_workspace(gemm_f16_plan_t plan, int form, int M, int N, int K, int experts,
                          int a_transposed);
+/* What a call of these sizes launches, on the host and for given facts: SMs,
+ * co-resident CTA pairs, GEMM_F16_OPT_SM_LIMIT (0: none).  info[0]: 1 the kernel
+ * for few rows, 2 that for many; info[1]: CTAs that share a tile's inner range
+ * (1), or parts of a cut tile (2; 1: none is cut); info[2]: CTAs of the product;
+ * info[3]: CTAs of the kernel that joins cut tiles (0: there is none).  Returns
+ * GEMM_F16_OK or GEMM_F16_ERR_INVALID_ARG. */
+int gemm_f8_run_choice(int form, int M, int N, int K, int experts, int a_transposed, int num_sms,
+                       int max_pairs, int sm_limit, int info[4]);
 int gemm_f8_validate(int form, int M, int N, int K, int experts, const int32_t *starts,
                      const gemm_f8_operand *A, const gemm_f8_operand *B, const void *C,
                      int64_t ldc, int64_t c_batch, int type, int accumulate);

@@ -135,3 +135,34 @@ def test_a_tangent_of_a_gradient_is_refused(g, plan):
         with fwd.dual_level(), pytest.raises(RuntimeError, match="forward-mode"):
             dy = fwd.make_dual(torch.ones_like(y), torch.ones_like(y))
             torch.autograd.grad(y, leaf, dy, retain_graph=True)
+
+
+# ------------------------------------------------------------------ few SMs
+
+@pytest.mark.parametrize("limit", [1, 2, 3, 24])
+def test_cut_tiles_and_shared_tiles_on_a_few_sms(g, limit):
+    """Joined by fewer CTAs than there are pieces; experts' rows by one CTA an SM."""
+    with g.Plan(0) as p:
+        p.set_option(g.OPT_SM_LIMIT, limit)
+        for m, n, k, kind in ((300, 700, 4100, "forward"), (300, 700, 4100, "weights"),
+                              (5, 700, 4100, "forward")):
+            A, B = operands(g, p, 71, m, n, k, kind)
+            c = [g.matmul_f8(p, A, B, dtype=F32) for _ in range(2)]
+            ref.check_product(c[0], ref.values(A), ref.values(B))
+            assert torch.equal(*c)
+        A = g.quantize(p, rand(1, 90, 400))
+        B = g.quantize(p, rand(2, 3, 400, 300), "tiles")
+        c = g.matmul_f8(p, A, B, dtype=F32, starts=i32(0, 40, 41, 90))
+        for e, (lo, hi) in enumerate(((0, 40), (40, 41), (41, 90))):
+            ref.check_product(c[lo:hi], ref.values(A)[lo:hi], ref.values(B)[e])
+        assert p.status() == g.OK
+
+
+def test_a_plan_launches_what_the_host_says(g, plan):
+    """The choice for the device's own facts, and the workspace that goes with it."""
+    for m, n, k in ((300, 700, 4100), (5, 700, 4100), (1000, 1024, 8192)):
+        c = g.gemm_f8_run_choice(g.F8_DENSE, m, n, k, num_sms=plan.get_option(g.INFO_NUM_SMS))
+        bytes_ = g.gemm_f8_workspace(plan.handle, g.F8_DENSE, m, n, k)
+        assert (bytes_ > 0) == (c["join_ctas"] > 0)
+        if bytes_:
+            assert bytes_ == c["join_ctas"] // 16 * c["parts"] * 256 * 256 * 4

@@ -82,3 +82,42 @@ def test_forward_mode_derivatives_are_refused(torch, which, grad):
             calls[which]()
         with fwd._set_fwd_grad_enabled(False), pytest.raises(ValueError, match="plan's device"):
             calls[which]()       # switched off: the next refusal
+
+
+# ------------------------------------------------------------------ launches
+
+SIZES = [(g.F8_DENSE, 1, 4096, 4096, 1), (g.F8_DENSE, 7, 100, 8192, 1), (g.F8_DENSE, 64, 12288, 4096, 1),
+         (g.F8_DENSE, 129, 4096, 4096, 1), (g.F8_DENSE, 1000, 1024, 8192, 1),
+         (g.F8_DENSE, 8192, 8192, 4096, 1), (g.F8_BY_ROWS, 96, 4096, 2048, 16),
+         (g.F8_BY_ROWS, 16384, 4096, 2048, 16), (g.F8_BY_INNER, 2048, 2048, 4096, 8)]
+
+
+@pytest.mark.parametrize("limit", [1, 2, 3, 7, 16, 40, 152])
+@pytest.mark.parametrize("form,m,n,k,experts", SIZES)
+def test_a_limit_of_sms_bounds_every_launch(form, m, n, k, experts, limit):
+    """A CTA may have an SM of its own: there are no more of them than SMs, but
+    for one cluster of two where a single SM is allowed."""
+    kernel, parts, product, join = g.gemm_f8_run_choice(form, m, n, k, experts, sm_limit=limit).values()
+    assert 1 <= product <= max(limit, 2 if kernel == 2 else 1)
+    assert 0 <= join <= limit
+    assert product % (parts if kernel == 1 else 2) == 0
+
+
+@pytest.mark.parametrize("size,want", [
+    ((g.F8_DENSE, 1, 4096, 4096), (1, 8, 256, 0)), ((g.F8_DENSE, 64, 12288, 4096), (1, 2, 192, 0)),
+    ((g.F8_DENSE, 65, 4096, 4096), (2, 4, 128, 256)), ((g.F8_DENSE, 1000, 1024, 2048), (2, 1, 32, 0)),
+    ((g.F8_DENSE, 8192, 8192, 4096), (2, 2, 152, 576)), ((g.F8_BY_ROWS, 96, 4096, 2048, 16), (1, 1, 304, 0)),
+    ((g.F8_BY_ROWS, 16384, 4096, 2048, 16), (2, 1, 152, 0)),
+    ((g.F8_BY_INNER, 100, 100, 4096, 8), (2, 1, 16, 0)), ((g.F8_DENSE, 40, 512, 512, 1, 1), (2, 1, 4, 0))])
+def test_launches_without_a_limit(size, want):
+    """On 152 SMs with 76 pairs of CTAs."""
+    assert tuple(g.gemm_f8_run_choice(*size).values()) == want
+
+
+@pytest.mark.parametrize("change", [dict(form=3), dict(M=0), dict(N=-1), dict(K=0), dict(num_sms=0),
+                                    dict(max_pairs=0), dict(sm_limit=-1),
+                                    dict(form=g.F8_BY_ROWS, experts=0),
+                                    dict(form=g.F8_BY_INNER, experts=1025), dict(M=2 ** 31 - 1)])
+def test_launches_of_bad_sizes_are_refused(change):
+    with pytest.raises(g.GemmError):
+        g.gemm_f8_run_choice(**{**dict(form=0, M=1, N=1, K=1), **change})
