@@ -202,6 +202,8 @@ Tensor matmul_f8(int64_t plan, int device, const Tensor& a, const Tensor& sa, co
                     M > 1 ? c.stride(-2) : N, c.dim() == 3 ? c.stride(0) : 0, type, accumulate,
                     bytes > 0 ? ws.data_ptr() : nullptr, bytes, on.raw()),
         "gemm_f8_run");
+  // A graph that has saved C must not use it as it is now.
+  if (out_ && !c.is_inference()) c.unsafeGetTensorImpl()->bump_version();
   return c;
 }
 

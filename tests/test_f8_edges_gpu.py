@@ -166,3 +166,18 @@ def test_a_plan_launches_what_the_host_says(g, plan):
         assert (bytes_ > 0) == (c["join_ctas"] > 0)
         if bytes_:
             assert bytes_ == c["join_ctas"] // 16 * c["parts"] * 256 * 256 * 4
+
+
+# ------------------------------------------------------------------ a given C
+
+def test_a_given_result_that_a_graph_has_saved_is_noticed(g, plan):
+    A, B = operands(g, plan, 5, 20, 64, 128)
+    c, w = torch.randn(20, 64, device="cuda"), torch.randn(20, 64, device="cuda", requires_grad=True)
+    y = (w * c).sum()
+    g.matmul_f8(plan, A, B, c, accumulate=True)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    with torch.inference_mode():
+        d = torch.zeros(20, 64, device="cuda")
+    g.matmul_f8(plan, A, B, d)
+    assert torch.equal(d, g.matmul_f8(plan, A, B, dtype=F32))
