@@ -185,6 +185,9 @@ Tensor matmul_f8(int64_t plan, int device, const Tensor& a, const Tensor& sa, co
                            ? c.dim() == 3 && c.size(0) == experts && c.size(1) == M && c.size(2) == N
                            : c.dim() == 2 && c.size(0) == M && c.size(1) == N;
     if (!shape || (N > 1 && c.stride(-1) != 1)) refuse("C must be row-major and of the product's shape");
+    // An expanded tensor: several experts' matrices in the same place.
+    if (c.dim() == 3 && experts > 1 && c.stride(0) == 0 && c.numel() > 0)
+      refuse("C must have a place for each expert's matrix");
   } else {
     if (accumulate) refuse("accumulate needs C");
     const auto o = a.options().dtype(dtype);

@@ -181,3 +181,17 @@ def test_a_given_result_that_a_graph_has_saved_is_noticed(g, plan):
         d = torch.zeros(20, 64, device="cuda")
     g.matmul_f8(plan, A, B, d)
     assert torch.equal(d, g.matmul_f8(plan, A, B, dtype=F32))
+
+
+def test_a_result_whose_matrices_share_their_place_is_refused(g, plan):
+    A, B = operands(g, plan, 6, 40, 64, 256, "weights")
+    one = torch.full((1, 40, 64), 7.0, device="cuda")
+    with pytest.raises(ValueError, match="place for each"):
+        g.matmul_f8(plan, A, B, one.expand(2, 40, 64), starts=i32(0, 128, 256))
+    g.matmul_f8(plan, A, B, one, starts=i32(0, 256))
+    assert torch.equal(one[0], g.matmul_f8(plan, A, B, dtype=F32))
+    beside = torch.full((40, 2, 64), 7.0, device="cuda").transpose(0, 1)     # rows in turn
+    g.matmul_f8(plan, A, B, beside, starts=i32(0, 128, 256))
+    for e in range(2):
+        r = slice(128 * e, 128 * e + 128)
+        ref.check_product(beside[e], ref.values(A, "rows")[:, r], ref.values(B, "columns")[r])
