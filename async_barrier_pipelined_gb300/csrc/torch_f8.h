@@ -425,6 +425,15 @@ struct Linear : torch::autograd::Function<Linear> {
     {
       at::AutoGradMode off(false);
       const Tensor dy = dense(grads[0]);
+      if (dy.size(1) == 0) {     // W has no rows: there is nothing to quantise
+        if (want_x) out[0] = at::zeros({dy.size(0), wq.size(-1)}, dy.options().dtype(type("x")));
+        if (want_w) {
+          std::vector<int64_t> shape = {0, xq.size(1)};
+          if (starts) shape.insert(shape.begin(), starts->size(0) - 1);
+          out[1] = at::zeros(shape, dy.options().dtype(type("w")));
+        }
+        return once(std::move(out));
+      }
       const Quantized g =
           quantize(h, plan->device, dy,
                    want_x && want_w ? GEMM_F8_BOTH : want_x ? GEMM_F8_ROWS : GEMM_F8_COLUMNS,

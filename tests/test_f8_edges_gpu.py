@@ -195,3 +195,21 @@ def test_a_result_whose_matrices_share_their_place_is_refused(g, plan):
     for e in range(2):
         r = slice(128 * e, 128 * e + 128)
         ref.check_product(beside[e], ref.values(A, "rows")[:, r], ref.values(B, "columns")[r])
+
+
+@pytest.mark.parametrize("experts", [0, 3])
+def test_weights_without_rows(g, plan, experts):
+    """A result of no columns: X's gradient is 0."""
+    x = torch.randn(10, 72, device="cuda").to(BF16).requires_grad_()
+    w = torch.zeros((experts, 0, 72) if experts else (0, 72), device="cuda", requires_grad=True)
+    m = g.expert_maps(plan, torch.arange(5, device="cuda")[:, None] % 3, 3, align=128) if experts else None
+    if experts:
+        x = torch.randn(m.source.numel(), 72, device="cuda").to(BF16).requires_grad_()
+    y = g.linear_f8(plan, x, w, starts=m)
+    assert y.shape == (x.shape[0], 0) and y.dtype == BF16
+    dx, dw = torch.autograd.grad(y, (x, w), torch.zeros_like(y))
+    assert dx.shape == x.shape and dx.dtype == BF16 and (dx == 0).all()
+    assert dw.shape == w.shape and dw.dtype == w.dtype
+    dx, = torch.autograd.grad(g.linear_f8(plan, x, w.detach(), starts=m).sum(), x)
+    assert (dx == 0).all()
+    assert plan.status() == g.OK
