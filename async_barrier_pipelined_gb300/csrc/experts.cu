@@ -184,7 +184,7 @@ struct alignas(V * sizeof(T)) Vec {
 template <typename T, int V>
 __device__ __forceinline__ Vec<T, V> load(const T* at) {
   Vec<T, V> x;
-  if constexpr (V > 1) *reinterpret_cast<uint4*>(x.v) = __ldg(reinterpret_cast<const uint4*>(at));
+  if constexpr (V > 1) *reinterpret_cast<uint4*>(x.v) = *reinterpret_cast<const uint4*>(at);
   else x.v[0] = *at;
   return x;
 }
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(ROW_THREADS) experts_gather_kernel(const RowPa
   for (int64_t at = (int64_t)blockIdx.x * ROW_WARPS + (threadIdx.x >> 5); at < work; at += step) {
     const int64_t r = at / pieces;
     const int u0 = (int)(at - r * pieces) * 32 * GATHER_STEPS + lane;
-    const int s = __ldg(p.source + r);
+    const int s = p.source[r];
     const bool real = s >= 0 && s / p.choices < p.x_rows;
     if (!real && s != -1) report(p);
     const T* x = static_cast<const T*>(p.X) + (real ? (int64_t)(s / p.choices) * p.ldx : 0);
@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(ROW_THREADS) experts_combine_kernel(const RowP
 #pragma unroll
       for (int j = 0; j < AT_ONCE; ++j) {
         const int64_t n = t * p.choices + j0 + j;
-        r[j] = j0 + j < p.choices ? __ldg(p.map + n) : -1;
+        r[j] = j0 + j < p.choices ? p.map[n] : -1;
         w[j] = p.w && j0 + j < p.choices ? to_float<W>(static_cast<const W*>(p.w)[n]) : 1.f;
       }
 #pragma unroll
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(ROW_THREADS) experts_combine_gradient_kernel(c
   const int lane = threadIdx.x & 31, units = p.cols / V;
   const int64_t step = (int64_t)gridDim.x * ROW_WARPS;
   for (int64_t r = (int64_t)blockIdx.x * ROW_WARPS + (threadIdx.x >> 5); r < p.rows; r += step) {
-    const int s = __ldg(p.source + r);
+    const int s = p.source[r];
     const bool real = s >= 0 && s < p.entries;
     if (!real && s != -1) report(p);
     T* ds = static_cast<T*>(p.Y) + r * p.ldy;
@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(ROW_THREADS) experts_combine_gradient_kernel(c
   if (p.dw)   // choices that have no row
     for (int64_t i = (int64_t)blockIdx.x * ROW_THREADS + threadIdx.x; i < p.entries;
          i += (int64_t)gridDim.x * ROW_THREADS)
-      if (__ldg(p.map + i) < 0) static_cast<W*>(p.dw)[i] = from_float<W>(0.f);
+      if (p.map[i] < 0) static_cast<W*>(p.dw)[i] = from_float<W>(0.f);
 }
 
 using RowKernel = void (*)(const RowParams);

@@ -7,6 +7,11 @@
 // zero into tensor memory (FP32; products of 4-bit by 4-bit significands are
 // exact) and the promotion warps add it, scaled, to FP32 registers: the scales
 // change from block to block, so a tile's sum cannot stay in tensor memory.
+//
+// Loads.  Every kernel here starts beside the end of the one before it
+// (griddepcontrol) and its inputs may be written after it has started: they are
+// read by ordinary loads after the wait, never as data that stay the same while
+// the kernel runs (__ldg, ld.global.nc).
 #pragma once
 
 #include <cuda_bf16.h>

@@ -430,8 +430,8 @@ __device__ __forceinline__ void promote_role(const Params& p, const Segments& s,
     pa = p.sa + (int64_t)(row >> p.sa_shift) * p.sa_outer + (int64_t)g.blk0 * p.sa_inner;
     pb = p.sb + (int64_t)(col >> 7) * p.sb_outer + (int64_t)g.blk0 * p.sb_inner +
          (p.form == GEMM_F8_BY_ROWS ? g.expert * p.sb_batch : 0);
-    na = __ldg(pa);
-    nb = __ldg(pb);
+    na = *pa;
+    nb = *pb;
   };
   if (pair < units) begin(pair);
   for (int u = pair; u < units; u += npairs) {
@@ -447,9 +447,9 @@ __device__ __forceinline__ void promote_role(const Params& p, const Segments& s,
           got = wait_phase_inline(b.sfull + 8 * pos.stage, consumer_wait_parity(pos), p, abort_flag);
       } else if (i + 1 < nkb) {     // the next block's scales, on their way during this one
         pa += p.sa_inner;
-        na = __ldg(pa);
+        na = *pa;
         pb += p.sb_inner;
-        nb = __ldg(pb);
+        nb = *pb;
       }
       got = wait_phase_inline(b.tfull + 8 * half, (done >> 1) & 1u, p, abort_flag) && got;
       if (!__all_sync(0xffffffffu, got)) return;

@@ -109,7 +109,7 @@ __device__ __forceinline__ void load16(Pack<T>& x, const T* row, int col, int co
   if (VEC && row && col + 16 <= cols) {
 #pragma unroll
     for (int i = 0; i < 16 / V; ++i)
-      reinterpret_cast<uint4*>(out)[i] = __ldg(reinterpret_cast<const uint4*>(row + col) + i);
+      reinterpret_cast<uint4*>(out)[i] = reinterpret_cast<const uint4*>(row + col)[i];
   } else {
 #pragma unroll
     for (int i = 0; i < 16; ++i) out[i] = row && col + i < cols ? row[col + i] : T(0.f);

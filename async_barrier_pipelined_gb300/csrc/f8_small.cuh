@@ -190,9 +190,9 @@ __device__ __forceinline__ void promote_role(const Params& p, const Segments& s,
       pa[i] = p.sa + (int64_t)(min(g.m0 + (int)lane + 32 * i, g.m_end - 1) >> p.sa_shift) * p.sa_outer +
               (int64_t)kb0 * p.sa_inner;
     if (kb0 < kb1) {
-      nb = __ldg(pb);
+      nb = *pb;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) na[i] = __ldg(pa[i]);
+      for (int i = 0; i < PER; ++i) na[i] = *pa[i];
     }
     uint64_t acc[NT / 2];
 #pragma unroll
@@ -205,11 +205,11 @@ __device__ __forceinline__ void promote_role(const Params& p, const Segments& s,
         if (NT >= 32 || (int)lane < NT) st_shared_f32(abuf + (lane + 32u * c) * 4u, na[c]);
       if (i + 1 < kb1) {
         pb += p.sb_inner;
-        nb = __ldg(pb);
+        nb = *pb;
 #pragma unroll
         for (int c = 0; c < PER; ++c) {
           pa[c] += p.sa_inner;
-          na[c] = __ldg(pa[c]);
+          na[c] = *pa[c];
         }
       }
       const bool got = wait_phase(b.tfull + 8 * half, (done >> 1) & 1u, p, abort_flag);

@@ -213,3 +213,25 @@ def test_weights_without_rows(g, plan, experts):
     dx, = torch.autograd.grad(g.linear_f8(plan, x, w.detach(), starts=m).sum(), x)
     assert (dx == 0).all()
     assert plan.status() == g.OK
+
+
+# ------------------------------------------------------------------ launches that overlap
+
+def test_a_chain_of_calls_through_the_same_buffers(g, plan):
+    """Quantisation, product, quantisation into the same codes and scales, product,
+    ..., nothing between: each launch starts beside the end of the one before."""
+    s = torch.cuda.current_stream().cuda_stream
+    m, k, n = 16, 4096, 2048
+    W = g.quantize(plan, torch.randn(n, k, generator=gen(1), device="cuda"), "tiles").t()
+    xs = [torch.randn(m, k, generator=gen(2 + i), device="cuda") * 10 ** i for i in range(4)]
+    want = [g.matmul_f8(plan, g.quantize(plan, x), W, dtype=F32) for x in xs]
+    q, outs = g.quantize(plan, xs[0]), [torch.empty(m, n, device="cuda") for _ in xs]
+    torch.cuda.synchronize()
+    for _ in range(50):
+        for x, c in zip(xs, outs):
+            g.gemm_f8_quantize(plan.handle, g.F8_ROWS, g.F8_E4M3, 2, 1, m, k, x.data_ptr(), k, 0, 0, 1,
+                               0, q.data.data_ptr(), k, 0, q.scales.data_ptr(), stream=s)
+            g.matmul_f8(plan, q, W, c)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    assert plan.status() == g.OK

@@ -2,6 +2,7 @@
 wrongly, on the host.  Nothing is computed here."""
 from __future__ import annotations
 
+import re
 import types
 
 import pytest
@@ -121,3 +122,17 @@ def test_launches_without_a_limit(size, want):
 def test_launches_of_bad_sizes_are_refused(change):
     with pytest.raises(g.GemmError):
         g.gemm_f8_run_choice(**{**dict(form=0, M=1, N=1, K=1), **change})
+
+
+# ------------------------------------------------------------------ sources
+
+def test_kernels_that_start_early_read_their_inputs_by_ordinary_loads():
+    """A read-only load is for memory that nothing writes while the kernel runs.
+    These kernels start before the one that writes their inputs has ended."""
+    import glob
+    import os
+    found = []
+    for path in glob.glob(os.path.join(gbuild.CSRC, "f8*")) + [os.path.join(gbuild.CSRC, "experts.cu")]:
+        text = re.sub(r"//[^\n]*", "", open(path).read())
+        found += [(os.path.basename(path), w) for w in ("__ldg", "global.nc", "__restrict__") if w in text]
+    assert not found
