@@ -235,3 +235,98 @@ def test_a_chain_of_calls_through_the_same_buffers(g, plan):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(outs, want))
     assert plan.status() == g.OK
+
+
+# ------------------------------------------------------------------ the largest sizes
+
+def test_matrices_of_more_numbers_than_32_bits_count(g, plan):
+    """The last rows of 262,149 by 8200 numbers, of codes and of results."""
+    rows, cols = 2 ** 18 + 5, 8200
+    end = slice(rows - 300, rows)
+    x = torch.zeros(rows, cols, dtype=F16, device="cuda")
+    x[end] = torch.randn(300, cols, generator=gen(1), device="cuda").half()
+    for blocks in ("rows", "both"):
+        q = g.quantize(plan, x, blocks)
+        q = q[0] if blocks == "both" else q
+        codes, scales = ref.quantize(x[end], "rows", E4)
+        assert torch.equal(q.data[end].view(torch.uint8), codes.view(torch.uint8))
+        assert torch.equal(q.scales[end], scales)
+    at = (rows - 300) // 128 * 128
+    for b, kind in ((g.quantize(plan, x, "tiles"), "tiles"), (g.quantize(plan, x, "columns"), "columns")):
+        codes, scales = ref.quantize(x[at:], kind, E4)
+        assert torch.equal(b.data[at:].view(torch.uint8), codes.view(torch.uint8))
+        assert torch.equal(b.scales[at // 128:], scales)
+    del b, codes, scales
+    # a result as large, dense and by experts' rows
+    A = g.quantize(plan, torch.randn(rows, 130, generator=gen(2), device="cuda").half())
+    B = g.quantize(plan, torch.randn(2, 130, cols, generator=gen(3), device="cuda"), "tiles")
+    a, b = ref.values(g.Blocks(A.data[end], A.scales[end])), ref.values(B)
+    c = g.matmul_f8(plan, A, g.Blocks(B.data[0], B.scales[0]), x)
+    ref.check_product(c[end], a, b[0])
+    x.zero_()
+    c = g.matmul_f8(plan, A, B, x, starts=i32(0, rows - 200, rows))
+    ref.check_product(c[end][:100], a[:100], b[0])
+    ref.check_product(c[end][100:], a[100:], b[1])
+    # rows there and back
+    picks = torch.arange(rows, device="cuda").int()[:, None] % 2
+    m = g.expert_maps(plan, picks, 2)
+    s = g.expert_gather(plan, x, m)
+    assert torch.equal(s[end], x[m.source[end].long()])
+    assert torch.equal(g.expert_combine(plan, s, m)[end], x[end])
+    assert plan.status() == g.OK
+
+
+@pytest.mark.parametrize("m", [3000, 200000])
+def test_as_many_experts_as_there_may_be(g, plan, m):
+    """1024 experts, half of them without rows."""
+    e = torch.arange(1024, device="cuda")
+    lengths = torch.where(e % 2 == 0, 0, m // 512 - (e % 3))
+    starts = torch.cat((torch.zeros(1, device="cuda"), lengths.cumsum(0))).int()
+    A = g.quantize(plan, torch.randn(m, 130, generator=gen(1), device="cuda"))
+    B = g.quantize(plan, torch.randn(1024, 130, 72, generator=gen(2), device="cuda"), "tiles")
+    c = g.matmul_f8(plan, A, B, dtype=F32, starts=starts)
+    at = starts.tolist()
+    a, b = ref.values(A), ref.values(B)
+    for i in list(range(0, 1024, 97)) + [1022, 1023]:
+        ref.check_product(c[at[i]:at[i + 1]], a[at[i]:at[i + 1]], b[i])
+    assert (c[at[-1]:] == 0).all()
+    inner = torch.cat((torch.zeros(1, device="cuda"), torch.where(e % 2 == 0, 0, 128).cumsum(0))).int()
+    k = 512 * 128
+    A = g.quantize(plan, torch.randn(k, 40, generator=gen(3), device="cuda"), "columns").t()
+    B = g.quantize(plan, torch.randn(k, 72, generator=gen(4), device="cuda"), "columns")
+    c = g.matmul_f8(plan, A, B, dtype=F32, starts=inner)
+    a, b = ref.values(A, "rows"), ref.values(B, "columns")
+    for i in (0, 1, 2, 511, 777, 1023):
+        r = slice(inner[i].item(), inner[i + 1].item())
+        ref.check_product(c[i], a[:, r], b[r])
+    assert plan.status() == g.OK
+
+
+def test_one_kernel_time_for_each_product(g):
+    """The product's, without the join of cut tiles."""
+    with g.Plan(0) as p:
+        calls = [operands(g, p, 7, m, n, k) for m, n, k in ((5, 300, 1000), (300, 700, 4100), (300, 700, 400))]
+        p.set_option(g.OPT_KERNEL_TIMING, 1)
+        for A, B in calls:
+            g.matmul_f8(p, A, B)
+            ms, count = p.kernel_time()
+            assert count == 1 and 0 < ms < 1000
+
+
+@pytest.mark.parametrize("m", [65, 300])
+def test_linear_of_transposed_views_has_the_same_bits(g, plan, m):
+    """Above 64 rows the same kernel takes X and W either way."""
+    x = torch.randn(m, 200, generator=gen(21), device="cuda").to(BF16)
+    w = torch.randn(130, 200, generator=gen(22), device="cuda").to(BF16)
+    dy = torch.randn(m, 130, generator=gen(23), device="cuda").to(BF16)
+
+    def run(x, w):
+        x, w = x.detach().requires_grad_(), w.detach().requires_grad_()
+        y = g.linear_f8(plan, x, w)
+        return (y, *torch.autograd.grad(y, (x, w), dy))
+
+    want = run(x, w)
+    turned = lambda t: t.t().contiguous().t()
+    for a, b in ((turned(x), w), (x, turned(w)), (turned(x), turned(w))):
+        for c, d in zip(run(a, b), want):
+            assert torch.equal(c, d)
