@@ -57,7 +57,10 @@ Choice choose(const gemm_f16_plan_s* p, int form, int M, int N, int K, int exper
   c.parts = 1;
   const int kblocks = (int)ceil_div(K, f8::BLOCK);
   // Rows of a tile of the small kernel: those of the call, or of an expert on
-  // the average.  Up to 64 of them: 64 x 4096 x 4096 takes 13.2 us there and 14.1
+  // the average if all of M, the room, is filled.  (How many rows there are is
+  // known on the device alone: maps that fill experts up to a multiple of 128 come
+  // here with 128 rows an expert, however few of them are tokens'.)  Up to 64 of
+  // them: 64 x 4096 x 4096 takes 12.8 us there and 14.1
   // in the large kernel, 64 experts of 64 rows (1024 x 2048) 40.6 and 44.1; with a
   // tile of 128 rows 128 x 4096 x 4096 took 18.8 and 16 experts of 96 rows (4096 x
   // 2048) 102, in the large kernel 16.4 and 43.

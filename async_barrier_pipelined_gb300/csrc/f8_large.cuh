@@ -12,9 +12,10 @@
 // 256 x 128 products at 8192 a cycle), its four FP32 pipes 256 for one fused
 // multiply-add per product (scales per tile of B: sa * sb is one number for a
 // thread's 128 columns) or 512 for two operations (a scale per column of B).
-// Measured at 4864 x 4096 x 8192: 405 ns a block with a scale per tile (2.8
-// PFLOP/s), 650 with one per column (1.8), 350 for the copies and the tensor
-// core alone.  MMAs of 128 columns, which would give tensor memory four slots
+// Measured at 4864 x 4096 x 8192: 405 ns a block with a scale per tile (3.1
+// PFLOP/s while blocks follow one another), 650 with one per column (2.0), 350
+// (3.6) for the copies and the tensor core alone; the start and the end of a tile
+// come on top, about 3 us.  MMAs of 128 columns, which would give tensor memory four slots
 // and the promotion warps more time for each, took 600.
 //
 // DENSE: pairs walk the tiles in bands of eight tile rows.  The `rem` tiles of

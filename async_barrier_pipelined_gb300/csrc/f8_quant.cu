@@ -15,8 +15,11 @@
 // 8 KB of shared memory, and writes the codes of one or both directions from the
 // same registers, so that X is read once.  Maxima are taken of pairs in the
 // numbers' own type, divisions spread over the lanes.  Tiles take 43 us (4.6
-// TB/s), columns 54 and both directions 73 (3.6 TB/s), bound by their 16 to 22
-// instructions a number and the two barriers.  Tried: four columns of eight rows
+// TB/s), columns 54 and both directions 73 (3.6 TB/s).  What bounds them is too
+// little overlap: at 64 registers two CTAs of 512 threads an SM load, wait at two
+// barriers and store in turn, and neither the memory (38 % of its time in both
+// directions) nor the issue slots (51 %) are busy; the bf16 form of both
+// directions also spills a few registers.  Tried: four columns of eight rows
 // a lane (stores of four bytes; tiles 55, both 73), CTAs that stay and fetch the
 // next tile early (82), two FP32 products at once (the pairs' moves cost more).
 

@@ -14,7 +14,9 @@
  * rounding to C's type.  A block's inner sum is multiplied with one scale and
  * then the other (or, where that is a normal FP32 number, with their product):
  * where the first of these is below 2^-126, digits are lost that a large second
- * scale would have shown.  The last block of a dimension may be shorter.
+ * scale would have shown, and where it passes FP32's largest number (a scale
+ * above 2^89) the result is infinite even if a small second scale would have
+ * brought it back.  The last block of a dimension may be shorter.
  *
  * Conventions are those of gemm_f16.h: device pointers on the plan's device,
  * leading dimensions in elements, GEMM_F16_* codes (on an error nothing has
@@ -136,7 +138,8 @@ enum {
  * Returns GEMM_F16_OK, GEMM_F16_ERR_INVALID_ARG, GEMM_F16_ERR_MISALIGNED,
  * GEMM_F16_ERR_SCRATCH_TOO_SMALL (the workspace) or GEMM_F16_ERR_CUDA.
  * GEMM_F16_OPT_TIMEOUT_NS, _SM_LIMIT (both launches of a product with cut tiles;
- * no other call of this header) and _KERNEL_TIMING apply;
+ * no other call of this header) and _KERNEL_TIMING (the product's kernel, not the
+ * join of cut tiles, which takes up to 7 us) apply;
  * GEMM_F16_OPT_FAULT_UNIT names the unit whose first copy is left out.
  */
 int gemm_f8_run(gemm_f16_plan_t plan, int form, int M, int N, int K, int experts,
